@@ -26,6 +26,8 @@ __all__ = ["lib", "verify_stochastic", "verify_greedy", "logits_process", "works
            "tree_branches", "outcome_lookup", "logits_apply", "verify_greedy_lmhead",
            "status_string", "SpecError", "verify_stochastic_path", "device_cu_count",
            "verify_stochastic_noalloc", "NOALLOC_SCRATCH_BYTES",
+           "CACHE4_PAGE", "cache4_record_bytes", "cache4_alloc", "cache4_write", "cache4_read",
+           "attention_cache4", "tree_mask", "quantize_fp8", "lmhead_fp8",
            "library_path"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -55,6 +57,19 @@ class spec_processors_t(ctypes.Structure):
                 ("allow_pos_stride", ctypes.c_int64), ("penalize", ctypes.c_void_p),
                 ("pen_seq_stride", ctypes.c_int64), ("pen_pos_stride", ctypes.c_int64),
                 ("theta", ctypes.c_float)]
+
+
+class spec_cache4_t(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("n_pages", ctypes.c_int32),
+                ("table_cols", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class spec_heads_t(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("seq_stride", ctypes.c_int64),
+                ("pos_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class SpecError(RuntimeError):
@@ -121,6 +136,24 @@ def lib():
             L.spec_verify_stochastic_path.restype = ctypes.c_int
             L.spec_device_cu_count.argtypes = [vp]
             L.spec_device_cu_count.restype = ctypes.c_int
+            L.spec_cache4_record_bytes.argtypes = [i32]
+            L.spec_cache4_record_bytes.restype = sz
+            for f in (L.spec_cache4_write, L.spec_cache4_read):
+                f.argtypes = [spec_cache4_t, spec_heads_t, spec_heads_t, i32, i32, vp, vp, vp]
+                f.restype = ctypes.c_int
+            L.spec_attention_cache4_workspace.argtypes = [i32] * 5
+            L.spec_attention_cache4_workspace.restype = sz
+            L.spec_attention_cache4.argtypes = [spec_cache4_t, spec_heads_t, i32, i32, i32, vp, vp,
+                                                vp, i64, i64, ctypes.c_float, spec_heads_t, vp, vp,
+                                                sz, vp]
+            L.spec_attention_cache4.restype = ctypes.c_int
+            L.spec_quantize_fp8.argtypes = [vp, i32, i64, i32, i32, vp, vp, vp]
+            L.spec_quantize_fp8.restype = ctypes.c_int
+            L.spec_lmhead_fp8_workspace.argtypes = [i32, i32, i32]
+            L.spec_lmhead_fp8_workspace.restype = sz
+            L.spec_lmhead_fp8.argtypes = [spec_logits_t, i32, i32, i32, vp, i64, vp, i32,
+                                          spec_logits_t, vp, sz, vp]
+            L.spec_lmhead_fp8.restype = ctypes.c_int
             L.spec_status_string.argtypes = [ctypes.c_int]
             L.spec_status_string.restype = ctypes.c_char_p
             _lib = L
@@ -621,3 +654,292 @@ def verify_greedy_lmhead(hidden: torch.Tensor, weight: torch.Tensor, draft_token
                                          ws.numel() * ws.element_size(), _stream(stream, dev))
     _check(rc, "spec_verify_greedy_lmhead")
     return acc, toks
+
+
+# ---------------------------------------------------------------------------
+# The target's pass over the candidates in few bits (specverify_lowbit.h): a
+# key/value cache in 4 bits, written, read back and attended to, and the LM
+# head in 8-bit floating point.
+#
+# These calls take every tensor in its final type and place (nothing is
+# converted or copied), make their outputs on the call's stream, and take
+# scratch from torch's allocator on that stream unless `workspace` gives some:
+# it is theirs alone, also inside a captured graph, whose pool then owns it.
+
+CACHE4_PAGE = 64
+
+
+class _on:
+    """The tensors' device and the call's stream as torch's current ones."""
+
+    def __init__(self, dev, stream):
+        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
+        if self.stream.device != dev:
+            raise ValueError("the stream must belong to %s, got %s" % (dev, self.stream.device))
+        self.ctx = None
+        if stream is not None or torch.cuda.current_device() != dev.index:
+            self.ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _scratch(workspace, dev, need):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    return _workspace_arg(workspace, dev, need, None)
+
+
+def _device_tensor(t, what, dtype, dim, dev=None):
+    """`t` checked: a device tensor of the dtype(s) and dimension, on `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a tensor" % what)
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.dim() != dim:
+        raise ValueError("%s must have %d axes, got shape %s" % (what, dim, tuple(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must live in device memory" % what)
+    if dev is not None and t.device != dev:
+        raise ValueError("%s must live on %s, got %s" % (what, dev, t.device))
+    return t
+
+
+def _stride(t, axis) -> int:
+    """The axis's stride; 0 where it is never stepped along."""
+    return t.stride(axis) if t.shape[axis] > 1 else 0
+
+
+def _heads(t, what, shape=None) -> spec_heads_t:
+    """Heads of positions [B][T][heads][D], last axis contiguous."""
+    if t.stride(3) != 1:
+        raise ValueError("the last axis of %s must be contiguous" % what)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be of shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    return spec_heads_t(t.data_ptr(), _dtype_code(t), 0, *(_stride(t, i) for i in range(3)))
+
+
+def _cache4(pages, table, D, B):
+    _device_tensor(pages, "pages", torch.uint8, 3)
+    _device_tensor(table, "table", torch.int32, 2, pages.device)
+    if not pages.is_contiguous() or pages.shape[2] != 68 * D:
+        raise ValueError("pages must be contiguous [n_pages][heads][%d] for heads of %d, got %s"
+                         % (68 * D, D, tuple(pages.shape)))
+    if table.shape[0] != B or table.stride(1) != 1:
+        raise ValueError("table must be [%d][pages of a sequence] with a contiguous last axis" % B)
+    return spec_cache4_t(pages.data_ptr(), table.data_ptr(), max(table.stride(0), table.shape[1]),
+                         pages.shape[0], table.shape[1], pages.shape[1], D)
+
+
+def _per_sequence(t, what, B, dev):
+    if t is None:
+        return None
+    _device_tensor(t, what, torch.int32, 1, dev)
+    if t.shape[0] != B or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 [%d]" % (what, B))
+    return t.data_ptr()
+
+
+def cache4_record_bytes(head_dim: int) -> int:
+    """Bytes of one page's record of one kv head (0: unsupported head_dim)."""
+    return int(lib().spec_cache4_record_bytes(int(head_dim)))
+
+
+def cache4_alloc(n_pages: int, heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """An empty pool of pages [n_pages][heads][record bytes] for a 4-bit
+    cache; a page holds CACHE4_PAGE tokens."""
+    n = cache4_record_bytes(head_dim)
+    if n == 0:
+        _check(SPEC_ERR_UNSUPPORTED, "spec_cache4_record_bytes")
+    return torch.zeros((n_pages, heads, n), dtype=torch.uint8, device=device)
+
+
+def cache4_write(pages: torch.Tensor, table: torch.Tensor, start: torch.Tensor, k: torch.Tensor,
+                 v: torch.Tensor, *, count: torch.Tensor | None = None, stream=None) -> None:
+    """Quantises new keys and values k, v [B][T][heads][D] (float32 or
+    bfloat16) into the 4-bit cache, at positions start[b] .. start[b] +
+    count[b] - 1 (count None: T) of the sequences whose pages ``table`` [B][P]
+    names.  start, count and table are int32; nothing is written for an
+    ill-formed sequence or position.  After a verify call the next step's
+    start is start + accepted_len + 1 (a chain): what lies behind is
+    overwritten."""
+    _device_tensor(k, "k", (torch.float32, torch.bfloat16), 4)
+    _device_tensor(v, "v", k.dtype, 4, k.device)
+    B, T, H, D = k.shape
+    cache = _cache4(pages, table, D, B)
+    if pages.device != k.device or pages.shape[1] != H:
+        raise ValueError("pages and k disagree on device or heads")
+    s, n = (_per_sequence(t, w, B, k.device) for t, w in ((start, "start"), (count, "count")))
+    if s is None:
+        raise ValueError("start is required")
+    kd, vd = _heads(k, "k"), _heads(v, "v", k.shape)
+    with _on(k.device, stream) as st:
+        rc = lib().spec_cache4_write(cache, kd, vd, B, T, s, n, st)
+    _check(rc, "spec_cache4_write")
+
+
+def cache4_read(pages: torch.Tensor, table: torch.Tensor, start: torch.Tensor, T: int,
+                head_dim: int, *, count: torch.Tensor | None = None,
+                dtype: torch.dtype = torch.bfloat16, out=None, stream=None):
+    """Reads positions start[b] .. start[b] + count[b] - 1 of the 4-bit cache
+    back as (k, v) [B][T][heads][head_dim]; both dtypes hold the values
+    exactly.  Rows past count[b] are zero, or left as they were in
+    ``out`` = (k, v).  Ill-formed sequences and positions read as NaN."""
+    B = start.shape[0]
+    cache = _cache4(pages, table, head_dim, B)
+    dev = pages.device
+    s, n = (_per_sequence(t, w, B, dev) for t, w in ((start, "start"), (count, "count")))
+    shape = (B, int(T), pages.shape[1], head_dim)
+    with _on(dev, stream) as st:
+        if out is None:
+            make = torch.empty if count is None else torch.zeros
+            k, v = (make(shape, dtype=dtype, device=dev) for _ in range(2))
+        else:
+            k, v = out
+            _device_tensor(k, "out[0]", (torch.float32, torch.bfloat16), 4, dev)
+            _device_tensor(v, "out[1]", k.dtype, 4, dev)
+        rc = lib().spec_cache4_read(cache, _heads(k, "out[0]", shape), _heads(v, "out[1]", shape), B,
+                                    int(T), s, n, st)
+    _check(rc, "spec_cache4_read")
+    return k, v
+
+
+def tree_mask(parents) -> torch.Tensor:
+    """The attention mask of a parent-pointer candidate tree (tree_branches):
+    node i sees itself and its ancestors.  Returns int32 words
+    [1][N][ceil(N / 32)] on the CPU, bit j % 32 of word j / 32 for node j."""
+    par = [int(x) for x in (parents.tolist() if hasattr(parents, "tolist") else parents)]
+    N = len(par)
+    if N < 1 or par[0] != -1:
+        raise ValueError("a tree needs a root (parent -1)")
+    bits = [0] * N
+    for i in range(N):
+        if i and not 0 <= par[i] < i:
+            raise ValueError("node %d: parent must precede it" % i)
+        bits[i] = (bits[par[i]] if i else 0) | (1 << i)
+    words = [[(x >> (32 * w)) & 0xFFFFFFFF for w in range((N + 31) // 32)] for x in bits]
+    signed = [[w - (1 << 32) if w >> 31 else w for w in row] for row in words]
+    return torch.tensor([signed], dtype=torch.int32)
+
+
+def attention_cache4(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor,
+                     start: torch.Tensor, *, count: torch.Tensor | None = None,
+                     mask: torch.Tensor | None = None, scale: float | None = None,
+                     return_lse: bool = False, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     stream=None):
+    """Attention of new positions over a 4-bit cache that already holds their
+    own keys and values (cache4_write with the same start and count).
+    q [B][T][q_heads][D] bfloat16, q_heads a multiple of the cache's heads.
+    Token i of sequence b sees the start[b] cached tokens and, of the new
+    ones, those whose bits are set in ``mask`` int32 words
+    [B|1][T][ceil(T/32)] (tree_mask), or those up to itself (mask None).
+    scale: 1 / sqrt(D) unless given.  Returns out [B][T][q_heads][D] bfloat16
+    and, with return_lse or an ``lse`` tensor, the log of the softmax's
+    denominator [B][T][q_heads] float32.  Rows past count[b] are zero, or left
+    as they were in the caller's tensors; a token that sees nothing gets 0 and
+    -inf; ill-formed sequences get NaN."""
+    _device_tensor(q, "q", torch.bfloat16, 4)
+    B, T, Hq, D = q.shape
+    dev = q.device
+    cache = _cache4(pages, table, D, B)
+    if pages.device != dev:
+        raise ValueError("q and pages must live on one device")
+    s, n = (_per_sequence(t, w, B, dev) for t, w in ((start, "start"), (count, "count")))
+    if s is None:
+        raise ValueError("start is required")
+    mp, ms, mr = None, 0, 0
+    if mask is not None:
+        _device_tensor(mask, "mask", torch.int32, 3, dev)
+        if mask.shape[0] not in (1, B) or tuple(mask.shape[1:]) != (T, (T + 31) // 32) or \
+                mask.stride(2) != 1:
+            raise ValueError("mask must be int32 words [B|1][%d][%d] with contiguous words"
+                             % (T, (T + 31) // 32))
+        mp, ms, mr = mask.data_ptr(), _stride(mask, 0), _stride(mask, 1)
+    if lse is not None:
+        _out_tensor(lse, (B, T, Hq), torch.float32, dev, "lse")
+    need = lib().spec_attention_cache4_workspace(B, T, Hq, pages.shape[1], D)
+    if need == 0:
+        _check(SPEC_ERR_UNSUPPORTED if B and T and Hq and Hq % pages.shape[1] == 0
+               else SPEC_ERR_INVALID_ARG, "spec_attention_cache4_workspace")
+    with _on(dev, stream) as st:
+        make = torch.empty if count is None else torch.zeros
+        if out is None:
+            out = make((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
+        else:
+            _device_tensor(out, "out", torch.bfloat16, 4, dev)
+        if return_lse and lse is None:
+            lse = make((B, T, Hq), dtype=torch.float32, device=dev)
+        ws = _scratch(workspace, dev, need)
+        rc = lib().spec_attention_cache4(
+            cache, _heads(q, "q"), B, T, Hq, s, n, mp, ms, mr,
+            float(scale) if scale is not None else D ** -0.5, _heads(out, "out", q.shape),
+            lse.data_ptr() if lse is not None else None, ws.data_ptr(),
+            ws.numel() * ws.element_size(), st)
+    _check(rc, "spec_attention_cache4")
+    return (out, lse) if lse is not None else out
+
+
+def quantize_fp8(weight: torch.Tensor, *, out=None, stream=None):
+    """Weights [V][d] (float32 or bfloat16, d a multiple of 32) to 8-bit
+    floating point: returns (q [V][d] float8_e4m3fn, scale
+    [ceil(V/128)][ceil(d/128)] float32), one power-of-two scale per 128 x 128
+    block."""
+    _device_tensor(weight, "weight", (torch.float32, torch.bfloat16), 2)
+    if weight.stride(1) != 1:
+        raise ValueError("the last axis of weight must be contiguous")
+    V, d = weight.shape
+    dev = weight.device
+    blocks = ((V + 127) // 128, (d + 127) // 128)
+    with _on(dev, stream) as st:
+        if out is None:
+            q = torch.empty((V, d), dtype=torch.float8_e4m3fn, device=dev)
+            scale = torch.empty(blocks, dtype=torch.float32, device=dev)
+        else:
+            q = _out_tensor(out[0], (V, d), torch.float8_e4m3fn, dev, "out[0]")
+            scale = _out_tensor(out[1], blocks, torch.float32, dev, "out[1]")
+        rc = lib().spec_quantize_fp8(weight.data_ptr(), _dtype_code(weight), weight.stride(0), V, d,
+                                     q.data_ptr(), scale.data_ptr(), st)
+    _check(rc, "spec_quantize_fp8")
+    return q, scale
+
+
+def lmhead_fp8(hidden: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, *,
+               out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.float32,
+               workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """LM head in 8-bit floating point: logits [B][rows][V] of hidden
+    [B][rows][d] (float32 or bfloat16; rounded to e4m3 in blocks of 128 with a
+    scale each) and weight [V][d] float8_e4m3fn with weight_scale
+    [ceil(V/128)][ceil(d/128)] float32 (quantize_fp8, or a checkpoint's own).
+    The logits, float32 or bfloat16, are what the verify calls take."""
+    _device_tensor(hidden, "hidden", (torch.float32, torch.bfloat16), 3)
+    dev = hidden.device
+    _device_tensor(weight, "weight", torch.float8_e4m3fn, 2, dev)
+    B, rows, d = hidden.shape
+    V = weight.shape[0]
+    if hidden.stride(2) != 1 or weight.stride(1) != 1 or weight.shape[1] != d:
+        raise ValueError("expected hidden [B][rows][d] and weight [V][d] with contiguous last axes")
+    scale = _out_tensor(weight_scale, ((V + 127) // 128, (d + 127) // 128), torch.float32, dev,
+                        "weight_scale")
+    need = lib().spec_lmhead_fp8_workspace(B, rows, d)
+    if need == 0:
+        _check(SPEC_ERR_INVALID_ARG, "spec_lmhead_fp8_workspace")
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((B, rows, V), dtype=out_dtype, device=dev)
+        elif tuple(out.shape) != (B, rows, V) or out.device != dev:
+            raise ValueError("out must be [%d][%d][%d] on %s" % (B, rows, V, dev))
+        ws = _scratch(workspace, dev, need)
+        h = spec_logits_t(hidden.data_ptr(), _dtype_code(hidden), 0, _stride(hidden, 0),
+                          _stride(hidden, 1))
+        rc = lib().spec_lmhead_fp8(h, B, rows, d, weight.data_ptr(), max(weight.stride(0), d),
+                                   scale.data_ptr(), V, _logits(out, rows), ws.data_ptr(),
+                                   ws.numel() * ws.element_size(), st)
+    _check(rc, "spec_lmhead_fp8")
+    return out

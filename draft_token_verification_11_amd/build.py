@@ -11,7 +11,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libspecverify.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = [os.path.join(CSRC, "sv_abi.hip")]
+SOURCES = [os.path.join(CSRC, "sv_abi.hip"), os.path.join(CSRC, "sv_lowbit.hip")]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     # keep hand-written and compiler-made packed fp32 arithmetic out of the code

@@ -1,0 +1,312 @@
+// sv_lowbit.hip -- the C ABI of the target's pass in few bits: argument
+// validation and kernel launches for gfx950.  See
+// include/specverify_lowbit.h for the contract of every entry point.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "specverify_lowbit.h"
+#include "sv_cache4.hpp"
+#include "sv_fp8.hpp"
+
+namespace {
+
+constexpr int64_t kMaxWorkItems = (int64_t(1) << 32) - 1;
+constexpr int32_t kMaxB = 1 << 16;         // sequences of a cache call
+constexpr int32_t kMaxNew = 1 << 24;       // new tokens of a sequence in a cache call
+constexpr int32_t kMaxTableCols = 1 << 24;  // positions stay below 2^30
+constexpr int32_t kMaxQHeads = 16384;
+
+size_t elem_size(int dtype) { return dtype == SPEC_DTYPE_BF16 ? 2 : 4; }
+bool dtype_ok(int dtype) { return dtype == SPEC_DTYPE_F32 || dtype == SPEC_DTYPE_BF16; }
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+bool grid_fits(int64_t blocks, int threads) { return blocks >= 1 && blocks * threads <= kMaxWorkItems; }
+int finish_launch() { return hipGetLastError() == hipSuccess ? SPEC_OK : SPEC_ERR_HIP; }
+
+bool head_dim_ok(int32_t d) { return d == 64 || d == 128 || d == 256; }
+
+int check_cache(const spec_cache4_t& c) {
+  if (!c.pages || !c.table) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(c.pages, 16) || !aligned(c.table, 4)) return SPEC_ERR_INVALID_ARG;
+  if (c.n_pages < 1 || c.table_cols < 1 || c.heads < 1 || c.table_stride < c.table_cols)
+    return SPEC_ERR_INVALID_ARG;
+  if (!head_dim_ok(c.head_dim) || c.heads > SPEC_CACHE4_MAX_HEADS || c.table_cols > kMaxTableCols)
+    return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+int check_heads(const spec_heads_t& x) {
+  if (!x.data) return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(x.dtype)) return SPEC_ERR_UNSUPPORTED;
+  const int64_t per = int64_t(16 / elem_size(x.dtype));
+  if (!aligned(x.data, 16)) return SPEC_ERR_INVALID_ARG;
+  for (int64_t s : {x.seq_stride, x.pos_stride, x.head_stride})
+    if (s < 0 || s % per) return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+// Rows that are written must not share elements: every stride of an axis
+// longer than one is at least a head's width.
+int check_written(const spec_heads_t& x, int64_t B, int64_t T, int64_t heads, int64_t d) {
+  if ((B > 1 && x.seq_stride < d) || (T > 1 && x.pos_stride < d) || (heads > 1 && x.head_stride < d))
+    return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+int check_new(int32_t B, int32_t T, const int32_t* start) {
+  if (B < 1 || T < 1 || !start || !aligned(start, 4)) return SPEC_ERR_INVALID_ARG;
+  if (B > kMaxB || T > kMaxNew) return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+sv::C4View view(const spec_cache4_t& c) {
+  return {static_cast<uint8_t*>(c.pages), c.table, c.table_stride, c.n_pages, c.table_cols, c.heads};
+}
+sv::C4Heads heads(const spec_heads_t& x) {
+  return {x.data, x.seq_stride, x.pos_stride, x.head_stride};
+}
+
+// Arguments of the two moving calls, and their grid.
+int move_args(const spec_cache4_t& c, const spec_heads_t& k, const spec_heads_t& v, int32_t B,
+              int32_t T, const int32_t* start, const int32_t* count, sv::C4MoveArgs* A,
+              unsigned* grid) {
+  int rc;
+  if ((rc = check_new(B, T, start)) != SPEC_OK) return rc;
+  if ((rc = check_cache(c)) != SPEC_OK) return rc;
+  if ((rc = check_heads(k)) != SPEC_OK) return rc;
+  if ((rc = check_heads(v)) != SPEC_OK) return rc;
+  if (k.dtype != v.dtype || (count && !aligned(count, 4))) return SPEC_ERR_INVALID_ARG;
+  const int64_t per = 512 / c.head_dim;  // tokens of a wave
+  const int64_t runs = (int64_t(T) + 2 * per - 2) / per;
+  const int64_t waves = int64_t(B) * runs * c.heads;
+  const int64_t blocks = (waves + 3) / 4;
+  if (!grid_fits(blocks, 256)) return SPEC_ERR_UNSUPPORTED;
+  *A = {view(c), heads(k), heads(v), start, count, waves, T, int32_t(runs)};
+  *grid = unsigned(blocks);
+  return SPEC_OK;
+}
+
+template <typename T>
+void launch_write(int32_t d, unsigned grid, const sv::C4MoveArgs& A, hipStream_t st) {
+  if (d == 64) hipLaunchKernelGGL((sv::k_cache4_write<T, 64>), dim3(grid), dim3(256), 0, st, A);
+  else if (d == 128) hipLaunchKernelGGL((sv::k_cache4_write<T, 128>), dim3(grid), dim3(256), 0, st, A);
+  else hipLaunchKernelGGL((sv::k_cache4_write<T, 256>), dim3(grid), dim3(256), 0, st, A);
+}
+template <typename T>
+void launch_read(int32_t d, unsigned grid, const sv::C4MoveArgs& A, hipStream_t st) {
+  if (d == 64) hipLaunchKernelGGL((sv::k_cache4_read<T, 64>), dim3(grid), dim3(256), 0, st, A);
+  else if (d == 128) hipLaunchKernelGGL((sv::k_cache4_read<T, 128>), dim3(grid), dim3(256), 0, st, A);
+  else hipLaunchKernelGGL((sv::k_cache4_read<T, 256>), dim3(grid), dim3(256), 0, st, A);
+}
+
+// Row tiles of 16 a workgroup keeps (its accumulators grow with them), and
+// how many such blocks hold the rows of a kv head.
+int max_tiles(int32_t d) { return d == 256 ? 2 : 4; }
+void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
+  const int64_t t = (rows + 15) / 16;
+  *blocks = (t + max_tiles(d) - 1) / max_tiles(d);
+  *tiles = int((t + *blocks - 1) / *blocks);
+  if (*tiles == 3) *tiles = 4;
+}
+
+// Workgroups of the attention: as many as the largest device of this kind
+// holds at once; fewer pages than that leave the rest idle.
+constexpr int64_t kAttnGrid = 512;
+
+int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
+  if (B < 1 || T < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads) return SPEC_ERR_INVALID_ARG;
+  if (B > kMaxB || T > SPEC_CACHE4_MAX_T || kv_heads > SPEC_CACHE4_MAX_HEADS ||
+      q_heads > kMaxQHeads || !head_dim_ok(d))
+    return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+size_t attention_workspace(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
+  int tiles;
+  int64_t blocks;
+  row_blocks(int64_t(T) * (q_heads / kv_heads), d, &tiles, &blocks);
+  return size_t(kAttnGrid) * 2 * size_t(tiles) * 16 * size_t(d + 2) * 4;
+}
+
+template <int D, int RT>
+void launch_attention(const sv::C4AttnArgs& A, unsigned join, hipStream_t st) {
+  hipLaunchKernelGGL((sv::k_attention_cache4<D, RT>), dim3(unsigned(A.grid)), dim3(256), 0, st, A);
+  hipLaunchKernelGGL((sv::k_attention_cache4_join<D, RT>), dim3(join), dim3(256), 0, st, A);
+}
+template <int D>
+void launch_attention(int tiles, const sv::C4AttnArgs& A, unsigned join, hipStream_t st) {
+  if (tiles == 1) launch_attention<D, 1>(A, join, st);
+  else if (tiles == 2) launch_attention<D, 2>(A, join, st);
+  else if constexpr (D < 256) launch_attention<D, 4>(A, join, st);
+}
+
+int check_head(const void* weight, int64_t row_bytes, int32_t V, int32_t d) {
+  if (!weight || V < 1 || d < 32 || d % 32) return SPEC_ERR_INVALID_ARG;
+  if (V > SPEC_MAX_V || d > 65536) return SPEC_ERR_UNSUPPORTED;
+  if (!aligned(weight, 16) || row_bytes % 16) return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+int64_t padded(int32_t d) { return (int64_t(d) + 127) / 128 * 128; }
+
+template <typename TO>
+void launch_head(const sv::F8HeadArgs& A, hipStream_t st) {
+  const unsigned gx = unsigned((A.V + 127) / 128);
+  if (A.M <= 16)
+    hipLaunchKernelGGL((sv::k_lmhead_fp8<TO, 1, 2>), dim3(gx, 1), dim3(256), 0, st, A);
+  else
+    hipLaunchKernelGGL((sv::k_lmhead_fp8<TO, 4, 2>), dim3(gx, unsigned((A.M + 63) / 64)), dim3(256), 0, st, A);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_cache4_record_bytes(int32_t head_dim) {
+  return head_dim_ok(head_dim) ? size_t(68) * size_t(head_dim) : 0;
+}
+
+int spec_cache4_write(spec_cache4_t cache, spec_heads_t k, spec_heads_t v, int32_t B, int32_t T,
+                      const int32_t* start, const int32_t* count, void* stream) {
+  sv::C4MoveArgs A;
+  unsigned grid;
+  const int rc = move_args(cache, k, v, B, T, start, count, &A, &grid);
+  if (rc != SPEC_OK) return rc;
+  auto st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (k.dtype == SPEC_DTYPE_BF16) launch_write<uint16_t>(cache.head_dim, grid, A, st);
+  else launch_write<float>(cache.head_dim, grid, A, st);
+  return finish_launch();
+}
+
+int spec_cache4_read(spec_cache4_t cache, spec_heads_t k, spec_heads_t v, int32_t B, int32_t T,
+                     const int32_t* start, const int32_t* count, void* stream) {
+  sv::C4MoveArgs A;
+  unsigned grid;
+  int rc = move_args(cache, k, v, B, T, start, count, &A, &grid);
+  if (rc != SPEC_OK) return rc;
+  if ((rc = check_written(k, B, T, cache.heads, cache.head_dim)) != SPEC_OK) return rc;
+  if ((rc = check_written(v, B, T, cache.heads, cache.head_dim)) != SPEC_OK) return rc;
+  auto st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (k.dtype == SPEC_DTYPE_BF16) launch_read<uint16_t>(cache.head_dim, grid, A, st);
+  else launch_read<float>(cache.head_dim, grid, A, st);
+  return finish_launch();
+}
+
+size_t spec_attention_cache4_workspace(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
+                                       int32_t head_dim) {
+  if (check_attention_sizes(B, T, q_heads, heads, head_dim) != SPEC_OK) return 0;
+  return attention_workspace(T, q_heads, heads, head_dim);
+}
+
+int spec_attention_cache4(spec_cache4_t cache, spec_heads_t q, int32_t B, int32_t T,
+                          int32_t q_heads, const int32_t* start, const int32_t* count,
+                          const uint32_t* mask, int64_t mask_seq_stride, int64_t mask_pos_stride,
+                          float scale, spec_heads_t out, float* lse, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  int rc;
+  if ((rc = check_new(B, T, start)) != SPEC_OK) return rc;
+  if ((rc = check_cache(cache)) != SPEC_OK) return rc;
+  if ((rc = check_attention_sizes(B, T, q_heads, cache.heads, cache.head_dim)) != SPEC_OK) return rc;
+  if ((rc = check_heads(q)) != SPEC_OK) return rc;
+  if ((rc = check_heads(out)) != SPEC_OK) return rc;
+  if (q.dtype != SPEC_DTYPE_BF16 || out.dtype != SPEC_DTYPE_BF16) return SPEC_ERR_UNSUPPORTED;
+  if ((rc = check_written(out, B, T, q_heads, cache.head_dim)) != SPEC_OK) return rc;
+  if ((count && !aligned(count, 4)) || (lse && !aligned(lse, 4))) return SPEC_ERR_INVALID_ARG;
+  if (mask && (!aligned(mask, 4) || mask_seq_stride < 0 || mask_pos_stride < 0))
+    return SPEC_ERR_INVALID_ARG;
+  const float c = float(double(scale) * 1.4426950408889634);
+  if (!std::isfinite(scale) || !(scale > 0.0f) || !std::isfinite(c) || !(c > 0.0f))
+    return SPEC_ERR_INVALID_ARG;
+  const int32_t G = q_heads / cache.heads;
+  int tiles;
+  int64_t blocks;
+  row_blocks(int64_t(T) * G, cache.head_dim, &tiles, &blocks);
+  const int64_t join = int64_t(B) * cache.heads * blocks;
+  if (!grid_fits(join, 256)) return SPEC_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) ||
+      workspace_bytes < attention_workspace(T, q_heads, cache.heads, cache.head_dim))
+    return SPEC_ERR_WORKSPACE;
+  sv::C4AttnArgs A{view(cache), static_cast<const uint16_t*>(q.data), q.seq_stride, q.pos_stride,
+                   q.head_stride, static_cast<uint16_t*>(out.data), out.seq_stride, out.pos_stride,
+                   out.head_stride, lse, start, count, mask, mask_seq_stride, mask_pos_stride, B, T, G,
+                   int32_t(blocks), c, static_cast<float*>(workspace), int32_t(kAttnGrid)};
+  auto st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (cache.head_dim == 64) launch_attention<64>(tiles, A, unsigned(join), st);
+  else if (cache.head_dim == 128) launch_attention<128>(tiles, A, unsigned(join), st);
+  else launch_attention<256>(tiles, A, unsigned(join), st);
+  return finish_launch();
+}
+
+int spec_quantize_fp8(const void* weight, int32_t dtype, int64_t weight_stride, int32_t V,
+                      int32_t d, void* q, float* scale, void* stream) {
+  if (!dtype_ok(dtype)) return SPEC_ERR_UNSUPPORTED;
+  int rc;
+  if ((rc = check_head(weight, weight_stride * int64_t(elem_size(dtype)), V, d)) != SPEC_OK) return rc;
+  if (weight_stride < d || !q || !scale || !aligned(q, 16) || !aligned(scale, 4))
+    return SPEC_ERR_INVALID_ARG;
+  const int64_t db = padded(d) / 128, blocks = (int64_t(V) + 127) / 128 * db;
+  if (!grid_fits(blocks, 256)) return SPEC_ERR_UNSUPPORTED;
+  auto st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  if (dtype == SPEC_DTYPE_BF16)
+    hipLaunchKernelGGL((sv::k_quantize_fp8<uint16_t>), dim3(unsigned(blocks)), dim3(256), 0, st,
+                       static_cast<const uint16_t*>(weight), weight_stride, int64_t(V), d, int32_t(db),
+                       static_cast<uint8_t*>(q), scale);
+  else
+    hipLaunchKernelGGL((sv::k_quantize_fp8<float>), dim3(unsigned(blocks)), dim3(256), 0, st,
+                       static_cast<const float*>(weight), weight_stride, int64_t(V), d, int32_t(db),
+                       static_cast<uint8_t*>(q), scale);
+  return finish_launch();
+}
+
+size_t spec_lmhead_fp8_workspace(int32_t B, int32_t rows, int32_t d) {
+  if (B < 1 || rows < 1 || d < 32 || d % 32 || B > (1 << 24) || rows > 2 * SPEC_MAX_K + 1 || d > 65536)
+    return 0;
+  return align256(size_t(B) * size_t(rows) * size_t(padded(d)) * 2);
+}
+
+int spec_lmhead_fp8(spec_logits_t hidden, int32_t B, int32_t rows, int32_t d, const void* weight,
+                    int64_t weight_stride, const float* scale, int32_t V, spec_logits_t logits,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  int rc;
+  if (B < 1 || rows < 1) return SPEC_ERR_INVALID_ARG;
+  if (B > (1 << 24) || rows > 2 * SPEC_MAX_K + 1) return SPEC_ERR_UNSUPPORTED;
+  if ((rc = check_head(weight, weight_stride, V, d)) != SPEC_OK) return rc;
+  if (weight_stride < d || !scale || !aligned(scale, 4)) return SPEC_ERR_INVALID_ARG;
+  if (!dtype_ok(hidden.dtype) || !dtype_ok(logits.dtype)) return SPEC_ERR_UNSUPPORTED;
+  const int64_t per = int64_t(16 / elem_size(hidden.dtype));
+  if (!hidden.data || !aligned(hidden.data, 16) || hidden.seq_stride < 0 || hidden.pos_stride < 0 ||
+      hidden.seq_stride % per || hidden.pos_stride % per)
+    return SPEC_ERR_INVALID_ARG;
+  // written rows must not share elements
+  if (!logits.data || !aligned(logits.data, elem_size(logits.dtype)) ||
+      (rows > 1 && logits.pos_stride < V) || (B > 1 && logits.seq_stride < V))
+    return SPEC_ERR_INVALID_ARG;
+  const int64_t M = int64_t(B) * rows, dp = padded(d);
+  const int64_t rounding = (M * (dp / 128) + 15) / 16;
+  if (!grid_fits(rounding, 256) || !grid_fits((int64_t(V) + 127) / 128, 256) || (M + 63) / 64 > 65535)
+    return SPEC_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < spec_lmhead_fp8_workspace(B, rows, d))
+    return SPEC_ERR_WORKSPACE;
+  auto st = static_cast<hipStream_t>(stream);
+  sv::F8HiddenArgs H{hidden.data, hidden.seq_stride, hidden.pos_stride, rows, M, d, int32_t(dp),
+                     static_cast<uint16_t*>(workspace)};
+  sv::F8HeadArgs A{H.out, M, V, d, int32_t(dp), rows, static_cast<const uint8_t*>(weight),
+                   weight_stride, scale, const_cast<void*>(logits.data), logits.seq_stride,
+                   logits.pos_stride};
+  (void)hipGetLastError();
+  if (hidden.dtype == SPEC_DTYPE_BF16)
+    hipLaunchKernelGGL((sv::k_hidden_fp8<uint16_t>), dim3(unsigned(rounding)), dim3(256), 0, st, H);
+  else
+    hipLaunchKernelGGL((sv::k_hidden_fp8<float>), dim3(unsigned(rounding)), dim3(256), 0, st, H);
+  if (logits.dtype == SPEC_DTYPE_BF16) launch_head<uint16_t>(A, st);
+  else launch_head<float>(A, st);
+  return finish_launch();
+}
+
+}  // extern "C"

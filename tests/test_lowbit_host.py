@@ -1,0 +1,260 @@
+"""Host-side checks of the target's pass in few bits (no GPU needed): the
+header and its symbols, sizes, refusals before any HIP call, the record's
+layout and bounds, and the plain forms the GPU tests compare with."""
+import ctypes
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import draft_token_verification_11_amd as sv
+from tests import lowbit_plain as plain
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "specverify_lowbit.h")
+HIPCC = "/opt/rocm/bin/hipcc"
+OK, BAD, UNSUP, WS = sv.SPEC_OK, sv.SPEC_ERR_INVALID_ARG, sv.SPEC_ERR_UNSUPPORTED, sv.SPEC_ERR_WORKSPACE
+
+
+def test_header_and_symbols():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(spec_[a-z0-9_]+)\s*\(", text)))
+    assert names == sorted(["spec_cache4_record_bytes", "spec_cache4_write", "spec_cache4_read",
+                            "spec_attention_cache4_workspace", "spec_attention_cache4",
+                            "spec_quantize_fp8", "spec_lmhead_fp8_workspace", "spec_lmhead_fp8"])
+    out = subprocess.run(["nm", "-D", "--defined-only", sv.library_path()], capture_output=True,
+                         text=True, check=True).stdout.split()
+    assert all(n in out for n in names)
+
+
+@pytest.mark.parametrize("lang", ["c", "c++"])
+def test_header_compiles(tmp_path, lang):
+    src = tmp_path / ("t.c" if lang == "c" else "t.cpp")
+    src.write_text('#include "specverify_lowbit.h"\nint main(void) { return (int)sizeof(spec_cache4_t) - 40'
+                   ' + (int)sizeof(spec_heads_t) - 40; }\n')
+    subprocess.run(["gcc" if lang == "c" else "g++", "-Wall", "-Werror", "-I", os.path.dirname(HEADER),
+                    "-o", str(tmp_path / "t"), str(src)], check=True)
+    assert subprocess.run([str(tmp_path / "t")]).returncode == 0
+    assert ctypes.sizeof(sv.spec_cache4_t) == 40 and ctypes.sizeof(sv.spec_heads_t) == 40
+
+
+def test_sizes():
+    assert [sv.cache4_record_bytes(d) for d in (64, 128, 256, 96, 0, -1)] == [4352, 8704, 17408, 0, 0, 0]
+    L = sv.lib()
+    assert L.spec_attention_cache4_workspace(1, 1, 8, 8, 128) > 0
+    for bad in [(0, 1, 8, 8, 128), (1, 0, 8, 8, 128), (1, 257, 8, 8, 128), (1, 1, 9, 8, 128), (1, 1, 8, 0, 128),
+                (1, 1, 8, 8, 80), ((1 << 16) + 1, 1, 8, 8, 128), (1, 1, 16385, 1, 64)]:
+        assert L.spec_attention_cache4_workspace(*bad) == 0, bad
+    assert L.spec_lmhead_fp8_workspace(1, 9, 4096) >= 9 * 4096
+    for bad in [(0, 1, 128), (1, 0, 128), (1, 130, 128), (1, 1, 16), (1, 1, 100), (1, 1, 65568)]:
+        assert L.spec_lmhead_fp8_workspace(*bad) == 0, bad
+
+
+def _cache(pages=4096, table=4096, stride=4, n=8, cols=4, heads=2, d=128):
+    return sv.spec_cache4_t(pages, table, stride, n, cols, heads, d)
+
+
+def _heads(ptr=4096, dtype=1, seq=4096, pos=256, head=128):
+    return sv.spec_heads_t(ptr, dtype, 0, seq, pos, head)
+
+
+BAD_CACHES = [(dict(pages=0), BAD), (dict(pages=4104), BAD), (dict(table=0), BAD), (dict(table=4098), BAD),
+              (dict(stride=3), BAD), (dict(n=0), BAD), (dict(cols=0), BAD), (dict(heads=0), BAD),
+              (dict(d=96), UNSUP), (dict(heads=1025), UNSUP), (dict(cols=(1 << 24) + 1, stride=1 << 25), UNSUP)]
+BAD_HEADS = [(dict(ptr=0), BAD), (dict(ptr=4098), BAD), (dict(dtype=2), UNSUP), (dict(seq=-8), BAD),
+             (dict(pos=100), BAD), (dict(head=4), BAD)]
+
+
+@pytest.mark.parametrize("which", ["write", "read"])
+def test_cache_refusals(which):
+    L, p = sv.lib(), ctypes.c_void_p(4096)
+    f = L.spec_cache4_write if which == "write" else L.spec_cache4_read
+
+    def call(c=None, k=None, v=None, B=2, T=3, start=p, count=None):
+        return f(c or _cache(), k or _heads(), v or _heads(), B, T, start, count, None)
+
+    for kw, want in BAD_CACHES:
+        assert call(c=_cache(**kw)) == want, kw
+    for kw, want in BAD_HEADS:
+        assert call(k=_heads(**kw)) == want and call(v=_heads(**kw)) == want, kw
+    assert call(v=_heads(dtype=0)) == BAD
+    assert call(B=0) == BAD and call(T=0) == BAD and call(start=None) == BAD
+    assert call(start=ctypes.c_void_p(4098)) == BAD and call(count=ctypes.c_void_p(4097)) == BAD
+    assert call(B=(1 << 16) + 1) == UNSUP and call(T=(1 << 24) + 1) == UNSUP
+    if which == "read":  # written rows share no elements
+        for kw in (dict(seq=0), dict(pos=64), dict(head=64)):
+            assert call(k=_heads(**kw)) == BAD and call(v=_heads(**kw)) == BAD
+
+
+def test_attention_refusals():
+    L, p = sv.lib(), ctypes.c_void_p(4096)
+    ws = ctypes.c_void_p(1 << 20)
+
+    def call(c=None, q=None, B=2, T=3, Hq=4, start=p, count=None, mask=None, ms=0, mp=1, scale=0.1, out=None,
+             lse=None, w=ws, wb=1 << 30):
+        return L.spec_attention_cache4(c or _cache(), q or _heads(head=128, pos=512), B, T, Hq, start, count, mask,
+                                       ms, mp, scale, out or _heads(head=128, pos=512), lse, w, wb, None)
+
+    for kw, want in BAD_CACHES:
+        assert call(c=_cache(**kw)) == want, kw
+    for kw, want in BAD_HEADS:
+        assert call(q=_heads(**kw)) == want and call(out=_heads(**kw)) == want, kw
+    assert call(q=_heads(dtype=0)) == UNSUP and call(out=_heads(dtype=0)) == UNSUP
+    for kw in (dict(seq=0), dict(pos=64), dict(head=64)):
+        assert call(out=_heads(**kw)) == BAD
+    assert call(Hq=3) == BAD and call(Hq=0) == BAD and call(T=257) == UNSUP
+    for s in (0.0, -1.0, float("nan"), float("inf"), 3e38):
+        assert call(scale=s) == BAD, s
+    assert call(mask=ctypes.c_void_p(4098)) == BAD and call(mask=p, ms=-1) == BAD and call(mask=p, mp=-1) == BAD
+    assert call(lse=ctypes.c_void_p(4098)) == BAD and call(start=None) == BAD
+    assert call(w=None) == WS and call(wb=16) == WS and call(w=ctypes.c_void_p((1 << 20) + 16)) == WS
+
+
+def test_head_refusals():
+    L, p = sv.lib(), ctypes.c_void_p(1 << 16)
+    ws = ctypes.c_void_p(1 << 20)
+
+    def quant(w=p, dtype=1, stride=256, V=300, d=256, q=p, s=p):
+        return L.spec_quantize_fp8(w, dtype, stride, V, d, q, s, None)
+
+    assert quant(w=None) == BAD and quant(w=ctypes.c_void_p(4104)) == BAD and quant(dtype=3) == UNSUP
+    assert quant(stride=128) == BAD and quant(stride=260) == BAD and quant(V=0) == BAD and quant(d=0) == BAD
+    assert quant(d=100) == BAD and quant(d=65568, stride=65568) == UNSUP and quant(V=(1 << 24) + 1) == UNSUP
+    assert quant(q=None) == BAD and quant(q=ctypes.c_void_p(4104)) == BAD and quant(s=None) == BAD
+
+    def lg(ptr=1 << 16, dtype=0, seq=1500, pos=300):
+        return sv.spec_logits_t(ptr, dtype, 0, seq, pos)
+
+    def head(h=None, B=2, rows=5, d=256, w=p, stride=256, s=p, V=300, out=None, wk=ws, wb=1 << 30):
+        return L.spec_lmhead_fp8(h or lg(seq=1280, pos=256), B, rows, d, w, stride, s, V, out or lg(), wk, wb, None)
+
+    assert head(B=0) == BAD and head(rows=0) == BAD and head(rows=130) == UNSUP and head(B=(1 << 24) + 1) == UNSUP
+    assert head(d=48) == BAD and head(d=16) == BAD and head(V=0) == BAD and head(V=(1 << 24) + 1) == UNSUP
+    assert head(w=None) == BAD and head(stride=248) == BAD and head(stride=264) == BAD and head(s=None) == BAD
+    assert head(h=lg(ptr=0)) == BAD and head(h=lg(ptr=4104)) == BAD and head(h=lg(dtype=2)) == UNSUP
+    assert head(h=lg(pos=257)) == BAD and head(h=lg(seq=-4)) == BAD
+    assert head(out=lg(ptr=0)) == BAD and head(out=lg(ptr=4098)) == BAD and head(out=lg(pos=299)) == BAD
+    assert head(out=lg(seq=299)) == BAD and head(out=lg(dtype=5)) == UNSUP
+    assert head(wk=None) == WS and head(wb=64) == WS and head(wk=ctypes.c_void_p((1 << 20) + 128)) == WS
+
+
+def test_binding_refusals():
+    z = torch.zeros
+    with pytest.raises(ValueError):
+        sv.cache4_write(z(1, 1, 8704, dtype=torch.uint8), z(1, 1, dtype=torch.int32), z(1, dtype=torch.int32),
+                        z(1, 1, 1, 128), z(1, 1, 1, 128))  # not on a device
+    with pytest.raises(TypeError):
+        sv.attention_cache4(z(1, 1, 1, 128), None, None, None)
+    with pytest.raises(TypeError):
+        sv.quantize_fp8(z(4, 32, dtype=torch.float16))
+    with pytest.raises(TypeError):
+        sv.lmhead_fp8([0], None, None)
+    with pytest.raises(sv.SpecError):
+        sv.cache4_alloc(1, 1, 80, "cpu")
+    for bad in ([], [0], [-1, 1], [-1, 0, 2]):
+        with pytest.raises(ValueError):
+            sv.tree_mask(bad)
+
+
+def test_tree_mask():
+    m = sv.tree_mask([-1] + [i - 1 for i in range(1, 40)])
+    assert m.shape == (1, 40, 2) and m.dtype == torch.int32
+    full = (m.long() & 0xFFFFFFFF)[0]
+    assert all(int(full[i, 0]) + (int(full[i, 1]) << 32) == (1 << (i + 1)) - 1 for i in range(40))
+    assert sv.tree_mask([-1, 0, 0, 2])[0, :, 0].tolist() == [1, 3, 5, 13]
+
+
+LAYOUT = r"""
+#include <hip/hip_runtime.h>
+#include <cstdio>
+#include <vector>
+#include "sv_cache4.hpp"
+static int bad = 0;
+template <int D> void layout() {
+  constexpr int NG = D / 32, U = D == 64 ? 2 : 4;
+  std::vector<int> hit(68 * D, 0);
+  auto mark = [&](int at, int n) { for (int i = 0; i < n; ++i) { if (at + i < 0 || at + i >= 68 * D) { bad++; continue; } hit[at + i]++; } };
+  for (int t = 0; t < 64; ++t) {
+    for (int u = 0; u < D / 8; ++u) {
+      mark(t * (D / 2) + 4 * u, 4);
+      mark(sv::c4_val_off<D>(t, u), U);
+      if (D == 64) mark(sv::c4_val_off<D>(t, u) + 4 * NG, U);
+    }
+    for (int g = 0; g < NG; ++g) { mark(sv::c4_key_exp_off<D>(t, g), 1); mark(sv::c4_val_exp_off<D>(t, g), 1); }
+  }
+  for (int x : hit) bad += x != 1;
+  // what a wave of the attention loads: every byte of the record, and no other
+  std::vector<int> seen(68 * D, 0);
+  auto load = [&](int at, int n) { if (at % (n < 16 ? n : 16)) bad++; for (int i = 0; i < n; ++i) { if (at + i < 0 || at + i >= 68 * D) bad++; else seen[at + i] = 1; } };
+  for (int lane = 0; lane < 64; ++lane) {
+    const int n = lane & 15, q = lane >> 4;
+    for (int t = 0; t < 4; ++t) {
+      load((16 * t + n) * (D / 2) + q * (D / 8), D / 8);
+      load(sv::C4<D>::kVal + (t * 64 + lane) * (D / 8), D / 8);
+      load(sv::C4<D>::kValExp + (4 * t + q) * (4 * NG) + (n * NG / 16) * 4, 4);
+    }
+    load(sv::C4<D>::kKeyExp + (q * NG / 4) * 64 + n * 4, 4);
+    if (D == 256) load(sv::C4<D>::kKeyExp + (q * NG / 4 + 1) * 64 + n * 4, 4);
+  }
+  for (int x : seen) bad += x != 1;
+}
+int main() {
+  layout<64>(); layout<128>(); layout<256>();
+  // page numbers of any kind are refused or in range
+  std::vector<int32_t> table = {0, 6, 7, -1, 2147483647, -2147483647 - 1};
+  sv::C4View v{nullptr, table.data(), 6, 7, 6, 1};
+  const int32_t want[] = {0, 6, -1, -1, -1, -1};
+  for (int p = 0; p < 6; ++p) bad += v.page(0, p) != want[p];
+  struct { int32_t s, n, T; bool ok; } f[] = {{0, 1, 1, true}, {-1, 1, 1, false}, {0, -1, 1, false}, {0, 2, 1, false},
+    {383, 1, 1, true}, {384, 0, 1, true}, {384, 1, 1, false}, {2147483647, 2147483647, 2147483647, false}};
+  for (auto& x : f) bad += v.fits(x.s, x.n, x.T) != x.ok;
+  // records of a large pool pass 32 bits
+  sv::C4View big{nullptr, nullptr, 0, 2000000000, 1, 8};
+  bad += reinterpret_cast<uintptr_t>(big.record<128>(1999999999, 7)) != (uintptr_t)(1999999999ull * 8 + 7) * 8704;
+  std::printf(bad ? "bad %d\n" : "layout ok\n", bad);
+  return bad != 0;
+}
+"""
+
+
+@pytest.mark.skipif(not os.path.exists(HIPCC), reason="no ROCm toolchain")
+def test_layout_and_bounds_on_the_host(tmp_path):
+    src, exe = tmp_path / "t.hip", str(tmp_path / "t")
+    src.write_text(LAYOUT)
+    r = subprocess.run([HIPCC, "--offload-arch=gfx950", "-O1", "-std=c++17", "-w",
+                        "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-I",
+                        os.path.join(ROOT, "draft_token_verification_11_amd", "csrc"), "-o", exe, str(src)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert "layout ok" in subprocess.run([exe], capture_output=True, text=True).stdout
+
+
+def test_plain_forms():
+    """The plain forms against the definitions' own examples, with a planted mistake in each."""
+    x = np.zeros(32)
+    x[:9] = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, -6.0]
+    c, e = plain.group4(x)
+    assert e == 127 and c[:9].tolist() == [0, 2, 2, 4, 4, 6, 6, 7, 15]
+    assert plain.group4(x * 1.0001)[1] == 128 and plain.group4(np.zeros(32))[1] == 1
+    assert [plain.exponent(a, 448.0) for a in (448.0, 448.1, 1.0)] == [127, 128, 119]
+    assert plain.E4M3[-1] == 448.0 and len(plain.E4M3) == 127
+    for D in (64, 128, 256):
+        at = np.concatenate([np.concatenate(plain.offsets(t, D)) for t in range(64)])
+        assert np.array_equal(np.sort(at), np.arange(68 * D))
+    rs = np.random.default_rng(0)
+    pages, table = np.zeros((3, 1, 68 * 64), np.uint8), np.array([[2, 0]], np.int32)
+    K, V = rs.normal(0, 1, (70, 64)), rs.normal(0, 1, (70, 64))
+    for p in range(70):
+        plain.store(pages, table, 0, 0, p, K[p], V[p])
+    k0, v0 = plain.fetch(pages, table, 0, 0, 65, 64)
+    # a step of e2m1 is at most a third of its value (1.5 to 2), half of the least code below
+    assert (np.abs(k0 - K[65]) <= np.maximum(np.abs(K[65]) / 5, np.abs(K[65]).max() / 6)).all()
+    q = rs.normal(0, 1, (1, 2, 1, 64))
+    out, lse, bo, bl = plain.attention(q, pages, table, [68], [2], lambda b, i, j: j <= i, 0.125)
+    s = np.array([plain.fetch(pages, table, 0, 0, p, 64)[0] for p in range(70)]) @ q[0, 1, 0] * 0.125
+    assert abs(lse[0, 1, 0] - np.log(np.exp(s).sum())) < 1e-12
+    wrong, *_ = plain.attention(q, pages, table, [68], [2], lambda b, i, j: True, 0.125)
+    assert (np.abs(wrong - out)[0, 0] > bo[0, 0]).any()  # a mask's mistake passes the bounds
