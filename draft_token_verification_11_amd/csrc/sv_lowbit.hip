@@ -151,13 +151,30 @@ int check_head(const void* weight, int64_t row_bytes, int32_t V, int32_t d) {
 
 int64_t padded(int32_t d) { return (int64_t(d) + 127) / 128 * 128; }
 
+// Few rows go straight from memory to the matrix instructions, more through
+// LDS in tiles.
+constexpr int64_t kHeadRows = 64;
+
+template <typename TO, int MB, int NB>
+void launch_head_rows(const sv::F8HeadArgs& A, hipStream_t st) {
+  hipLaunchKernelGGL((sv::k_lmhead_fp8_rows<TO, MB, NB>), dim3(unsigned((A.V + 16 * NB - 1) / (16 * NB))),
+                     dim3(64), 0, st, A);
+}
+template <typename TO, bool F8, int BV, int BM, int WV>
+void launch_head_tile(sv::F8HeadArgs A, hipStream_t st) {
+  A.v_tiles = int32_t((A.V + BV - 1) / BV);
+  A.m_tiles = int32_t((A.M + BM - 1) / BM);
+  const int64_t tiles = int64_t(A.v_tiles) * A.m_tiles;
+  hipLaunchKernelGGL((sv::k_lmhead_fp8_tile<TO, F8, BV, BM, WV>), dim3(unsigned((tiles + 7) / 8 * 8)),
+                     dim3(512), 0, st, A);
+}
 template <typename TO>
 void launch_head(const sv::F8HeadArgs& A, hipStream_t st) {
-  const unsigned gx = unsigned((A.V + 127) / 128);
-  if (A.M <= 16)
-    hipLaunchKernelGGL((sv::k_lmhead_fp8<TO, 1, 2>), dim3(gx, 1), dim3(256), 0, st, A);
-  else
-    hipLaunchKernelGGL((sv::k_lmhead_fp8<TO, 4, 2>), dim3(gx, unsigned((A.M + 63) / 64)), dim3(256), 0, st, A);
+  if (A.M <= 16) launch_head_rows<TO, 1, 4>(A, st);
+  else if (A.M <= 32) launch_head_rows<TO, 2, 4>(A, st);
+  else if (A.M <= kHeadRows) launch_head_rows<TO, 4, 2>(A, st);
+  else if constexpr (sizeof(TO) == 2) launch_head_tile<TO, true, 256, 256, 4>(A, st);
+  else launch_head_tile<TO, false, 128, 256, 2>(A, st);
 }
 
 }  // namespace
@@ -267,7 +284,8 @@ int spec_quantize_fp8(const void* weight, int32_t dtype, int64_t weight_stride, 
 size_t spec_lmhead_fp8_workspace(int32_t B, int32_t rows, int32_t d) {
   if (B < 1 || rows < 1 || d < 32 || d % 32 || B > (1 << 24) || rows > 2 * SPEC_MAX_K + 1 || d > 65536)
     return 0;
-  return align256(size_t(B) * size_t(rows) * size_t(padded(d)) * 2);
+  const size_t M = size_t(B) * size_t(rows);
+  return align256(M * size_t(padded(d))) + align256(M) * size_t(padded(d) / 128);
 }
 
 int spec_lmhead_fp8(spec_logits_t hidden, int32_t B, int32_t rows, int32_t d, const void* weight,
@@ -289,16 +307,18 @@ int spec_lmhead_fp8(spec_logits_t hidden, int32_t B, int32_t rows, int32_t d, co
     return SPEC_ERR_INVALID_ARG;
   const int64_t M = int64_t(B) * rows, dp = padded(d);
   const int64_t rounding = (M * (dp / 128) + 15) / 16;
-  if (!grid_fits(rounding, 256) || !grid_fits((int64_t(V) + 127) / 128, 256) || (M + 63) / 64 > 65535)
-    return SPEC_ERR_UNSUPPORTED;
+  const int64_t tiles = ((int64_t(V) + 127) / 128) * ((M + 127) / 128);  // of the smallest kind, and a round of 8
+  if (!grid_fits(rounding, 256) || !grid_fits(tiles + 8, 512)) return SPEC_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < spec_lmhead_fp8_workspace(B, rows, d))
     return SPEC_ERR_WORKSPACE;
   auto st = static_cast<hipStream_t>(stream);
   sv::F8HiddenArgs H{hidden.data, hidden.seq_stride, hidden.pos_stride, rows, M, d, int32_t(dp),
-                     static_cast<uint16_t*>(workspace)};
-  sv::F8HeadArgs A{H.out, M, V, d, int32_t(dp), rows, static_cast<const uint8_t*>(weight),
+                     static_cast<uint8_t*>(workspace),
+                     static_cast<uint8_t*>(workspace) + align256(size_t(M) * size_t(dp)),
+                     int64_t(align256(size_t(M)))};
+  sv::F8HeadArgs A{H.out, H.exps, H.m_pitch, M, V, d, int32_t(dp), rows, static_cast<const uint8_t*>(weight),
                    weight_stride, scale, const_cast<void*>(logits.data), logits.seq_stride,
-                   logits.pos_stride};
+                   logits.pos_stride, 0, 0};
   (void)hipGetLastError();
   if (hidden.dtype == SPEC_DTYPE_BF16)
     hipLaunchKernelGGL((sv::k_hidden_fp8<uint16_t>), dim3(unsigned(rounding)), dim3(256), 0, st, H);
