@@ -24,6 +24,12 @@ struct C4 {
   static constexpr int kValExp = kVal + 32 * D;
 };
 
+// A value that every lane of a wave needs, read by the scalar unit, so that
+// waiting for it is no wait for the vector loads under way.
+__device__ __forceinline__ int32_t c4_scalar(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(p);
+}
+
 struct C4View {
   uint8_t* pages;
   const int32_t* table;
@@ -37,6 +43,11 @@ struct C4View {
   // The pool page of the sequence's page `p` (0 <= p < table_cols), or -1.
   __host__ __device__ __forceinline__ int32_t page(int64_t b, int32_t p) const {
     const int32_t x = table[b * table_stride + p];
+    return (uint32_t)x < (uint32_t)n_pages ? x : -1;
+  }
+  // As page(), for a wave's common b and p.
+  __device__ __forceinline__ int32_t page_of_wave(int64_t b, int32_t p) const {
+    const int32_t x = c4_scalar(table + b * table_stride + p);
     return (uint32_t)x < (uint32_t)n_pages ? x : -1;
   }
   template <int D>
@@ -270,9 +281,13 @@ __global__ __launch_bounds__(256) void k_cache4_read(C4MoveArgs A) {
 // Work split: the pages of all (sequence, kv head, block of rows) are laid end
 // to end and cut into one equal range per workgroup, whatever the sequences'
 // lengths; the four waves of a workgroup take the range's pages in turn.  A
-// workgroup whose range ends inside a sequence leaves its rows' maximum, sum
-// and unnormalised output in the workspace, and k_attention_cache4_join adds
-// those up in order, so that results do not depend on the order of workgroups.
+// workgroup whose range cuts one of them leaves its rows' maximum, sum and
+// unnormalised output in the workspace, and k_attention_cache4_join adds those
+// up in order, so that results do not depend on the order of workgroups.
+// Workgroups of a call: two for each of 256 compute units, which is what fits
+// one.  Where fewer pages do not need them the rest end at once.
+constexpr int32_t kC4Grid = 512;
+
 struct C4AttnArgs {
   C4View cache;
   const uint16_t* q;
@@ -286,21 +301,42 @@ struct C4AttnArgs {
   int64_t mask_seq, mask_pos;
   int32_t B, T, G, row_blocks;
   float c;                // scale log2 e
-  float* parts;           // [2 grid] records of a workgroup's first and last cut segment
-  int32_t grid;
+  int32_t split;          // 0: no segment is cut, and there is nothing to join
+  struct C4Cut* cuts;     // [kC4Grid] the segment that a workgroup begins and others end
+  float* parts;           // [2 kC4Grid] records of a workgroup's first and last cut segment
+};
+
+struct C4Cut {
+  int32_t b, hr, nnew;  // its sequence, head and block of rows, and the sequence's new tokens
+  int32_t parts, slot;  // workgroups that hold it, from this one on (0: none); its record in this one
+  int32_t pad[3];
 };
 
 // Pages of sequence b that its new tokens attend to; 0 when it has no rows.
 // `bad`: ill-formed (one page then stands for the sequence, so that its rows
 // are visited).
+template <bool UNIFORM>
 __device__ __forceinline__ int32_t c4_pages(const C4AttnArgs& A, int64_t b, bool& bad) {
-  const int32_t s = A.start[b], n = A.count ? A.count[b] : A.T;
+  const int32_t s = UNIFORM ? c4_scalar(A.start + b) : A.start[b];
+  const int32_t n = !A.count ? A.T : UNIFORM ? c4_scalar(A.count + b) : A.count[b];
   bad = !A.cache.fits(s, n, A.T);
   if (bad) return 1;
   return n == 0 ? 0 : (s + n + kC4Page - 1) / kC4Page;
 }
 
-// Prefix sums of the sequences' pages over a workgroup: thread t owns
+// Beginning and ending a segment (its rows, the first loads, joining the four
+// waves) costs a workgroup as much time as about this many pages; without it
+// in the shares a batch with short sequences waits for the workgroups that
+// hold many of them (16 sequences of 37 to 8,155 tokens with 168 rows: 0.39 ms
+// against 0.10 for equal lengths).
+constexpr int32_t kC4SegCost = 6;
+
+// Weight of a segment of `pages`.
+__device__ __forceinline__ int64_t c4_weight(int32_t pages) {
+  return pages ? pages + kC4SegCost : 0;
+}
+
+// Prefix sums of the sequences' weights over a workgroup: thread t owns
 // sequences t * per .. + per.
 struct C4Plan {
   int64_t before[256];
@@ -314,7 +350,7 @@ __device__ __forceinline__ int32_t c4_plan(const C4AttnArgs& A, C4Plan& P) {
   for (int32_t j = 0; j < per; ++j) {
     const int64_t b = (int64_t)tid * per + j;
     bool bad;
-    if (b < A.B) sum += c4_pages(A, b, bad);
+    if (b < A.B) sum += c4_weight(c4_pages<false>(A, b, bad));
   }
   int64_t incl = sum;
 #pragma unroll
@@ -334,10 +370,23 @@ __device__ __forceinline__ int32_t c4_plan(const C4AttnArgs& A, C4Plan& P) {
   return per;
 }
 
-// Pages of each workgroup's range: an equal share, at least one page per wave.
-__device__ __forceinline__ int64_t c4_share(int64_t pages, int32_t grid) {
-  const int64_t s = (pages + grid - 1) / grid;
-  return s < 4 ? 4 : s;
+// A value from LDS that all lanes share, as a scalar.
+__device__ __forceinline__ int64_t c4_lanes_same(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int32_t)(x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// The weight of each workgroup's range: an equal share, at least one page per
+// wave and a segment's cost.
+__device__ __forceinline__ int64_t c4_share(int64_t weight) {
+  const int64_t s = (weight + kC4Grid - 1) / kC4Grid;
+  return s < 4 + kC4SegCost ? 4 + kC4SegCost : s;
+}
+// Page of a segment of `pages` at which weight `x` from its begin lies.
+__device__ __forceinline__ int32_t c4_cut(int64_t x, int32_t pages) {
+  x -= kC4SegCost;
+  return x <= 0 ? 0 : (x >= pages ? pages : (int32_t)x);
 }
 
 template <int D, int RT>
@@ -362,40 +411,36 @@ __device__ __forceinline__ float c4_sum_quads(float x) {
 constexpr float kC4Low = -3.0e38f;  // a maximum before any score
 constexpr float kC4Raise = 8.0f;    // a score passes the maximum by 2^8 before it is raised
 
-// What a row's new token sees of the 64 positions from `base` on (relative to
+// What a row's new token sees of the 32 positions from `base` on (relative to
 // start): bit x for position base + x.
-__device__ __forceinline__ uint64_t c4_sees(const C4AttnArgs& A, int64_t b, int32_t i, int32_t n,
+__device__ __forceinline__ uint32_t c4_sees(const C4AttnArgs& A, int64_t b, int32_t i, int32_t n,
                                             int64_t base) {
   if (i >= n) return 0;
   if (!A.mask) {
     const int64_t seen = (int64_t)i + 1 - base;  // positions below base + seen
-    return seen <= 0 ? 0 : (seen >= 64 ? ~0ull : (1ull << seen) - 1);
+    return seen <= 0 ? 0 : (seen >= 32 ? ~0u : (1u << seen) - 1u);
   }
   const uint32_t* row = A.mask + b * A.mask_seq + i * A.mask_pos;
   const int32_t words = (A.T + 31) / 32;
-  auto word = [&](int64_t k) -> uint64_t {
-    if (k < 0) return 0xFFFFFFFFull;      // cached tokens
+  auto word = [&](int64_t k) -> uint32_t {
+    if (k < 0) return ~0u;                // cached tokens
     if (k >= words) return 0;
-    uint32_t w = row[k];
     const int64_t left = n - 32 * k;      // new tokens of this word
-    if (left < 32) w &= left <= 0 ? 0u : (1u << left) - 1u;
-    return w;
+    return left >= 32 ? row[k] : row[k] & (left <= 0 ? 0u : (1u << left) - 1u);
   };
-  const int64_t k0 = base >> 5;           // floor: base may be negative
+  const int64_t k = base >> 5;            // floor: base may be negative
   const int sh = (int)(base & 31);
-  const uint64_t lo = word(k0) | (word(k0 + 1) << 32);
-  return sh == 0 ? lo : (lo >> sh) | (word(k0 + 2) << (64 - sh));
+  return sh == 0 ? word(k) : (word(k) >> sh) | (word(k + 1) << (32 - sh));
 }
 
-// The codes and exponents of one page in a lane's registers.
+// The codes and exponents of a pair of 16-token tiles in a lane's registers.
 template <int D>
-struct C4PageRegs {
-  static constexpr int NG = C4<D>::NG;
-  static constexpr int KW = D / 32;            // dwords of key codes per tile
-  uint32_t k[4][KW];                           // 4 tiles: D / 8 bytes of one token
-  uint32_t v[4][D / 32];                       // 4 tiles: 4 tokens x D / 32 bytes
-  uint32_t ke[D == 256 ? 2 : 1];               // byte `tile`: this lane's token
-  uint32_t ve[4];                              // byte j: token 4 q + j of the tile
+struct C4Unit {
+  static constexpr int W = D / 32;    // dwords of codes per tile, keys and values each
+  uint32_t k[2][W];                   // D / 4 elements of one token
+  uint32_t v[2][W];                   // 4 tokens x D / 16 elements
+  uint32_t ke[D == 256 ? 2 : 1];      // byte `tile`: this lane's token
+  uint32_t ve[2];                     // byte j: token 4 q + j of the tile
 };
 
 template <int N>
@@ -412,23 +457,6 @@ __device__ __forceinline__ void c4_load_words(const uint8_t* p, uint32_t* out) {
   }
 }
 
-template <int D>
-__device__ __forceinline__ void c4_load_page(const uint8_t* rec, int lane, C4PageRegs<D>& R) {
-  constexpr int NG = C4<D>::NG;
-  const int n = lane & 15, q = lane >> 4;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    c4_load_words<D / 32>(rec + (16 * t + n) * (D / 2) + q * (D / 8), R.k[t]);
-    c4_load_words<D / 32>(rec + C4<D>::kVal + (t * 64 + lane) * (D / 8), R.v[t]);
-    R.ve[t] = *reinterpret_cast<const uint32_t*>(rec + C4<D>::kValExp + (4 * t + q) * (4 * NG) +
-                                                 (n * NG / 16) * 4);
-  }
-  const int g = q * NG / 4;
-  R.ke[0] = *reinterpret_cast<const uint32_t*>(rec + C4<D>::kKeyExp + g * 64 + n * 4);
-  if constexpr (D == 256)
-    R.ke[1] = *reinterpret_cast<const uint32_t*>(rec + C4<D>::kKeyExp + (g + 1) * 64 + n * 4);
-}
-
 __device__ __forceinline__ uint32_t c4_cvt(uint32_t w, float scale, int byte) {
   // the byte select is an immediate; `byte` is constant at every call
   switch (byte) {
@@ -439,9 +467,11 @@ __device__ __forceinline__ uint32_t c4_cvt(uint32_t w, float scale, int byte) {
   }
 }
 
-// Scale 2^(e - 127) of exponent byte `i` of w; 255 stands for NaN.
+// A conversion's scale operand with exponent byte `i` of w as its exponent
+// field: 2^(e - 127), 255 for NaN.  The conversions take nothing but that
+// field, so the other bytes may stand around it: one shift.
 __device__ __forceinline__ float c4_byte_scale(uint32_t w, int i) {
-  return __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
+  return __uint_as_float(i < 3 ? w << (23 - 8 * i) : w >> 1);
 }
 
 template <int D, int RT>
@@ -450,138 +480,134 @@ struct C4State {
   float m[RT], l[RT];
 };
 
-// One page.  MASKED: some of its positions are not seen by some row (sees[]:
-// this lane's rows; `valid`: positions that hold tokens, as bits).
-template <int D, int RT, bool MASKED>
-__device__ __forceinline__ void c4_page(const C4PageRegs<D>& R, const c4_bf16x8 (&qf)[RT][D / 32],
-                                        C4State<D, RT>& S, float c, int lane,
-                                        const uint64_t (&sees)[RT], uint64_t valid) {
+// One pair of tiles.  masked (of the wave): some of its 32 positions are not
+// seen by some row; sees[] then has this lane's rows' bits, and `valid` those
+// of the positions that hold tokens.  q_of(rt, j): the rows' operand.
+template <int D, int RT, typename Q>
+__device__ __forceinline__ void c4_unit(C4Unit<D>& R, Q q_of, C4State<D, RT>& S, float c, int lane,
+                                        bool masked, const uint32_t (&sees)[RT], uint32_t valid) {
   const int q = lane >> 4;
-  c4_f32x4 s[RT][4];
+  if (masked) {  // what stands past the last token is not a value: zeros with an exponent of 1
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) s[rt][t] = c4_f32x4{0.f, 0.f, 0.f, 0.f};
-    float scale[D == 256 ? 2 : 1];
-    scale[0] = c4_byte_scale(R.ke[0], t);
-    if constexpr (D == 256) scale[1] = c4_byte_scale(R.ke[1], t);
+      for (int j = 0; j < 4; ++j)
+        if (!((valid >> (16 * i + 4 * q + j)) & 1)) {
+          R.ve[i] = (R.ve[i] & ~(0xFFu << (8 * j))) | (127u << (8 * j));
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
+          for (int x = 0; x < (D + 127) / 128; ++x) {
+            // token j's D / 32 bytes of this lane's codes
+            if constexpr (D == 64) R.v[i][j / 2] &= j % 2 ? 0xFFFFu : 0xFFFF0000u;
+            else R.v[i][D / 128 * j + x] = 0u;
+          }
+        }
+  }
+  c4_f32x4 s[RT][2];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s[rt][i] = c4_f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < D / 32; ++j) {
+    c4_bf16x8 kf[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float sc = c4_byte_scale(R.ke[D == 256 ? j / 4 : 0], i);
       uint4 a;
-      const float sc = scale[D == 256 ? j / 4 : 0];
-      a.x = c4_cvt(R.k[t][j], sc, 0);
-      a.y = c4_cvt(R.k[t][j], sc, 1);
-      a.z = c4_cvt(R.k[t][j], sc, 2);
-      a.w = c4_cvt(R.k[t][j], sc, 3);
-      const c4_bf16x8 kf = __builtin_bit_cast(c4_bf16x8, a);
+      a.x = c4_cvt(R.k[i][j], sc, 0);
+      a.y = c4_cvt(R.k[i][j], sc, 1);
+      a.z = c4_cvt(R.k[i][j], sc, 2);
+      a.w = c4_cvt(R.k[i][j], sc, 3);
+      kf[i] = __builtin_bit_cast(c4_bf16x8, a);
+    }
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        s[rt][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[rt][j], s[rt][t], 0, 0, 0);
+    for (int rt = 0; rt < RT; ++rt) {
+      const c4_bf16x8 qf = q_of(rt, j);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        s[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], qf, s[rt][i], 0, 0, 0);
     }
   }
-  uint4 p[RT][2];  // P' of tile pairs, the B operands
+  c4_bf16x8 p[RT];  // P' of the pair, the second product's operand
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
-    if constexpr (MASKED) {
-      const uint64_t mine = sees[rt] >> (4 * q);
+    if (masked) {
+      const uint32_t mine = sees[rt] >> (4 * q);
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (!((mine >> (16 * t + r)) & 1)) s[rt][t][r] = -__builtin_inff();
+          if (!((mine >> (16 * i + r)) & 1)) s[rt][i][r] = -__builtin_inff();
     }
     float top = fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3]));
 #pragma unroll
-    for (int t = 1; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) top = fmaxf(top, s[rt][t][r]);
-    top = c4_max_quads(top) * c;
-    if (__any(top > S.m[rt] + kC4Raise)) {
-      const float m = fmaxf(S.m[rt], top);
+    for (int r = 0; r < 4; ++r) top = fmaxf(top, s[rt][1][r]);
+    if (__any(top * c > S.m[rt] + kC4Raise)) {  // rare: the lanes of a row agree on it here
+      const float m = fmaxf(S.m[rt], c4_max_quads(top) * c);
       const float f = __builtin_amdgcn_exp2f(S.m[rt] - m);
       S.m[rt] = m;
       S.l[rt] *= f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) S.o[rt][i] *= f;
     }
-    float e[4][4];
     float sum = 0.f;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        e[t][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][t][r], c, -S.m[rt]));
-        sum += e[t][r];
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i][r], c, -S.m[rt]));
+        sum += e;
+        p[rt][4 * i + r] = (__bf16)e;
       }
     S.l[rt] += sum;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      c4_bf16x8 x;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[r] = (__bf16)e[2 * h][r];
-        x[4 + r] = (__bf16)e[2 * h + 1][r];
-      }
-      p[rt][h] = __builtin_bit_cast(uint4, x);
-    }
   }
-  // V' of a tile pair: byte y of token j's codes gives that token's values of
-  // two neighbouring d; tokens are paired for each d by a byte permutation
+  // V' of the pair: byte y of token j's codes gives that token's values of two
+  // neighbouring d; tokens are paired for each d by a byte permutation
   constexpr int NB = D / 32;  // bytes of a lane's codes of one token
+  float sc[2][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int y = 0; y < NB; ++y) {
-      uint32_t a[2][4];  // [tile of the pair][token]: bf16 of d = 2 y, 2 y + 1
+    for (int j = 0; j < 4; ++j) sc[i][j] = c4_byte_scale(R.ve[i], j);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+  for (int y = 0; y < NB; ++y) {
+    uint32_t a[2][4];  // [tile][token]: bf16 of d = 2 y, 2 y + 1
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t w = R.v[2 * h + t][(j * NB + y) / 4];
-          float sc = c4_byte_scale(R.ve[2 * h + t], j);
-          if constexpr (MASKED) {  // what stands past the last token is not a value
-            const bool have = (valid >> (16 * (2 * h + t) + 4 * q + j)) & 1;
-            w = have ? w : 0u;
-            sc = have ? sc : 1.0f;
-          }
-          a[t][j] = c4_cvt(w, sc, (j * NB + y) % 4);
-        }
-      uint4 lo, hi;
-      lo.x = __builtin_amdgcn_perm(a[0][1], a[0][0], 0x05040100u);
-      lo.y = __builtin_amdgcn_perm(a[0][3], a[0][2], 0x05040100u);
-      lo.z = __builtin_amdgcn_perm(a[1][1], a[1][0], 0x05040100u);
-      lo.w = __builtin_amdgcn_perm(a[1][3], a[1][2], 0x05040100u);
-      hi.x = __builtin_amdgcn_perm(a[0][1], a[0][0], 0x07060302u);
-      hi.y = __builtin_amdgcn_perm(a[0][3], a[0][2], 0x07060302u);
-      hi.z = __builtin_amdgcn_perm(a[1][1], a[1][0], 0x07060302u);
-      hi.w = __builtin_amdgcn_perm(a[1][3], a[1][2], 0x07060302u);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const c4_bf16x8 pf = __builtin_bit_cast(c4_bf16x8, p[rt][h]);
-        S.o[rt][2 * y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(c4_bf16x8, lo), pf, S.o[rt][2 * y], 0, 0, 0);
-        S.o[rt][2 * y + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(c4_bf16x8, hi), pf, S.o[rt][2 * y + 1], 0, 0, 0);
+      for (int j = 0; j < 4; ++j) {
+        a[i][j] = c4_cvt(R.v[i][(j * NB + y) / 4], sc[i][j], (j * NB + y) % 4);
       }
+    uint4 lo, hi;
+    lo.x = __builtin_amdgcn_perm(a[0][1], a[0][0], 0x05040100u);
+    lo.y = __builtin_amdgcn_perm(a[0][3], a[0][2], 0x05040100u);
+    lo.z = __builtin_amdgcn_perm(a[1][1], a[1][0], 0x05040100u);
+    lo.w = __builtin_amdgcn_perm(a[1][3], a[1][2], 0x05040100u);
+    hi.x = __builtin_amdgcn_perm(a[0][1], a[0][0], 0x07060302u);
+    hi.y = __builtin_amdgcn_perm(a[0][3], a[0][2], 0x07060302u);
+    hi.z = __builtin_amdgcn_perm(a[1][1], a[1][0], 0x07060302u);
+    hi.w = __builtin_amdgcn_perm(a[1][3], a[1][2], 0x07060302u);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      S.o[rt][2 * y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(c4_bf16x8, lo), p[rt], S.o[rt][2 * y], 0, 0, 0);
+      S.o[rt][2 * y + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(c4_bf16x8, hi), p[rt], S.o[rt][2 * y + 1], 0, 0, 0);
     }
   }
 }
 
-// Eight output values of a row as bf16.
-__device__ __forceinline__ void c4_store8(uint16_t* p, const float* x) {
-  c4_bf16x8 y;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = (__bf16)x[i];
-  *reinterpret_cast<uint4*>(p) = __builtin_bit_cast(uint4, y);
-}
-
-// Writes a finished row's eighth-of-... values: normalised, or NaN.
-__device__ __forceinline__ void c4_finish8(const C4AttnArgs& A, int64_t b, int32_t i, int32_t head,
-                                           int d0, float* x, float m, float l) {
+// Writes N values of a finished row, normalised, or NaN; with the first ones
+// the row's lse.
+template <int N>
+__device__ __forceinline__ void c4_finish(const C4AttnArgs& A, int64_t b, int32_t i, int32_t head,
+                                          int d0, const float* x, float m, float l) {
   const float inv = l == 0.f ? 0.f : 1.0f / l;  // a NaN sum stays NaN
+  typedef __bf16 Out __attribute__((ext_vector_type(N)));
+  Out y;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= inv;
-  c4_store8(A.out + b * A.o_seq + i * A.o_pos + head * A.o_head + d0, x);
+  for (int e = 0; e < N; ++e) y[e] = (__bf16)(x[e] * inv);
+  *reinterpret_cast<Out*>(A.out + b * A.o_seq + i * A.o_pos + head * A.o_head + d0) = y;
   if (d0 == 0 && A.lse) {
     constexpr float kLn2 = 0.6931471805599453f;
     const int64_t at = (b * A.T + i) * ((int64_t)A.G * A.cache.heads) + head;
@@ -589,58 +615,179 @@ __device__ __forceinline__ void c4_finish8(const C4AttnArgs& A, int64_t b, int32
   }
 }
 
+// How the cached pages come: each wave fills two LDS buffers of its own with
+// pairs of tiles, straight from memory (buffer_load ... lds), and takes them out
+// in the order it put them in.  Nothing is shared, so the only wait is the
+// wave's own, and what is on its way costs no registers, which belong to the
+// accumulators.  A buffer holds kPairs pairs of 4.75 KiB (at D = 128): with 8
+// waves a CU 70 KiB or more are in flight, while the code of a pair, which the
+// instruction cache has to bring at every launch, stands twice and no more.
 template <int D, int RT>
-__global__ __launch_bounds__(256) void k_attention_cache4(C4AttnArgs A) {
-  constexpr int kRows = RT * 16;
-  constexpr int kPad = D + 4;  // an LDS row of O: the 16 rows of a tile on different banks
-  __shared__ C4Plan plan;
-  __shared__ float oacc[4][16 * kPad];
+struct C4Shape {
+  // whether the rows' operand stays in registers (else LDS, read per pair)
+  static constexpr bool kQRegs = D * RT <= 256;
+  static constexpr int kPairs = D * RT <= 256 && D <= 128 ? 2 : 1;
+  static constexpr int kCodes = 2 * 16 * D / 2;        // bytes of a pair's keys, or values
+  static constexpr int kKeyExps = (D == 256 ? 2 : 1) * 256;
+  static constexpr int kUnit = 2 * kCodes + kKeyExps + 512;
+  static constexpr int kBuf = kPairs * kUnit;           // a wave's part of a buffer
+  // memory instructions of a pair
+  static constexpr int kLoads = 2 * kCodes / 1024 + kKeyExps / 256 + 2;
+  static constexpr int kWaves = D == 256 && RT == 2 ? 1 : 2;  // a SIMD's
+};
+
+// Starts the loads of pair `half` of the record into `to`.
+template <int D>
+__device__ __forceinline__ void c4_fetch(const uint8_t* rec, int half, int lane, uint8_t* to) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host's pass does not know the buffer resource's type
+  constexpr int NG = C4<D>::NG, kCodes = 16 * D;
+  typedef __attribute__((address_space(3))) void* Lds;
+  const int n = lane & 15, q = lane >> 4;
+  const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(rec), 0, C4<D>::kRecord, 0x00020000);
+  // D = 64: as the bytes stand; else 16 bytes a lane, the ones it will take
+  const int ko = D == 64 ? lane * 16 : n * (D / 2) + q * (D / 8);
+  const int vo = C4<D>::kVal + (D == 64 ? lane * 16 : lane * (D / 8));
+  constexpr int kTiles = D == 64 ? 1 : 2, kParts = D == 256 ? 2 : 1;
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int x = 0; x < kParts; ++x) {
+      const int at = (i * kParts + x) * 1024;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (Lds)(to + at), 16, ko, (2 * half + i) * (8 * D) + 16 * x, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (Lds)(to + kCodes + at), 16, vo,
+                                               (2 * half + i) * (8 * D) + 16 * x, 0, 0);
+    }
+  uint8_t* ex = to + 2 * kCodes;
+#pragma unroll
+  for (int x = 0; x < kParts; ++x)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (Lds)(ex + 256 * x), 4,
+                                             C4<D>::kKeyExp + (q * NG / 4) * 64 + n * 4, 64 * x, 0, 0);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (Lds)(ex + 256 * (kParts + i)), 4,
+                                             C4<D>::kValExp + q * (4 * NG) + (n * NG / 16) * 4,
+                                             (2 * half + i) * (16 * NG), 0, 0);
+#endif
+}
+
+// Takes pair `half` of a page out of its buffer.
+template <int D>
+__device__ __forceinline__ void c4_take(const uint8_t* from, int half, int lane, C4Unit<D>& R) {
+  constexpr int kCodes = 16 * D, kParts = D == 256 ? 2 : 1;
+  const int n = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (D == 64) {
+      c4_load_words<2>(from + (16 * i + n) * 32 + q * 8, R.k[i]);
+      c4_load_words<2>(from + kCodes + i * 512 + lane * 8, R.v[i]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < kParts; ++x) {
+        const int at = (i * kParts + x) * 1024 + lane * 16;
+        c4_load_words<4>(from + at, R.k[i] + 4 * x);
+        c4_load_words<4>(from + kCodes + at, R.v[i] + 4 * x);
+      }
+    }
+    R.ve[i] = *reinterpret_cast<const uint32_t*>(from + 2 * kCodes + 256 * (kParts + i) + lane * 4);
+  }
+#pragma unroll
+  for (int x = 0; x < kParts; ++x)
+    R.ke[x] = *reinterpret_cast<const uint32_t*>(from + 2 * kCodes + 256 * x + lane * 4) >> (16 * half);
+}
+
+template <int D, int RT>
+__global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cache4(C4AttnArgs A) {
+  using Sh = C4Shape<D, RT>;
+  constexpr int kRows = RT * 16, N = Sh::kPairs;
+  // Two arrays, each named where it is used, so that the compiler does not wait
+  // for the other's loads when it reads one.
+  __shared__ __attribute__((aligned(16))) uint8_t ring0[4 * Sh::kBuf], ring1[4 * Sh::kBuf];
+  __shared__ uint4 qs[Sh::kQRegs ? 1 : RT][Sh::kQRegs ? 1 : D / 32][Sh::kQRegs ? 1 : 64];
   __shared__ float ms[4][kRows], ls[4][kRows];
+  // Between segments the buffers hold the plan, or O of 16 rows x kCols columns
+  // of each wave, in turn.
+  constexpr int kCols = D == 64 ? 64 : N == 2 ? 128 : 64, kPad = kCols + 4, kRun = kCols / 16;
+  static_assert(sizeof(C4Plan) <= sizeof(ring0) && 4 * 16 * kPad * 4 <= sizeof(ring0), "room");
+  C4Plan& plan = *reinterpret_cast<C4Plan*>(ring0);
+
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, q = lane >> 4;
   const int32_t per = c4_plan(A, plan);
   const int64_t HR = (int64_t)A.cache.heads * A.row_blocks;
-  const int64_t share = c4_share(plan.total * HR, A.grid);
+  const int64_t all = c4_lanes_same(plan.total) * HR;  // weight of all segments
+  const int64_t share = c4_share(all);
   const int64_t lo = (int64_t)blockIdx.x * share;
-  const int64_t hi = min(lo + share, plan.total * HR);
-  if (lo >= hi) return;
+  const int64_t hi = min(lo + share, all);
+  int32_t cut_b = 0, cut_hr = 0, cut_new = 0, cut_parts = 0, cut_slot = 0;
+  auto note = [&] {
+    if (A.split && tid == 0) A.cuts[blockIdx.x] = {cut_b, cut_hr, cut_new, cut_parts, cut_slot, {0, 0, 0}};
+  };
+  if (lo >= hi) {
+    note();
+    return;
+  }
 
-  // the sequence of page `lo`: its thread's run of sequences, then within it
-  int64_t b = 0, seq_at = 0;  // seq_at: pages before b, over all heads and row blocks
-  {
-    int t0 = 0, t1 = 255;
-    while (t0 < t1) {  // last thread whose first page is at or before lo
-      const int mid = (t0 + t1 + 1) / 2;
-      if (plan.before[mid] * HR <= lo) t0 = mid;
-      else t1 = mid - 1;
-    }
+  // the sequence of weight `lo`: its thread's run of sequences, then within it
+  int64_t b = 0, seq_at = 0;  // seq_at: weight before b
+  if (A.B > 1) {
+    int t0 = 0;  // the last thread whose first sequence is at or before lo
+#pragma unroll
+    for (int step = 128; step; step >>= 1)
+      if (plan.before[t0 + step] * HR <= lo) t0 += step;
+    t0 = __builtin_amdgcn_readfirstlane(t0);
     b = (int64_t)t0 * per;
-    seq_at = plan.before[t0] * HR;
+    seq_at = c4_lanes_same(plan.before[t0]) * HR;
   }
+  __syncthreads();  // the plan is read: its buffer is free
   bool bad;
-  int32_t pages = c4_pages(A, b, bad);
-  while (seq_at + pages * HR <= lo) {
-    seq_at += pages * HR;
-    pages = c4_pages(A, ++b, bad);
+  int32_t pages = c4_pages<true>(A, b, bad);
+  while (seq_at + c4_weight(pages) * HR <= lo) {
+    seq_at += c4_weight(pages) * HR;
+    pages = c4_pages<true>(A, ++b, bad);
   }
-  int64_t at = lo;
+  // its segment of that weight, and where that begins
+  int32_t hr = (int32_t)((lo - seq_at) / c4_weight(pages));
+  int64_t seg = seq_at + hr * c4_weight(pages);
   const int32_t R = A.T * A.G;
-  while (at < hi) {
-    if (at >= seq_at + pages * HR) {  // the next sequence with pages
-      do {
-        seq_at += pages * HR;
-        pages = c4_pages(A, ++b, bad);
-      } while (pages == 0);
+  for (; seg < hi; seg += c4_weight(pages), ++hr) {
+    if (hr == HR) {  // the next sequence with pages (seg is its begin)
+      do pages = c4_pages<true>(A, ++b, bad);
+      while (pages == 0);
+      hr = 0;
     }
-    const int64_t hr = (at - seq_at) / pages;
-    const int64_t seg = seq_at + hr * pages;  // the segment's first page
-    const int32_t p0 = (int32_t)(at - seg);
-    const int32_t p1 = (int32_t)min((int64_t)pages, hi - seg);
-    at = seg + p1;
-    const int32_t h = (int32_t)(hr / A.row_blocks), r0 = (int32_t)(hr % A.row_blocks) * kRows;
-    const int32_t s0 = A.start[b], nnew = bad ? A.T : (A.count ? A.count[b] : A.T);
+    int32_t p0 = c4_cut(lo - seg, pages), p1 = c4_cut(hi - seg, pages);
+    if (!A.split) p0 = 0, p1 = seg < lo ? 0 : pages;  // whole, where it begins
+    if (p0 == p1) continue;  // its pages are another workgroup's
+    const int32_t h = hr / A.row_blocks, r0 = hr % A.row_blocks * kRows;
+    const int32_t s0 = c4_scalar(A.start + b);
+    const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
+    if (p0 == 0 && p1 < pages) {
+      cut_b = (int32_t)b, cut_hr = hr, cut_new = nnew, cut_slot = seg > lo ? 1 : 0;
+      cut_parts = (int32_t)((seg + kC4SegCost + pages - 1) / share - blockIdx.x + 1);
+    }
 
-    c4_bf16x8 qf[RT][D / 32];
+    // The waves take the segment's pairs of tiles in turn, so that a wave's are
+    // all first or all second ones of their pages.  A page outside the pool
+    // stands for page 0 and marks the rows.
+    bool faulty = bad;
+    const int half = w & 1;
+    const int32_t end = bad ? p0 : p1, pw = p0 + (w >> 1);  // this wave's pages: pw, pw + 2, ..
+    int32_t nu = end > pw ? (end - pw + 1) / 2 : 0;
+    // the last page may hold no token in its second half
+    if (nu && (pw + 2 * (nu - 1)) * (int64_t)kC4Page + 32 * half >= (int64_t)s0 + nnew) --nu;
+    auto page_of = [&](int32_t u) { return u < nu ? c4_scalar(A.cache.table + b * A.cache.table_stride + pw + 2 * u) : 0; };
+    auto fetch = [&](int32_t page, uint8_t* buf, int k) {
+      if ((uint32_t)page >= (uint32_t)A.cache.n_pages) {
+        faulty = true;
+        page = 0;
+      }
+      c4_fetch<D>(A.cache.record<D>(page, h), half, lane, buf + w * Sh::kBuf + k * Sh::kUnit);
+    };
+    int32_t first[2 * N];  // all on their way before the first is needed
+#pragma unroll
+    for (int k = 0; k < 2 * N; ++k) first[k] = page_of(k);
+
+    c4_bf16x8 qf[Sh::kQRegs ? RT : 1][D / 32];
     int32_t tok[RT];  // this lane's rows' tokens; T past the last row
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -651,10 +798,20 @@ __global__ __launch_bounds__(256) void k_attention_cache4(C4AttnArgs A) {
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R && i < nnew) x = load16(qp + q * (D / 4) + 8 * j);
-        qf[rt][j] = __builtin_bit_cast(c4_bf16x8, x);
+        if (r < R && i < nnew && (Sh::kQRegs || j % 4 == w)) x = load16(qp + q * (D / 4) + 8 * j);
+        if constexpr (Sh::kQRegs) qf[rt][j] = __builtin_bit_cast(c4_bf16x8, x);
+        else if (j % 4 == w) qs[rt][j][lane] = x;
       }
     }
+#pragma unroll
+    for (int k = 0; k < 2 * N; ++k)
+      if (k < nu) fetch(first[k], k < N ? ring0 : ring1, k % N);
+    int32_t ahead = page_of(2 * N);  // the page of the next fetch
+    if constexpr (!Sh::kQRegs) __syncthreads();
+    auto q_of = [&](int rt, int j) {
+      if constexpr (Sh::kQRegs) return qf[rt][j];
+      else return __builtin_bit_cast(c4_bf16x8, qs[rt][j][lane]);
+    };
     C4State<D, RT> S;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -663,34 +820,46 @@ __global__ __launch_bounds__(256) void k_attention_cache4(C4AttnArgs A) {
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) S.o[rt][i] = c4_f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    bool faulty = bad;
-    if (!bad) {
-      for (int32_t p = p0 + w; p < p1; p += 4) {
-        const int32_t page = A.cache.page(b, p);
-        if (page < 0) {
-          faulty = true;
-          continue;
-        }
-        C4PageRegs<D> regs;
-        c4_load_page<D>(A.cache.record<D>(page, h), lane, regs);
-        const int64_t base = (int64_t)p * kC4Page - s0;
-        uint64_t sees[RT];
-        if (base + kC4Page <= 0) {
-          c4_page<D, RT, false>(regs, qf, S, A.c, lane, sees, ~0ull);
-        } else {
+    // the pairs u .. u + N - 1 of one buffer
+    auto work = [&](int32_t u, uint8_t* buf) {
+#pragma unroll 1
+      for (int k = 0; k < N; ++k, ++u) {
+        if (u >= nu) return;
+        // this pair has arrived when no more than the later ones' loads are left
+        // (loads return in order)
+        if (u + 2 * N - 1 < nu) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((2 * N - 1) * Sh::kLoads) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        C4Unit<D> U;
+        c4_take<D>(buf + w * Sh::kBuf + k * Sh::kUnit, half, lane, U);
+        // the first of its positions relative to the new tokens'
+        const int64_t base = (int64_t)(pw + 2 * u) * kC4Page + 32 * half - s0;
+        const bool masked = base + 32 > 0;
+        uint32_t sees[RT] = {}, valid = 0;
+        if (masked) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) sees[rt] = c4_sees(A, b, tok[rt], nnew, base);
-          const int64_t have = nnew - base;  // tokens of this page
-          const uint64_t valid = have >= 64 ? ~0ull : (1ull << have) - 1;
-          c4_page<D, RT, true>(regs, qf, S, A.c, lane, sees, valid);
+          const int64_t have = nnew - base;
+          valid = have >= 32 ? ~0u : (1u << have) - 1u;
+        }
+        c4_unit<D, RT>(U, q_of, S, A.c, lane, masked, sees, valid);
+        if (u + 2 * N < nu) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the buffer has been taken out
+          fetch(ahead, buf, k);
+          ahead = page_of(u + 2 * N + 1);
         }
       }
+    };
+    for (int32_t u = 0; u < nu; u += 2 * N) {
+      work(u, ring0);
+      work(u + N, ring1);
     }
     if (faulty) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) S.l[rt] = __builtin_nanf("");
     }
-    // the four waves' rows together
+    // The four waves' rows together, a tile of 16 rows x kCols columns at a
+    // time: column group 4 q + y of a lane holds D / 16 columns, of which a run
+    // of kRun goes each time.
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const float l = c4_sum_quads(S.l[rt]);
@@ -699,94 +868,150 @@ __global__ __launch_bounds__(256) void k_attention_cache4(C4AttnArgs A) {
         ls[w][16 * rt + n16] = l;
       }
     }
-    __syncthreads();
+    __syncthreads();  // also: every wave has emptied its buffers
     const bool whole = p0 == 0 && p1 == pages;
     float* part = A.parts + ((int64_t)blockIdx.x * 2 + (seg > lo ? 1 : 0)) * C4Rec<D, RT>::kFloats;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int row = 16 * rt + n16;
+      const int mine = 16 * rt + n16;
+      const float f = __builtin_amdgcn_exp2f(
+          S.m[rt] - fmaxf(fmaxf(ms[0][mine], ms[1][mine]), fmaxf(ms[2][mine], ms[3][mine])));
+      const int rr = tid >> 4, row = 16 * rt + rr;  // this thread's row of the sums
       const float top = fmaxf(fmaxf(ms[0][row], ms[1][row]), fmaxf(ms[2][row], ms[3][row]));
-      const float f = __builtin_amdgcn_exp2f(S.m[rt] - top);
+      float l = 0.f;
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int x = 0; x < 4; ++x) l += ls[x][row] * __builtin_amdgcn_exp2f(ms[x][row] - top);
+      const int32_t r = r0 + row, i = r / A.G, head = h * A.G + (r - i * A.G);
+      const bool live = whole && r < R && i < nnew;
 #pragma unroll
-        for (int i = 0; i < D / 16; i += 4)
-          *reinterpret_cast<float4*>(&oacc[w][n16 * kPad + (4 * q + r) * (D / 16) + i]) =
-              make_float4(S.o[rt][i][r] * f, S.o[rt][i + 1][r] * f, S.o[rt][i + 2][r] * f,
-                          S.o[rt][i + 3][r] * f);
-      __syncthreads();
-      // 16 rows x D: eight values of a row per step
-      for (int x = tid; x < 2 * D; x += 256) {
-        const int rr = x / (D / 8), d0 = (x % (D / 8)) * 8;
-        const int row2 = 16 * rt + rr;
-        float v[8] = {};
+      for (int x = 0; x < D / kCols; ++x) {
+        // the buffers in turn: one barrier a time
+        float* const oacc = reinterpret_cast<float*>((rt * (D / kCols) + x) & 1 ? ring1 : ring0);
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+          for (int e = 0; e < kRun; e += 4)
+            *reinterpret_cast<float4*>(&oacc[(w * 16 + n16) * kPad + (4 * q + y) * kRun + e]) =
+                make_float4(S.o[rt][x * kRun + e][y] * f, S.o[rt][x * kRun + e + 1][y] * f,
+                            S.o[rt][x * kRun + e + 2][y] * f, S.o[rt][x * kRun + e + 3][y] * f);
+        __syncthreads();
+        const int grp = tid & 15, d0 = grp * (D / 16) + x * kRun;
+        float v[kRun] = {};
 #pragma unroll
         for (int ww = 0; ww < 4; ++ww)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += oacc[ww][rr * kPad + d0 + e];
-        const float mt = fmaxf(fmaxf(ms[0][row2], ms[1][row2]), fmaxf(ms[2][row2], ms[3][row2]));
-        float l = 0.f;
+          for (int e = 0; e < kRun; ++e) v[e] += oacc[(ww * 16 + rr) * kPad + grp * kRun + e];
+        if (live) {
+          c4_finish<kRun>(A, b, i, head, d0, v, top, l);
+        } else if (!whole) {
 #pragma unroll
-        for (int ww = 0; ww < 4; ++ww) l += ls[ww][row2] * __builtin_amdgcn_exp2f(ms[ww][row2] - mt);
-        if (whole) {
-          const int32_t r = r0 + row2, i = r / A.G;
-          if (r < R && i < nnew)
-            c4_finish8(A, b, i, h * A.G + (r - i * A.G), d0, v, mt, l);
-        } else {
-          float4* dst = reinterpret_cast<float4*>(part + row2 * D + d0);
-          dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+          for (int e = 0; e < kRun; ++e) part[row * D + d0 + e] = v[e];
           if (d0 == 0) {
-            part[kRows * D + row2] = mt;
-            part[kRows * D + kRows + row2] = l;
+            part[kRows * D + row] = top;
+            part[kRows * D + kRows + row] = l;
           }
         }
       }
-      __syncthreads();
     }
+    __syncthreads();  // the buffers, ms and ls are free
+  }
+  note();
+}
+
+// Joins each cut segment's records, in order.  A workgroup takes four rows: of
+// a segment in few records a wave each, else every wave all four rows of a
+// quarter of the records, so that enough loads are under way.
+template <int D, int ROWS, int N>
+__device__ __forceinline__ void c4_gather(const float* first, const float* rest, int64_t floats, int rows,
+                                          int row, int32_t x0, int32_t x1, int lane, float (&m)[ROWS],
+                                          float (&l)[ROWS], float (&v)[ROWS][D / 64]) {
+  constexpr int E = D / 64;
+#pragma unroll
+  for (int y = 0; y < ROWS; ++y) {
+    m[y] = kC4Low;
+    l[y] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[y][e] = 0.f;
+  }
+  for (int32_t base = x0; base < x1; base += N) {
+    float pm[N][ROWS], pl[N][ROWS], o[N][ROWS][E];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int32_t x = min(base + k, x1 - 1);
+      const float* p = x == 0 ? first : rest + x * floats;
+#pragma unroll
+      for (int y = 0; y < ROWS; ++y) {
+        pm[k][y] = p[rows * D + row + y];
+        pl[k][y] = p[rows * D + rows + row + y];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[k][y][e] = p[(row + y) * D + lane * E + e];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (base + k < x1) {
+#pragma unroll
+        for (int y = 0; y < ROWS; ++y) {
+          const float top = fmaxf(m[y], pm[k][y]);
+          const float f = __builtin_amdgcn_exp2f(m[y] - top), g = __builtin_amdgcn_exp2f(pm[k][y] - top);
+          m[y] = top;
+          l[y] = l[y] * f + pl[k][y] * g;
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[y][e] = v[y][e] * f + o[k][y][e] * g;
+        }
+      }
   }
 }
 
-// Joins the cut segments of each (sequence, kv head, block of rows), in order.
 template <int D, int RT>
 __global__ __launch_bounds__(256) void k_attention_cache4_join(C4AttnArgs A) {
-  constexpr int kRows = RT * 16, kFloats = C4Rec<D, RT>::kFloats;
-  __shared__ C4Plan plan;
-  const int tid = threadIdx.x;
-  const int32_t per = c4_plan(A, plan);
-  const int64_t HR = (int64_t)A.cache.heads * A.row_blocks;
-  const int64_t share = c4_share(plan.total * HR, A.grid);
-  const int64_t b = blockIdx.x / HR, hr = blockIdx.x % HR;
-  bool bad;
-  int64_t before = plan.before[b / per];
-  for (int64_t x = b / per * per; x < b; ++x) before += c4_pages(A, x, bad);
-  const int32_t pages = c4_pages(A, b, bad);
-  if (pages == 0) return;
-  const int64_t seg = before * HR + hr * pages, end = seg + pages;
-  const int64_t w0 = seg / share, w1 = (end - 1) / share;
-  if (w0 == w1) return;  // written whole
-  const int32_t h = (int32_t)(hr / A.row_blocks), r0 = (int32_t)(hr % A.row_blocks) * kRows;
-  const int32_t nnew = bad ? A.T : (A.count ? A.count[b] : A.T), R = A.T * A.G;
-  auto rec = [&](int64_t wg) {
-    return A.parts + (wg * 2 + (wg == w0 && seg > wg * share ? 1 : 0)) * kFloats;
-  };
-  for (int x = tid; x < kRows * D / 8; x += 256) {
-    const int row = x / (D / 8), d0 = (x % (D / 8)) * 8;
-    const int32_t r = r0 + row, i = r / A.G;
-    if (r >= R || i >= nnew) continue;
-    float m = kC4Low, l = 0.f, v[8] = {};
-    for (int64_t wg = w0; wg <= w1; ++wg) {
-      const float* p = rec(wg);
-      const float pm = p[kRows * D + row], pl = p[kRows * D + kRows + row];
-      const float top = fmaxf(m, pm);
-      const float f = __builtin_amdgcn_exp2f(m - top), g = __builtin_amdgcn_exp2f(pm - top);
-      m = top;
-      l = l * f + pl * g;
+  constexpr int kRows = RT * 16, E = D / 64;  // E columns a lane
+  constexpr int64_t kFloats = C4Rec<D, RT>::kFloats;
+  __shared__ float vs[4][4][D], ms[4][4], ls[4][4];  // [quarter of the records][row]
+  const auto* cp = A.cuts + blockIdx.x;
+  const int32_t parts = c4_scalar(&cp->parts);
+  if (parts == 0) return;
+  const int32_t b = c4_scalar(&cp->b), hr = c4_scalar(&cp->hr), slot = c4_scalar(&cp->slot);
+  const int32_t nnew = c4_scalar(&cp->nnew);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float* rest = A.parts + (int64_t)blockIdx.x * 2 * kFloats;
+  const float* first = rest + slot * kFloats;
+  float m, l, v[E];
+  if (parts <= 8) {
+    float m1[1], l1[1], v1[1][E];
+    c4_gather<D, 1, 4>(first, rest, 2 * kFloats, kRows, blockIdx.y * 4 + w, 0, parts, lane, m1, l1, v1);
+    m = m1[0], l = l1[0];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = v[e] * f + p[row * D + d0 + e] * g;
+    for (int e = 0; e < E; ++e) v[e] = v1[0][e];
+  } else {
+    float m4[4], l4[4], v4[4][E];
+    const int32_t per = (parts + 3) / 4;
+    c4_gather<D, 4, 4>(first, rest, 2 * kFloats, kRows, blockIdx.y * 4, w * per, min(parts, w * per + per),
+                       lane, m4, l4, v4);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) vs[w][y][lane * E + e] = v4[y][e];
+      if (lane == 0) {
+        ms[w][y] = m4[y];
+        ls[w][y] = l4[y];
+      }
     }
-    c4_finish8(A, b, i, h * A.G + (r - i * A.G), d0, v, m, l);
+    __syncthreads();
+    m = fmaxf(fmaxf(ms[0][w], ms[1][w]), fmaxf(ms[2][w], ms[3][w]));
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float f = __builtin_amdgcn_exp2f(ms[x][w] - m);
+      l += ls[x][w] * f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += vs[x][w][lane * E + e] * f;
+    }
   }
+  const int32_t h = hr / A.row_blocks, r = hr % A.row_blocks * kRows + blockIdx.y * 4 + w, i = r / A.G;
+  if (r < A.T * A.G && i < nnew) c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l);
 }
 
 }  // namespace sv

@@ -103,17 +103,16 @@ void launch_read(int32_t d, unsigned grid, const sv::C4MoveArgs& A, hipStream_t 
 
 // Row tiles of 16 a workgroup keeps (its accumulators grow with them), and
 // how many such blocks hold the rows of a kv head.
-int max_tiles(int32_t d) { return d == 256 ? 2 : 4; }
+int max_tiles(int32_t d) { return d == 256 ? 2 : d == 128 ? 3 : 4; }
 void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
   const int64_t t = (rows + 15) / 16;
   *blocks = (t + max_tiles(d) - 1) / max_tiles(d);
   *tiles = int((t + *blocks - 1) / *blocks);
-  if (*tiles == 3) *tiles = 4;
 }
 
-// Workgroups of the attention: as many as the largest device of this kind
-// holds at once; fewer pages than that leave the rest idle.
-constexpr int64_t kAttnGrid = 512;
+// Sequences of at most this many pages are not cut: the pass that joins cut
+// ones costs more than a workgroup's time over four pages a wave.
+constexpr int32_t kAttnWhole = 16;
 
 int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
   if (B < 1 || T < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads) return SPEC_ERR_INVALID_ARG;
@@ -127,19 +126,23 @@ size_t attention_workspace(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t
   int tiles;
   int64_t blocks;
   row_blocks(int64_t(T) * (q_heads / kv_heads), d, &tiles, &blocks);
-  return size_t(kAttnGrid) * 2 * size_t(tiles) * 16 * size_t(d + 2) * 4;
+  return size_t(sv::kC4Grid) * (sizeof(sv::C4Cut) + 2 * size_t(tiles) * 16 * size_t(d + 2) * 4);
 }
 
 template <int D, int RT>
-void launch_attention(const sv::C4AttnArgs& A, unsigned join, hipStream_t st) {
-  hipLaunchKernelGGL((sv::k_attention_cache4<D, RT>), dim3(unsigned(A.grid)), dim3(256), 0, st, A);
-  hipLaunchKernelGGL((sv::k_attention_cache4_join<D, RT>), dim3(join), dim3(256), 0, st, A);
+void launch_attention(const sv::C4AttnArgs& A, hipStream_t st) {
+  hipLaunchKernelGGL((sv::k_attention_cache4<D, RT>), dim3(sv::kC4Grid), dim3(256), 0, st, A);
+  if (A.split)
+    hipLaunchKernelGGL((sv::k_attention_cache4_join<D, RT>), dim3(sv::kC4Grid, RT * 4), dim3(256), 0, st, A);
 }
 template <int D>
-void launch_attention(int tiles, const sv::C4AttnArgs& A, unsigned join, hipStream_t st) {
-  if (tiles == 1) launch_attention<D, 1>(A, join, st);
-  else if (tiles == 2) launch_attention<D, 2>(A, join, st);
-  else if constexpr (D < 256) launch_attention<D, 4>(A, join, st);
+void launch_attention(int tiles, const sv::C4AttnArgs& A, hipStream_t st) {
+  if (tiles == 1) launch_attention<D, 1>(A, st);
+  else if (tiles == 2) launch_attention<D, 2>(A, st);
+  else if constexpr (D < 256) {
+    if (tiles == 3) launch_attention<D, 3>(A, st);
+    else if constexpr (D == 64) launch_attention<D, 4>(A, st);
+  }
 }
 
 int check_head(const void* weight, int64_t row_bytes, int32_t V, int32_t d) {
@@ -242,20 +245,20 @@ int spec_attention_cache4(spec_cache4_t cache, spec_heads_t q, int32_t B, int32_
   int tiles;
   int64_t blocks;
   row_blocks(int64_t(T) * G, cache.head_dim, &tiles, &blocks);
-  const int64_t join = int64_t(B) * cache.heads * blocks;
-  if (!grid_fits(join, 256)) return SPEC_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < attention_workspace(T, q_heads, cache.heads, cache.head_dim))
     return SPEC_ERR_WORKSPACE;
   sv::C4AttnArgs A{view(cache), static_cast<const uint16_t*>(q.data), q.seq_stride, q.pos_stride,
                    q.head_stride, static_cast<uint16_t*>(out.data), out.seq_stride, out.pos_stride,
                    out.head_stride, lse, start, count, mask, mask_seq_stride, mask_pos_stride, B, T, G,
-                   int32_t(blocks), c, static_cast<float*>(workspace), int32_t(kAttnGrid)};
+                   int32_t(blocks), c, cache.table_cols > kAttnWhole,
+                   static_cast<sv::C4Cut*>(workspace),
+                   reinterpret_cast<float*>(static_cast<sv::C4Cut*>(workspace) + sv::kC4Grid)};
   auto st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (cache.head_dim == 64) launch_attention<64>(tiles, A, unsigned(join), st);
-  else if (cache.head_dim == 128) launch_attention<128>(tiles, A, unsigned(join), st);
-  else launch_attention<256>(tiles, A, unsigned(join), st);
+  if (cache.head_dim == 64) launch_attention<64>(tiles, A, st);
+  else if (cache.head_dim == 128) launch_attention<128>(tiles, A, st);
+  else launch_attention<256>(tiles, A, st);
   return finish_launch();
 }
 
