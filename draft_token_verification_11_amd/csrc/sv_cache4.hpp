@@ -336,45 +336,63 @@ __device__ __forceinline__ int64_t c4_weight(int32_t pages) {
   return pages ? pages + kC4SegCost : 0;
 }
 
-// Prefix sums of the sequences' weights over a workgroup: thread t owns
-// sequences t * per .. + per.
-struct C4Plan {
-  int64_t before[256];
-  int64_t wave[4];
-  int64_t total;
-};
-__device__ __forceinline__ int32_t c4_plan(const C4AttnArgs& A, C4Plan& P) {
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int32_t per = (A.B + 255) / 256;
+// floor(x / y) for 0 <= x < 2^52, 0 < y < 2^31, the quotient below 2^31.
+__device__ __forceinline__ int32_t c4_div(int64_t x, int32_t y) {
+  int32_t q = (int32_t)((double)x * __builtin_amdgcn_rcp((double)y));  // off by a few at most
+  int64_t r = x - (int64_t)q * y;
+  while (r < 0) --q, r += y;
+  while (r >= y) ++q, r -= y;
+  return q;
+}
+
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ int64_t c4_prefix(int64_t x, int lane) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t o = __shfl_up(x, off);
+    if (lane >= off) x += o;
+  }
+  return x;
+}
+__device__ __forceinline__ int64_t c4_lane(int64_t x, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int32_t)x, l);
+  const uint32_t hi = __builtin_amdgcn_readlane((int32_t)(x >> 32), l);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// Weight of all sequences' segments (of one head and row block): a lane sums a
+// run of `per` sequences; `before`: the weight before its run.
+__device__ __forceinline__ int64_t c4_plan(const C4AttnArgs& A, int lane, int32_t per, int64_t& before) {
   int64_t sum = 0;
   for (int32_t j = 0; j < per; ++j) {
-    const int64_t b = (int64_t)tid * per + j;
+    const int64_t b = (int64_t)lane * per + j;
     bool bad;
     if (b < A.B) sum += c4_weight(c4_pages<false>(A, b, bad));
   }
-  int64_t incl = sum;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int64_t o = __shfl_up(incl, off);
-    if (lane >= off) incl += o;
-  }
-  if (lane == 63) P.wave[w] = incl;
-  __syncthreads();
-  int64_t base = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (i < w) base += P.wave[i];
-  P.before[tid] = base + incl - sum;
-  if (tid == 255) P.total = base + incl;
-  __syncthreads();
-  return per;
+  const int64_t incl = c4_prefix(sum, lane);
+  before = incl - sum;
+  return c4_lane(incl, 63);
 }
-
-// A value from LDS that all lanes share, as a scalar.
-__device__ __forceinline__ int64_t c4_lanes_same(int64_t x) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int32_t)x);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((int32_t)(x >> 32));
-  return (int64_t)(((uint64_t)hi << 32) | lo);
+// The sequence in which weight x (below the total) lies, and the weight before
+// it: the lane's run, then 64 sequences of it at a time.
+__device__ __forceinline__ int64_t c4_find(const C4AttnArgs& A, int lane, int32_t per, int64_t before,
+                                           int64_t x, int64_t& at) {
+  const int run = 63 - __builtin_clzll(__ballot(before <= x));
+  at = c4_lane(before, run);
+  if (per == 1) return run;
+  for (int64_t b0 = (int64_t)run * per;; b0 += 64) {
+    const int64_t b = b0 + lane;
+    bool bad;
+    const int64_t wt = b < A.B ? c4_weight(c4_pages<false>(A, b, bad)) : 0;
+    const int64_t incl = c4_prefix(wt, lane);
+    const uint64_t past = __ballot(at + incl > x);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      at += c4_lane(incl - wt, l);
+      return b0 + l;
+    }
+    at += c4_lane(incl, 63);
+  }
 }
 
 // The weight of each workgroup's range: an equal share, at least one page per
@@ -704,17 +722,17 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   __shared__ __attribute__((aligned(16))) uint8_t ring0[4 * Sh::kBuf], ring1[4 * Sh::kBuf];
   __shared__ uint4 qs[Sh::kQRegs ? 1 : RT][Sh::kQRegs ? 1 : D / 32][Sh::kQRegs ? 1 : 64];
   __shared__ float ms[4][kRows], ls[4][kRows];
-  // Between segments the buffers hold the plan, or O of 16 rows x kCols columns
-  // of each wave, in turn.
+  // After a segment the buffers hold O of 16 rows x kCols columns of each wave, in turn.
   constexpr int kCols = D == 64 ? 64 : N == 2 ? 128 : 64, kPad = kCols + 4, kRun = kCols / 16;
-  static_assert(sizeof(C4Plan) <= sizeof(ring0) && 4 * 16 * kPad * 4 <= sizeof(ring0), "room");
-  C4Plan& plan = *reinterpret_cast<C4Plan*>(ring0);
+  static_assert(4 * 16 * kPad * 4 <= sizeof(ring0), "room");
 
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n16 = lane & 15, q = lane >> 4;
-  const int32_t per = c4_plan(A, plan);
-  const int64_t HR = (int64_t)A.cache.heads * A.row_blocks;
-  const int64_t all = c4_lanes_same(plan.total) * HR;  // weight of all segments
+  // every wave for itself: no barrier before the first loads
+  const int32_t per = (A.B + 63) / 64;
+  const int32_t HR = A.cache.heads * A.row_blocks;
+  int64_t before;
+  const int64_t all = c4_plan(A, lane, per, before) * HR;  // weight of all segments
   const int64_t share = c4_share(all);
   const int64_t lo = (int64_t)blockIdx.x * share;
   const int64_t hi = min(lo + share, all);
@@ -727,27 +745,13 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     return;
   }
 
-  // the sequence of weight `lo`: its thread's run of sequences, then within it
-  int64_t b = 0, seq_at = 0;  // seq_at: weight before b
-  if (A.B > 1) {
-    int t0 = 0;  // the last thread whose first sequence is at or before lo
-#pragma unroll
-    for (int step = 128; step; step >>= 1)
-      if (plan.before[t0 + step] * HR <= lo) t0 += step;
-    t0 = __builtin_amdgcn_readfirstlane(t0);
-    b = (int64_t)t0 * per;
-    seq_at = c4_lanes_same(plan.before[t0]) * HR;
-  }
-  __syncthreads();  // the plan is read: its buffer is free
+  // the segment of weight `lo`: its sequence, then its head and block of rows
+  int64_t seq_at;
+  int64_t b = c4_find(A, lane, per, before, c4_div(lo, HR), seq_at);
   bool bad;
   int32_t pages = c4_pages<true>(A, b, bad);
-  while (seq_at + c4_weight(pages) * HR <= lo) {
-    seq_at += c4_weight(pages) * HR;
-    pages = c4_pages<true>(A, ++b, bad);
-  }
-  // its segment of that weight, and where that begins
-  int32_t hr = (int32_t)((lo - seq_at) / c4_weight(pages));
-  int64_t seg = seq_at + hr * c4_weight(pages);
+  int32_t hr = c4_div(lo - seq_at * HR, (int32_t)c4_weight(pages));
+  int64_t seg = seq_at * HR + hr * c4_weight(pages);  // where it begins
   const int32_t R = A.T * A.G;
   for (; seg < hi; seg += c4_weight(pages), ++hr) {
     if (hr == HR) {  // the next sequence with pages (seg is its begin)
@@ -763,7 +767,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
     if (p0 == 0 && p1 < pages) {
       cut_b = (int32_t)b, cut_hr = hr, cut_new = nnew, cut_slot = seg > lo ? 1 : 0;
-      cut_parts = (int32_t)((seg + kC4SegCost + pages - 1) / share - blockIdx.x + 1);
+      cut_parts = c4_div(seg + kC4SegCost + pages - 1, (int32_t)share) - blockIdx.x + 1;
     }
 
     // The waves take the segment's pairs of tiles in turn, so that a wave's are

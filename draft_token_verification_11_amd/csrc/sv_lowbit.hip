@@ -245,6 +245,9 @@ int spec_attention_cache4(spec_cache4_t cache, spec_heads_t q, int32_t B, int32_
   int tiles;
   int64_t blocks;
   row_blocks(int64_t(T) * G, cache.head_dim, &tiles, &blocks);
+  // the pages of all sequences, heads and blocks of rows are one sum
+  if (int64_t(B) * (int64_t(cache.table_cols) + sv::kC4SegCost) * cache.heads >= (int64_t(1) << 40) / blocks)
+    return SPEC_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < attention_workspace(T, q_heads, cache.heads, cache.head_dim))
     return SPEC_ERR_WORKSPACE;
