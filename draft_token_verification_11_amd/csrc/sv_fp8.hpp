@@ -155,6 +155,11 @@ __device__ __forceinline__ TO* f8_out_row(const F8HeadArgs& A, int64_t m) {
   const int64_t b = m / A.rows;
   return reinterpret_cast<TO*>(A.out) + b * A.o_seq + (m - b * A.rows) * A.o_pos;
 }
+__device__ __forceinline__ uint2 f8_bf16x4(const f8_f32x4& x) {
+  typedef __bf16 V __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(uint2, V{(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]});
+}
+
 // Four neighbouring logits of a row; `vec`: the row's fours are aligned.
 template <typename TO>
 __device__ __forceinline__ void f8_store4(TO* row, int64_t v, int64_t V, const f8_f32x4& x, bool vec) {
@@ -167,14 +172,13 @@ __device__ __forceinline__ void f8_store4(TO* row, int64_t v, int64_t V, const f
         if (v + r < V) row[v + r] = x[r];
     }
   } else {
-    const uint16_t h[4] = {__builtin_bit_cast(uint16_t, (__bf16)x[0]), __builtin_bit_cast(uint16_t, (__bf16)x[1]),
-                           __builtin_bit_cast(uint16_t, (__bf16)x[2]), __builtin_bit_cast(uint16_t, (__bf16)x[3])};
+    const uint2 h = f8_bf16x4(x);
     if (vec && v + 4 <= V) {
-      *reinterpret_cast<uint2*>(row + v) = make_uint2(h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16));
+      *reinterpret_cast<uint2*>(row + v) = h;
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (v + r < V) row[v + r] = h[r];
+        if (v + r < V) row[v + r] = (uint16_t)((r < 2 ? h.x : h.y) >> (16 * (r & 1)));
     }
   }
 }
@@ -184,109 +188,94 @@ __device__ __forceinline__ bool f8_vec_out(const F8HeadArgs& A) {
   return ((uintptr_t)A.out % n | (uintptr_t)(A.o_seq * sizeof(TO)) % n | (uintptr_t)(A.o_pos * sizeof(TO)) % n) == 0;
 }
 
-// Few hidden rows: bound by the weights' bytes.  A wave takes 16 NB vocabulary
-// entries and every row (16 MB of them), its fragments straight from memory to
-// registers, the blocks of 128 ahead of the one being summed in flight.
-template <typename TO, int MB, int NB>
-__global__ __launch_bounds__(64) void k_lmhead_fp8_rows(F8HeadArgs A) {
-  const int lane = threadIdx.x, n16 = lane & 15, q = lane >> 4;
-  const int64_t v0 = (int64_t)blockIdx.x * (16 * NB);
+// Up to 16 hidden rows: bound by the weights' bytes.  The hidden rows stand in
+// LDS whole, in the order in which lanes take them; a wave goes through units of
+// 16 vocabulary entries, their blocks of 128 columns straight from memory to
+// registers, kFly blocks in flight also from one unit into the next.
+template <typename TO, int BLOCKS>  // BLOCKS: the most blocks a row may have
+__global__ __launch_bounds__(512, 2) void k_lmhead_fp8_rows(F8HeadArgs A) {
+  constexpr int kFly = 6;
+  __shared__ __attribute__((aligned(16))) uint8_t hs[BLOCKS * 2048];
+  __shared__ uint8_t es[BLOCKS * 16];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n16 = lane & 15, q = lane >> 4;
   const int32_t blocks = A.dp / 128;
-  const uint8_t* wp[NB];
-#pragma unroll
-  for (int nb = 0; nb < NB; ++nb) {
-    const int64_t v = v0 + 16 * nb + n16;
-    wp[nb] = A.weight + (v < A.V ? v : A.V - 1) * A.w_stride;  // rows past V are not stored
-  }
-  const uint8_t* hp[MB];
-  const uint8_t* ep[MB];
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const int64_t m = 16 * mb + n16, row = m < A.M ? m : A.M - 1;
-    hp[mb] = A.hidden + row * A.dp + q * 16;
-    ep[mb] = A.exps + row;
-  }
-  const float* sp = A.scale + (v0 / 128) * blocks;  // 16 NB entries lie in one block of 128
+  const int32_t units = (int32_t)((A.V + 15) / 16), waves = gridDim.x * 8;  // V is at most 2^24
+  const int32_t mine = blockIdx.x * 8 + w;
 
+  // This wave's blocks: all of unit `mine`, then of `mine` + waves, ..  Where rows
+  // lie a multiple of 4 KiB apart, a unit's begin at column block unit % blocks:
+  // waves side by side would read the same columns of their rows at one time, and
+  // those share few memory channels (nine rows, 151,936 x 4,096: 137 us from
+  // column 0, 124 so; 32,000 x 8,192: 64 and 55; at pitches of 1,024 to 3,584
+  // bytes it would cost 2 to 8 %).  Past the last block the loads repeat it, unused: no branch makes the compiler wait
+  // for all of them.
   struct Block {
-    uint4 w[NB][2], h[MB][2];
-    uint32_t e[MB];
+    uint4 w[2];
     float s;
   };
-  auto load = [&](int32_t kb, Block& B) {
+  const bool turn = A.w_stride % 4096 == 0;
+  int32_t lu = min(mine, units - 1);  // where the loads are
+  int32_t lk = turn ? lu % blocks : 0, left = blocks;
+  auto load = [&](Block& B) {
+    const int64_t v = min((int64_t)lu * 16 + n16, A.V - 1);  // entries past V are not stored
+    const uint8_t* lw = A.weight + v * A.w_stride;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      // a column past d meets zeros of the hidden row: any byte of the same
-      // head row does
-      const int32_t col = kb * 128 + x * 64 + q * 16, c = col < A.d ? col : 0;
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) B.w[nb][x] = load16(wp[nb] + c);
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) B.h[mb][x] = load16(hp[mb] + kb * 128 + x * 64);
+      // a column past d meets zeros of the hidden rows: column 0 stands in
+      const int32_t col = lk * 128 + x * 64 + q * 16;
+      B.w[x] = load16(lw + (col < A.d ? col : 0));
     }
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) B.e[mb] = ep[mb][kb * A.m_pitch];
-    B.s = sp[kb];
+    B.s = A.scale[(int64_t)(lu / 8) * blocks + lk];  // a unit lies in one block of 128 entries
+    if (--left > 0) {
+      lk = lk + 1 == blocks ? 0 : lk + 1;
+    } else if (lu + waves < units) {
+      left = blocks;
+      lu += waves;
+      lk = turn ? lu % blocks : 0;
+    }
   };
-  f8_f32x4 acc[MB][NB];
+  Block ring[kFly];
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
-  auto add = [&](const Block& B) {
-    f8_f32x4 c[MB][NB];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) c[mb][nb] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f8_bf16x8 hf[MB];
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) hf[mb] = f8_widen(B.h[mb][x], h, f8_scale(B.e[mb]));
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const f8_bf16x8 wf = f8_widen(B.w[nb][x], h, 1.0f);
-#pragma unroll
-          for (int mb = 0; mb < MB; ++mb)
-            c[mb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, hf[mb], c[mb][nb], 0, 0, 0);
-        }
-      }
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[mb][nb][r] = __builtin_fmaf(c[mb][nb][r], B.s, acc[mb][nb][r]);
-  };
-  // three blocks in flight while one is summed
-  Block b0, b1, b2;
-  const int32_t last = blocks - 1;
-  load(0, b0);
-  load(min(1, last), b1);
-  load(min(2, last), b2);
-  int32_t kb = 0;
-  for (; kb + 3 <= blocks; kb += 3) {  // reloads past the end repeat the last block, unused
-    add(b0);
-    load(min(kb + 3, last), b0);
-    add(b1);
-    load(min(kb + 4, last), b1);
-    add(b2);
-    load(min(kb + 5, last), b2);
+  for (int k = 0; k < kFly; ++k) load(ring[k]);
+
+  for (int32_t i = w; i < 2 * blocks; i += 8) {
+    const int64_t m = min((int64_t)n16, A.M - 1);
+    *reinterpret_cast<uint4*>(hs + i * 1024 + lane * 16) =
+        load16(A.hidden + m * A.dp + (i >> 1) * 128 + (i & 1) * 64 + q * 16);
   }
-  if (kb < blocks) add(b0);
-  if (kb + 1 < blocks) add(b1);
+  for (int32_t i = threadIdx.x; i < blocks * 16; i += 512)
+    es[i] = A.exps[(i >> 4) * A.m_pitch + min((int64_t)(i & 15), A.M - 1)];
+  __syncthreads();
 
   const bool vec = f8_vec_out<TO>(A);
+  int32_t u = mine, kb = turn ? mine % blocks : 0, todo = blocks;
+  f8_f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  while (u < units) {
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const int64_t m = 16 * mb + n16;
-    if (m >= A.M) continue;
-    TO* row = f8_out_row<TO>(A, m);
+    for (int k = 0; k < kFly; ++k) {
+      if (u >= units) break;
+      const float sh = f8_scale(es[kb * 16 + n16]);
+      f8_f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) f8_store4<TO>(row, v0 + 16 * nb + 4 * q, A.V, acc[mb][nb], vec);
+      for (int x = 0; x < 2; ++x) {
+        const uint4 h = *reinterpret_cast<const uint4*>(hs + (2 * kb + x) * 1024 + lane * 16);
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen(ring[k].w[x], y, 1.0f), f8_widen(h, y, sh), c, 0, 0, 0);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(c[r], ring[k].s, acc[r]);
+      load(ring[k]);
+      kb = kb + 1 == blocks ? 0 : kb + 1;
+      if (--todo == 0) {
+        if (n16 < A.M) f8_store4<TO>(f8_out_row<TO>(A, n16), (int64_t)u * 16 + 4 * q, A.V, acc, vec);
+        acc = f8_f32x4{0.f, 0.f, 0.f, 0.f};
+        todo = blocks;
+        u += waves;
+        kb = turn ? u % blocks : 0;
+      }
+    }
   }
 }
 
@@ -294,16 +283,19 @@ __global__ __launch_bounds__(64) void k_lmhead_fp8_rows(F8HeadArgs A) {
 // WV x WM, the operands' blocks of 128 columns (one row of 128 bytes each)
 // through two LDS buffers that the memory pipeline fills by itself
 // (buffer_load ... lds, 16 bytes a lane) while the matrix instructions work on
-// the other.  A row's eight 16-byte chunks are stored in the order c ^ (row % 8),
-// by permuting the addresses that the lanes load from, so that the eight rows a
-// quarter of a fragment read touches fall on different banks.
+// the other.  A row's eight 16-byte chunks are stored in the order
+// c ^ (row / 2 % 8), by permuting the addresses that the lanes load from, so that
+// the 16 rows a quarter of a fragment read touches (256 bytes) fall on the 64
+// banks without conflict.
 template <typename TO, bool F8, int BV, int BM, int WV>
 __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
   constexpr int WM = 8 / WV, TV = BV / WV / 16, TM = BM / WM / 16;  // a wave's tiles of 16
   static_assert(TV * WV * 16 == BV && TM * WM * 16 == BM, "whole tiles");
   static_assert(BV % 64 == 0 && BM % 64 == 0, "8 rows a wave and load");
   static_assert(128 % (BV / WV) == 0, "a wave's entries lie in one block of 128");
-  constexpr int kTiles = BM;  // a buffer: the rows' exponents, then the bytes of [weights | hidden]
+  static_assert(TV <= 4, "a column's tiles are added in four steps");
+  constexpr int kTiles = 256;  // a buffer: the rows' exponents, then the bytes of [weights | hidden]
+  static_assert(BM <= 256, "room");
   constexpr int kBuf = kTiles + (BV + BM) * 128;
   // two arrays, each named where it is used, so that the compiler can tell a
   // fragment read of one from the fill of the other and does not wait for it
@@ -329,29 +321,31 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
                                                       mr * A.dp, 0x00020000);
   const auto esrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(A.exps + m0), 0,
                                                       (int32_t)min(A.m_pitch * blocks - m0, (int64_t)0x7FFFFFFF), 0x00020000);
-  const int row = 8 * w + lane / 8, chunk = ((lane & 7) ^ (lane >> 3)) * 16;  // row % 8 is lane / 8
+  const int row = 8 * w + lane / 8, chunk = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
   const int32_t woff = row * ws + chunk, hoff = row * A.dp + chunk;
   typedef __attribute__((address_space(3))) void* Lds;
-  auto stage = [&](int32_t kb, uint8_t* to) {
+  // Load x of block kb's kLoads: eight rows of the weights or the hidden rows,
+  // and last (the first wave's) the exponents.
+  constexpr int kLoads = BV / 64 + BM / 64;
+  auto stage = [&](int32_t kb, uint8_t* to, int x) {
     // one register per operand: the rows' offsets are added here, not kept
     int32_t wo = woff, ho = hoff;
     asm volatile("" : "+v"(wo), "+v"(ho));
-    // a column past d: the hidden row's zeros meet a zero
-    const bool in = kb * 128 + chunk < A.d;
-#pragma unroll
-    for (int i = 0; i < BV / 64; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc, (Lds)(to + kTiles + (64 * i + 8 * w) * 128), 16,
-                                               in ? wo + (kb * 128 + 64 * i * ws) : 0x7FFFFFFF, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < BM / 64; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(hsrc, (Lds)(to + kTiles + (BV + 64 * i + 8 * w) * 128), 16,
-                                               ho + (kb * 128 + 64 * i * A.dp), 0, 0, 0);
-    if (w < BM / 256)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(esrc, (Lds)(to + 256 * w), 4,
-                                               (int32_t)(kb * A.m_pitch) + 256 * w + 4 * lane, 0, 0, 0);
+    if (x < BV / 64) {
+      // a column past d: the hidden row's zeros meet a zero
+      const bool in = kb * 128 + chunk < A.d;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc, (Lds)(to + kTiles + (64 * x + 8 * w) * 128), 16,
+                                               in ? wo + (kb * 128 + 64 * x * ws) : 0x7FFFFFFF, 0, 0, 0);
+    } else {
+      const int y = x - BV / 64;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(hsrc, (Lds)(to + kTiles + (BV + 64 * y + 8 * w) * 128), 16,
+                                               ho + (kb * 128 + 64 * y * A.dp), 0, 0, 0);
+    }
+    if (x == kLoads - 1 && w == 0)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(esrc, (Lds)to, 4, (int32_t)(kb * A.m_pitch) + 4 * lane, 0, 0, 0);
   };
   auto chunk_of = [&](const uint8_t* from, int r, int c) {
-    return *reinterpret_cast<const uint4*>(from + kTiles + r * 128 + ((c ^ (r & 7)) * 16));
+    return *reinterpret_cast<const uint4*>(from + kTiles + r * 128 + ((c ^ ((r >> 1) & 7)) * 16));
   };
 
   f8_f32x4 acc[TV][TM];
@@ -364,7 +358,10 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
   const auto* sp = (const __attribute__((address_space(4))) float*)(
       A.scale + min((v0 + vw) / 128, (A.V - 1) / 128) * blocks);
 
-  auto compute = [&](int32_t kb, const uint8_t* from) {
+  // Computes block kb and starts the loads of the next one: spread over the
+  // columns, for issued together they hold the wave (and, after a barrier, all
+  // of them) for 700 to 1,200 cycles of a block's 4,000.
+  auto compute = [&](int32_t kb, const uint8_t* from, uint8_t* to) {
     const float s = sp[kb];
     uint4 wf[TV][2];
 #pragma unroll
@@ -377,17 +374,14 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
       for (int i = 0; i < TV; ++i)
 #pragma unroll
         for (int y = 0; y < 4; ++y) wb[i][y] = f8_widen(wf[i][y / 2], y & 1, 1.0f);
-    // a column of tiles is added to the running sums while the next one's
-    // products are under way
+    // a tile is added to the running sums while the matrix unit works on the one
+    // in its place of the next column
     f8_f32x4 c[2][TV];
-    auto add = [&](int j) {
+    auto add = [&](int i, int j) {
 #pragma unroll
-      for (int i = 0; i < TV; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(c[j & 1][i][r], s, acc[i][j][r]);
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(c[j & 1][i][r], s, acc[i][j][r]);
       // keeps the products here: without a use they may move past the barrier
-#pragma unroll
-      for (int i = 0; i < TV; ++i) asm volatile("" : "+v"(acc[i][j]));
+      asm volatile("" : "+v"(acc[i][j]));
     };
     uint4 hf[2][2];
     uint32_t e[2];
@@ -400,29 +394,41 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
       if (j + 1 < TM) rows(j + 1);
+      if (kb + 1 < blocks) {
 #pragma unroll
-      for (int i = 0; i < TV; ++i) c[j & 1][i] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int x = kLoads * j / TM; x < kLoads * (j + 1) / TM; ++x) stage(kb + 1, to, x);
+      }
       if constexpr (F8) {
         const f8_i32x8 hb = f8_join(hf[j & 1][0], hf[j & 1][1]);
 #pragma unroll
-        for (int i = 0; i < TV; ++i)
+        for (int i = 0; i < TV; ++i) {
           c[j & 1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              f8_join(wf[i][0], wf[i][1]), hb, c[j & 1][i], 0, 0, 0, 127, 0, (int)e[j & 1]);
+              f8_join(wf[i][0], wf[i][1]), hb, f8_f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, (int)e[j & 1]);
+          __builtin_amdgcn_sched_barrier(0);  // the order here is the one meant
+          if (j) add(i, j - 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       } else {
         const float sh = f8_scale(e[j & 1]);
+        f8_bf16x8 hb[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) hb[y] = f8_widen(hf[j & 1][y / 2], y & 1, sh);
+#pragma unroll
+        for (int i = 0; i < TV; ++i) c[j & 1][i] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const f8_bf16x8 hb = f8_widen(hf[j & 1][y / 2], y & 1, sh);
 #pragma unroll
-          for (int i = 0; i < TV; ++i)
-            c[j & 1][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[i][y], hb, c[j & 1][i], 0, 0, 0);
+          for (int i = 0; i < TV; ++i) {
+            c[j & 1][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[i][y], hb[y], c[j & 1][i], 0, 0, 0);
+            if (i == 0) __builtin_amdgcn_sched_barrier(0);
+          }
+          if (j && y < TV) add(y, j - 1);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if (j) add(j - 1);
-      // the order above is the one meant: fragments one column ahead, no more
-      __builtin_amdgcn_sched_barrier(0);
     }
-    add(TM - 1);
+#pragma unroll
+    for (int i = 0; i < TV; ++i) add(i, TM - 1);
     __builtin_amdgcn_sched_barrier(0);
   };
 
@@ -433,29 +439,76 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
   };
-  stage(0, buf0);
+#pragma unroll
+  for (int x = 0; x < kLoads; ++x) stage(0, buf0, x);
   int32_t kb = 0;
   for (; kb + 1 < blocks; kb += 2) {
     arrive();
-    stage(kb + 1, buf1);
-    compute(kb, buf0);
+    compute(kb, buf0, buf1);
     arrive();
-    if (kb + 2 < blocks) stage(kb + 2, buf0);
-    compute(kb + 1, buf1);
+    compute(kb + 1, buf1, buf0);
   }
   if (kb < blocks) {
     arrive();
-    compute(kb, buf0);
+    compute(kb, buf0, buf1);
   }
 
-  const bool vec = f8_vec_out<TO>(A);
+  // The tile leaves through LDS, so that a row's entries leave together: kOut
+  // rows at a time, 512 bytes of a row (its 16-byte chunks in the order
+  // c ^ (row % 32), for the banks), then 16 bytes a lane, or one entry a lane
+  // where the rows do not start at multiples of 16 bytes (240 rows of 128,003
+  // F32 entries: stored from the registers 0.26 ms, so 0.19).
+  constexpr int kOut = kBuf >= 128 * 512 ? 128 : kBuf >= 64 * 512 ? 64 : 32;
+  static_assert(BV * sizeof(TO) == 512 && kOut * 512 <= kBuf, "room");
+  constexpr int kRound = kOut / WM / 16;  // a wave's columns of tiles each time
+  static_assert(TM % kRound == 0, "whole rounds");
+  const bool vec = ((uintptr_t)A.out | (uintptr_t)(A.o_seq * sizeof(TO)) | (uintptr_t)(A.o_pos * sizeof(TO))) % 16 == 0;
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int64_t m = m0 + mw + 16 * j + n16;
-    if (m >= A.M) continue;
-    TO* row = f8_out_row<TO>(A, m);
+  for (int g = 0; g < TM / kRound; ++g) {
+    __syncthreads();  // every wave is done with the buffer
 #pragma unroll
-    for (int i = 0; i < TV; ++i) f8_store4<TO>(row, v0 + vw + 16 * i + 4 * q, A.V, acc[i][j], vec);
+    for (int j = 0; j < kRound; ++j) {
+      const int r = (w % WM) * (kRound * 16) + 16 * j + n16;
+#pragma unroll
+      for (int i = 0; i < TV; ++i) {
+        const f8_f32x4 x = acc[i][g * kRound + j];
+        const int at = (vw + 16 * i + 4 * q) * (int)sizeof(TO);  // 8 or 16 bytes
+        uint8_t* to = buf0 + r * 512 + (((at / 16) ^ (r & 31)) * 16) + at % 16;
+        if constexpr (sizeof(TO) == 4) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+        else *reinterpret_cast<uint2*>(to) = f8_bf16x4(x);
+      }
+    }
+    __syncthreads();
+    if (vec) {
+      const int c = threadIdx.x & 31;
+#pragma unroll
+      for (int k = 0; k < kOut / 16; ++k) {
+        const int r = 16 * k + (threadIdx.x >> 5);
+        const int64_t m = m0 + (r / (kRound * 16)) * (BM / WM) + g * kRound * 16 + r % (kRound * 16);
+        constexpr int kPer = 16 / sizeof(TO);
+        const int64_t v = v0 + c * kPer;
+        if (m >= A.M || v >= A.V) continue;
+        TO* row = f8_out_row<TO>(A, m);
+        const uint8_t* from = buf0 + r * 512 + ((c ^ (r & 31)) * 16);
+        if (v + kPer <= A.V) {
+          *reinterpret_cast<uint4*>(row + v) = *reinterpret_cast<const uint4*>(from);
+        } else {
+          for (int e = 0; v + e < A.V; ++e) row[v + e] = reinterpret_cast<const TO*>(from)[e];
+        }
+      }
+    } else {
+      for (int r = w; r < kOut; r += 8) {
+        const int64_t m = m0 + (r / (kRound * 16)) * (BM / WM) + g * kRound * 16 + r % (kRound * 16);
+        if (m >= A.M) continue;
+        TO* row = f8_out_row<TO>(A, m);
+#pragma unroll
+        for (int k = 0; k < BV / 64; ++k) {
+          const int x = 64 * k + lane, at = x * (int)sizeof(TO);
+          if (v0 + x < A.V)
+            row[v0 + x] = *reinterpret_cast<const TO*>(buf0 + r * 512 + (((at / 16) ^ (r & 31)) * 16) + at % 16);
+        }
+      }
+    }
   }
 }
 

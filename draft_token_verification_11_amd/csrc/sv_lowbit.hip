@@ -154,15 +154,6 @@ int check_head(const void* weight, int64_t row_bytes, int32_t V, int32_t d) {
 
 int64_t padded(int32_t d) { return (int64_t(d) + 127) / 128 * 128; }
 
-// Few rows go straight from memory to the matrix instructions, more through
-// LDS in tiles.
-constexpr int64_t kHeadRows = 64;
-
-template <typename TO, int MB, int NB>
-void launch_head_rows(const sv::F8HeadArgs& A, hipStream_t st) {
-  hipLaunchKernelGGL((sv::k_lmhead_fp8_rows<TO, MB, NB>), dim3(unsigned((A.V + 16 * NB - 1) / (16 * NB))),
-                     dim3(64), 0, st, A);
-}
 template <typename TO, bool F8, int BV, int BM, int WV>
 void launch_head_tile(sv::F8HeadArgs A, hipStream_t st) {
   A.v_tiles = int32_t((A.V + BV - 1) / BV);
@@ -171,13 +162,26 @@ void launch_head_tile(sv::F8HeadArgs A, hipStream_t st) {
   hipLaunchKernelGGL((sv::k_lmhead_fp8_tile<TO, F8, BV, BM, WV>), dim3(unsigned((tiles + 7) / 8 * 8)),
                      dim3(512), 0, st, A);
 }
+// One workgroup per compute unit of the kernel for up to 16 rows.
+constexpr unsigned kHeadGrid = 256;
+
 template <typename TO>
 void launch_head(const sv::F8HeadArgs& A, hipStream_t st) {
-  if (A.M <= 16) launch_head_rows<TO, 1, 4>(A, st);
-  else if (A.M <= 32) launch_head_rows<TO, 2, 4>(A, st);
-  else if (A.M <= kHeadRows) launch_head_rows<TO, 4, 2>(A, st);
-  else if constexpr (sizeof(TO) == 2) launch_head_tile<TO, true, 256, 256, 4>(A, st);
-  else launch_head_tile<TO, false, 128, 256, 2>(A, st);
+  constexpr bool f8 = sizeof(TO) == 2;        // BF16 logits: the 8-bit instructions' sums do
+  constexpr int BV = 512 / int(sizeof(TO));   // 512 bytes of a row of logits
+  // Up to 16 rows whose LDS image fits (rows of 8,192).
+  if (A.M <= 16 && A.dp <= 8192) {
+    if (A.dp <= 4096)
+      hipLaunchKernelGGL((sv::k_lmhead_fp8_rows<TO, 32>), dim3(kHeadGrid), dim3(512), 0, st, A);
+    else
+      hipLaunchKernelGGL((sv::k_lmhead_fp8_rows<TO, 64>), dim3(kHeadGrid), dim3(512), 0, st, A);
+  } else if (A.M <= 64) {
+    launch_head_tile<TO, f8, BV, 64, f8 ? 8 : 4>(A, st);
+  } else if ((A.M + 127) / 128 * 128 < (A.M + 255) / 256 * 256) {  // fewer padded rows
+    launch_head_tile<TO, f8, BV, 128, f8 ? 4 : 2>(A, st);
+  } else {
+    launch_head_tile<TO, f8, BV, 256, f8 ? 4 : 2>(A, st);
+  }
 }
 
 }  // namespace
@@ -313,7 +317,7 @@ int spec_lmhead_fp8(spec_logits_t hidden, int32_t B, int32_t rows, int32_t d, co
     return SPEC_ERR_INVALID_ARG;
   const int64_t M = int64_t(B) * rows, dp = padded(d);
   const int64_t rounding = (M * (dp / 128) + 15) / 16;
-  const int64_t tiles = ((int64_t(V) + 127) / 128) * ((M + 127) / 128);  // of the smallest kind, and a round of 8
+  const int64_t tiles = ((int64_t(V) + 127) / 128) * ((M + 63) / 64);  // of the smallest kind, and a round of 8
   if (!grid_fits(rounding, 256) || !grid_fits(tiles + 8, 512)) return SPEC_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < spec_lmhead_fp8_workspace(B, rows, d))
     return SPEC_ERR_WORKSPACE;
