@@ -15,6 +15,7 @@ every draft passes; greedy mode compares argmaxes.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -669,25 +670,18 @@ def verify_greedy_lmhead(hidden: torch.Tensor, weight: torch.Tensor, draft_token
 CACHE4_PAGE = 64
 
 
-class _on:
-    """The tensors' device and the call's stream as torch's current ones."""
+_here = contextlib.nullcontext()
 
-    def __init__(self, dev, stream):
-        self.stream = stream if stream is not None else torch.cuda.current_stream(dev)
-        if self.stream.device != dev:
-            raise ValueError("the stream must belong to %s, got %s" % (dev, self.stream.device))
-        self.ctx = None
-        if stream is not None or torch.cuda.current_device() != dev.index:
-            self.ctx = torch.cuda.stream(self.stream)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on(index: int, stream):
+    """(the call's raw stream, a context that makes it and device `index`
+    torch's current ones)."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+        return raw, _here if torch.cuda.current_device() == index else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError("the stream must belong to device %d, got %s" % (index, stream.device))
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _scratch(workspace, dev, need):
@@ -696,51 +690,57 @@ def _scratch(workspace, dev, need):
     return _workspace_arg(workspace, dev, need, None)
 
 
-def _device_tensor(t, what, dtype, dim, dev=None):
-    """`t` checked: a device tensor of the dtype(s) and dimension, on `dev`."""
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _device_tensor(t, what, dtypes, dim, index=None) -> int:
+    """`t` checked: a device tensor of one of the dtypes and so many axes, on
+    device `index` if given; its device's index."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a tensor" % what)
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
     if t.dim() != dim:
         raise ValueError("%s must have %d axes, got shape %s" % (what, dim, tuple(t.shape)))
     if not t.is_cuda:
         raise ValueError("%s must live in device memory" % what)
-    if dev is not None and t.device != dev:
-        raise ValueError("%s must live on %s, got %s" % (what, dev, t.device))
-    return t
-
-
-def _stride(t, axis) -> int:
-    """The axis's stride; 0 where it is never stepped along."""
-    return t.stride(axis) if t.shape[axis] > 1 else 0
+    i = t.get_device()
+    if index is not None and i != index:
+        raise ValueError("%s must live on device %d, got %s" % (what, index, t.device))
+    return i
 
 
 def _heads(t, what, shape=None) -> spec_heads_t:
-    """Heads of positions [B][T][heads][D], last axis contiguous."""
-    if t.stride(3) != 1:
+    """Heads of positions [B][T][heads][D], last axis contiguous; the stride of
+    an axis that is never stepped along is 0."""
+    n, s = t.shape, t.stride()
+    if s[3] != 1 and n[3] > 1:
         raise ValueError("the last axis of %s must be contiguous" % what)
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be of shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
-    return spec_heads_t(t.data_ptr(), _dtype_code(t), 0, *(_stride(t, i) for i in range(3)))
+    if shape is not None and n != shape:
+        raise ValueError("%s must be of shape %s, got %s" % (what, tuple(shape), tuple(n)))
+    return spec_heads_t(t.data_ptr(), SPEC_DTYPE_BF16 if t.dtype is torch.bfloat16 else SPEC_DTYPE_F32,
+                        0, s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
 
 
-def _cache4(pages, table, D, B):
-    _device_tensor(pages, "pages", torch.uint8, 3)
-    _device_tensor(table, "table", torch.int32, 2, pages.device)
-    if not pages.is_contiguous() or pages.shape[2] != 68 * D:
+def _cache4(pages, table, D, B, index=None):
+    """(the cache's descriptor, its device's index)."""
+    index = _device_tensor(pages, "pages", (torch.uint8,), 3, index)
+    _device_tensor(table, "table", (torch.int32,), 2, index)
+    n, heads, record = pages.shape
+    if record != 68 * D or not pages.is_contiguous():
         raise ValueError("pages must be contiguous [n_pages][heads][%d] for heads of %d, got %s"
                          % (68 * D, D, tuple(pages.shape)))
-    if table.shape[0] != B or table.stride(1) != 1:
+    rows, cols = table.shape
+    if rows != B or (table.stride(1) != 1 and cols > 1):
         raise ValueError("table must be [%d][pages of a sequence] with a contiguous last axis" % B)
-    return spec_cache4_t(pages.data_ptr(), table.data_ptr(), max(table.stride(0), table.shape[1]),
-                         pages.shape[0], table.shape[1], pages.shape[1], D)
+    return spec_cache4_t(pages.data_ptr(), table.data_ptr(),
+                         table.stride(0) if rows > 1 else max(1, cols), n, cols, heads, D), index
 
 
-def _per_sequence(t, what, B, dev):
+def _per_sequence(t, what, B, index):
     if t is None:
         return None
-    _device_tensor(t, what, torch.int32, 1, dev)
+    _device_tensor(t, what, (torch.int32,), 1, index)
     if t.shape[0] != B or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 [%d]" % (what, B))
     return t.data_ptr()
@@ -769,18 +769,19 @@ def cache4_write(pages: torch.Tensor, table: torch.Tensor, start: torch.Tensor, 
     ill-formed sequence or position.  After a verify call the next step's
     start is start + accepted_len + 1 (a chain): what lies behind is
     overwritten."""
-    _device_tensor(k, "k", (torch.float32, torch.bfloat16), 4)
-    _device_tensor(v, "v", k.dtype, 4, k.device)
+    index = _device_tensor(k, "k", _FLOATS, 4)
+    _device_tensor(v, "v", (k.dtype,), 4, index)
     B, T, H, D = k.shape
-    cache = _cache4(pages, table, D, B)
-    if pages.device != k.device or pages.shape[1] != H:
-        raise ValueError("pages and k disagree on device or heads")
-    s, n = (_per_sequence(t, w, B, k.device) for t, w in ((start, "start"), (count, "count")))
-    if s is None:
+    cache, _ = _cache4(pages, table, D, B, index)
+    if cache.heads != H:
+        raise ValueError("pages hold %d heads, k %d" % (cache.heads, H))
+    if start is None:
         raise ValueError("start is required")
-    kd, vd = _heads(k, "k"), _heads(v, "v", k.shape)
-    with _on(k.device, stream) as st:
-        rc = lib().spec_cache4_write(cache, kd, vd, B, T, s, n, st)
+    s = _per_sequence(start, "start", B, index)
+    n = _per_sequence(count, "count", B, index)
+    st, ctx = _on(index, stream)
+    with ctx:
+        rc = lib().spec_cache4_write(cache, _heads(k, "k"), _heads(v, "v", k.shape), B, T, s, n, st)
     _check(rc, "spec_cache4_write")
 
 
@@ -791,21 +792,27 @@ def cache4_read(pages: torch.Tensor, table: torch.Tensor, start: torch.Tensor, T
     back as (k, v) [B][T][heads][head_dim]; both dtypes hold the values
     exactly.  Rows past count[b] are zero, or left as they were in
     ``out`` = (k, v).  Ill-formed sequences and positions read as NaN."""
-    B = start.shape[0]
-    cache = _cache4(pages, table, head_dim, B)
-    dev = pages.device
-    s, n = (_per_sequence(t, w, B, dev) for t, w in ((start, "start"), (count, "count")))
-    shape = (B, int(T), pages.shape[1], head_dim)
-    with _on(dev, stream) as st:
+    if not isinstance(start, torch.Tensor) or start.dim() != 1:
+        raise ValueError("start must be an int32 tensor [B]")
+    B, T = start.shape[0], int(T)
+    cache, index = _cache4(pages, table, head_dim, B)
+    s = _per_sequence(start, "start", B, index)
+    n = _per_sequence(count, "count", B, index)
+    shape = (B, T, cache.heads, head_dim)
+    st, ctx = _on(index, stream)
+    with ctx:
         if out is None:
+            if dtype not in _FLOATS:
+                raise TypeError("dtype must be float32 or bfloat16, got %s" % dtype)
             make = torch.empty if count is None else torch.zeros
-            k, v = (make(shape, dtype=dtype, device=dev) for _ in range(2))
+            k = make(shape, dtype=dtype, device=pages.device)
+            v = make(shape, dtype=dtype, device=pages.device)
         else:
             k, v = out
-            _device_tensor(k, "out[0]", (torch.float32, torch.bfloat16), 4, dev)
-            _device_tensor(v, "out[1]", k.dtype, 4, dev)
+            _device_tensor(k, "out[0]", _FLOATS, 4, index)
+            _device_tensor(v, "out[1]", (k.dtype,), 4, index)
         rc = lib().spec_cache4_read(cache, _heads(k, "out[0]", shape), _heads(v, "out[1]", shape), B,
-                                    int(T), s, n, st)
+                                    T, s, n, st)
     _check(rc, "spec_cache4_read")
     return k, v
 
@@ -845,39 +852,39 @@ def attention_cache4(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor,
     denominator [B][T][q_heads] float32.  Rows past count[b] are zero, or left
     as they were in the caller's tensors; a token that sees nothing gets 0 and
     -inf; ill-formed sequences get NaN."""
-    _device_tensor(q, "q", torch.bfloat16, 4)
+    index = _device_tensor(q, "q", (torch.bfloat16,), 4)
     B, T, Hq, D = q.shape
-    dev = q.device
-    cache = _cache4(pages, table, D, B)
-    if pages.device != dev:
-        raise ValueError("q and pages must live on one device")
-    s, n = (_per_sequence(t, w, B, dev) for t, w in ((start, "start"), (count, "count")))
-    if s is None:
+    cache, _ = _cache4(pages, table, D, B, index)
+    if start is None:
         raise ValueError("start is required")
+    s = _per_sequence(start, "start", B, index)
+    n = _per_sequence(count, "count", B, index)
     mp, ms, mr = None, 0, 0
     if mask is not None:
-        _device_tensor(mask, "mask", torch.int32, 3, dev)
-        if mask.shape[0] not in (1, B) or tuple(mask.shape[1:]) != (T, (T + 31) // 32) or \
-                mask.stride(2) != 1:
-            raise ValueError("mask must be int32 words [B|1][%d][%d] with contiguous words"
-                             % (T, (T + 31) // 32))
-        mp, ms, mr = mask.data_ptr(), _stride(mask, 0), _stride(mask, 1)
+        _device_tensor(mask, "mask", (torch.int32,), 3, index)
+        rows, words = mask.shape[0], (T + 31) // 32
+        if rows not in (1, B) or tuple(mask.shape[1:]) != (T, words) or \
+                (mask.stride(2) != 1 and words > 1):
+            raise ValueError("mask must be int32 words [B|1][%d][%d] with contiguous words" % (T, words))
+        mp, ms, mr = mask.data_ptr(), mask.stride(0) if rows > 1 else 0, mask.stride(1) if T > 1 else 0
     if lse is not None:
-        _out_tensor(lse, (B, T, Hq), torch.float32, dev, "lse")
-    need = lib().spec_attention_cache4_workspace(B, T, Hq, pages.shape[1], D)
+        _out_tensor(lse, (B, T, Hq), torch.float32, q.device, "lse")
+    if out is not None:
+        _device_tensor(out, "out", (torch.bfloat16,), 4, index)
+    L = lib()
+    need = L.spec_attention_cache4_workspace(B, T, Hq, cache.heads, D)
     if need == 0:
-        _check(SPEC_ERR_UNSUPPORTED if B and T and Hq and Hq % pages.shape[1] == 0
+        _check(SPEC_ERR_UNSUPPORTED if B and T and Hq and Hq % cache.heads == 0
                else SPEC_ERR_INVALID_ARG, "spec_attention_cache4_workspace")
-    with _on(dev, stream) as st:
+    st, ctx = _on(index, stream)
+    with ctx:
         make = torch.empty if count is None else torch.zeros
         if out is None:
-            out = make((B, T, Hq, D), dtype=torch.bfloat16, device=dev)
-        else:
-            _device_tensor(out, "out", torch.bfloat16, 4, dev)
+            out = make((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
         if return_lse and lse is None:
-            lse = make((B, T, Hq), dtype=torch.float32, device=dev)
-        ws = _scratch(workspace, dev, need)
-        rc = lib().spec_attention_cache4(
+            lse = make((B, T, Hq), dtype=torch.float32, device=q.device)
+        ws = _scratch(workspace, q.device, need)
+        rc = L.spec_attention_cache4(
             cache, _heads(q, "q"), B, T, Hq, s, n, mp, ms, mr,
             float(scale) if scale is not None else D ** -0.5, _heads(out, "out", q.shape),
             lse.data_ptr() if lse is not None else None, ws.data_ptr(),
@@ -891,21 +898,22 @@ def quantize_fp8(weight: torch.Tensor, *, out=None, stream=None):
     floating point: returns (q [V][d] float8_e4m3fn, scale
     [ceil(V/128)][ceil(d/128)] float32), one power-of-two scale per 128 x 128
     block."""
-    _device_tensor(weight, "weight", (torch.float32, torch.bfloat16), 2)
-    if weight.stride(1) != 1:
-        raise ValueError("the last axis of weight must be contiguous")
+    index = _device_tensor(weight, "weight", _FLOATS, 2)
     V, d = weight.shape
-    dev = weight.device
-    blocks = ((V + 127) // 128, (d + 127) // 128)
-    with _on(dev, stream) as st:
+    if weight.stride(1) != 1 and d > 1:
+        raise ValueError("the last axis of weight must be contiguous")
+    dev, blocks = weight.device, ((V + 127) // 128, (d + 127) // 128)
+    st, ctx = _on(index, stream)
+    with ctx:
         if out is None:
             q = torch.empty((V, d), dtype=torch.float8_e4m3fn, device=dev)
             scale = torch.empty(blocks, dtype=torch.float32, device=dev)
         else:
             q = _out_tensor(out[0], (V, d), torch.float8_e4m3fn, dev, "out[0]")
             scale = _out_tensor(out[1], blocks, torch.float32, dev, "out[1]")
-        rc = lib().spec_quantize_fp8(weight.data_ptr(), _dtype_code(weight), weight.stride(0), V, d,
-                                     q.data_ptr(), scale.data_ptr(), st)
+        rc = lib().spec_quantize_fp8(weight.data_ptr(), _dtype_code(weight),
+                                     weight.stride(0) if V > 1 else d, V, d, q.data_ptr(),
+                                     scale.data_ptr(), st)
     _check(rc, "spec_quantize_fp8")
     return q, scale
 
@@ -918,28 +926,34 @@ def lmhead_fp8(hidden: torch.Tensor, weight: torch.Tensor, weight_scale: torch.T
     scale each) and weight [V][d] float8_e4m3fn with weight_scale
     [ceil(V/128)][ceil(d/128)] float32 (quantize_fp8, or a checkpoint's own).
     The logits, float32 or bfloat16, are what the verify calls take."""
-    _device_tensor(hidden, "hidden", (torch.float32, torch.bfloat16), 3)
-    dev = hidden.device
-    _device_tensor(weight, "weight", torch.float8_e4m3fn, 2, dev)
+    index = _device_tensor(hidden, "hidden", _FLOATS, 3)
+    _device_tensor(weight, "weight", (torch.float8_e4m3fn,), 2, index)
     B, rows, d = hidden.shape
     V = weight.shape[0]
-    if hidden.stride(2) != 1 or weight.stride(1) != 1 or weight.shape[1] != d:
+    hs = hidden.stride()
+    if weight.shape[1] != d or (d > 1 and (hs[2] != 1 or weight.stride(1) != 1)):
         raise ValueError("expected hidden [B][rows][d] and weight [V][d] with contiguous last axes")
-    scale = _out_tensor(weight_scale, ((V + 127) // 128, (d + 127) // 128), torch.float32, dev,
-                        "weight_scale")
-    need = lib().spec_lmhead_fp8_workspace(B, rows, d)
+    dev = hidden.device
+    _out_tensor(weight_scale, ((V + 127) // 128, (d + 127) // 128), torch.float32, dev, "weight_scale")
+    if out is not None:
+        _device_tensor(out, "out", _FLOATS, 3, index)
+        if tuple(out.shape) != (B, rows, V):
+            raise ValueError("out must be [%d][%d][%d], got %s" % (B, rows, V, tuple(out.shape)))
+    elif out_dtype not in _FLOATS:
+        raise TypeError("logits must be float32 or bfloat16, got %s" % out_dtype)
+    L = lib()
+    need = L.spec_lmhead_fp8_workspace(B, rows, d)
     if need == 0:
         _check(SPEC_ERR_INVALID_ARG, "spec_lmhead_fp8_workspace")
-    with _on(dev, stream) as st:
+    st, ctx = _on(index, stream)
+    with ctx:
         if out is None:
             out = torch.empty((B, rows, V), dtype=out_dtype, device=dev)
-        elif tuple(out.shape) != (B, rows, V) or out.device != dev:
-            raise ValueError("out must be [%d][%d][%d] on %s" % (B, rows, V, dev))
         ws = _scratch(workspace, dev, need)
-        h = spec_logits_t(hidden.data_ptr(), _dtype_code(hidden), 0, _stride(hidden, 0),
-                          _stride(hidden, 1))
-        rc = lib().spec_lmhead_fp8(h, B, rows, d, weight.data_ptr(), max(weight.stride(0), d),
-                                   scale.data_ptr(), V, _logits(out, rows), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(), st)
+        h = spec_logits_t(hidden.data_ptr(), _dtype_code(hidden), 0, hs[0] if B > 1 else 0,
+                          hs[1] if rows > 1 else 0)
+        rc = L.spec_lmhead_fp8(h, B, rows, d, weight.data_ptr(), weight.stride(0) if V > 1 else d,
+                               weight_scale.data_ptr(), V, _logits(out, rows), ws.data_ptr(),
+                               ws.numel() * ws.element_size(), st)
     _check(rc, "spec_lmhead_fp8")
     return out
