@@ -922,100 +922,112 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   note();
 }
 
-// Joins each cut segment's records, in order.  A workgroup takes four rows: of
-// a segment in few records a wave each, else every wave all four rows of a
-// quarter of the records, so that enough loads are under way.
-template <int D, int ROWS, int N>
+// Sums the records x0 .. x1 - 1 of a row, eight of them under way at a time.
+template <int D>
 __device__ __forceinline__ void c4_gather(const float* first, const float* rest, int64_t floats, int rows,
-                                          int row, int32_t x0, int32_t x1, int lane, float (&m)[ROWS],
-                                          float (&l)[ROWS], float (&v)[ROWS][D / 64]) {
-  constexpr int E = D / 64;
+                                          int row, int32_t x0, int32_t x1, int lane, float& m, float& l,
+                                          float (&v)[D / 64]) {
+  constexpr int E = D / 64, N = 8;
+  m = kC4Low;
+  l = 0.f;
 #pragma unroll
-  for (int y = 0; y < ROWS; ++y) {
-    m[y] = kC4Low;
-    l[y] = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[y][e] = 0.f;
-  }
+  for (int e = 0; e < E; ++e) v[e] = 0.f;
   for (int32_t base = x0; base < x1; base += N) {
-    float pm[N][ROWS], pl[N][ROWS], o[N][ROWS][E];
+    float pm[N], pl[N], o[N][E];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int32_t x = min(base + k, x1 - 1);
       const float* p = x == 0 ? first : rest + x * floats;
+      pm[k] = p[rows * D + row];
+      pl[k] = p[rows * D + rows + row];
 #pragma unroll
-      for (int y = 0; y < ROWS; ++y) {
-        pm[k][y] = p[rows * D + row + y];
-        pl[k][y] = p[rows * D + rows + row + y];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[k][y][e] = p[(row + y) * D + lane * E + e];
-      }
+      for (int e = 0; e < E; ++e) o[k][e] = p[row * D + lane * E + e];
     }
 #pragma unroll
     for (int k = 0; k < N; ++k)
       if (base + k < x1) {
+        const float top = fmaxf(m, pm[k]);
+        const float f = __builtin_amdgcn_exp2f(m - top), g = __builtin_amdgcn_exp2f(pm[k] - top);
+        m = top;
+        l = l * f + pl[k] * g;
 #pragma unroll
-        for (int y = 0; y < ROWS; ++y) {
-          const float top = fmaxf(m[y], pm[k][y]);
-          const float f = __builtin_amdgcn_exp2f(m[y] - top), g = __builtin_amdgcn_exp2f(pm[k][y] - top);
-          m[y] = top;
-          l[y] = l[y] * f + pl[k][y] * g;
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[y][e] = v[y][e] * f + o[k][y][e] * g;
-        }
+        for (int e = 0; e < E; ++e) v[e] = v[e] * f + o[k][e] * g;
       }
   }
 }
 
+// Joins the cut segments of calls with many of them, of few records each: four
+// rows a workgroup, a wave each, for the segment that workgroup blockIdx.x of
+// the attention began, if others end it.
 template <int D, int RT>
 __global__ __launch_bounds__(256) void k_attention_cache4_join(C4AttnArgs A) {
   constexpr int kRows = RT * 16, E = D / 64;  // E columns a lane
   constexpr int64_t kFloats = C4Rec<D, RT>::kFloats;
-  __shared__ float vs[4][4][D], ms[4][4], ls[4][4];  // [quarter of the records][row]
   const auto* cp = A.cuts + blockIdx.x;
   const int32_t parts = c4_scalar(&cp->parts);
   if (parts == 0) return;
   const int32_t b = c4_scalar(&cp->b), hr = c4_scalar(&cp->hr), slot = c4_scalar(&cp->slot);
   const int32_t nnew = c4_scalar(&cp->nnew);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t row = blockIdx.y * 4 + w, h = hr / A.row_blocks;
+  const int32_t r = hr % A.row_blocks * kRows + row, i = r / A.G;
+  if (r >= A.T * A.G || i >= nnew) return;
   const float* rest = A.parts + (int64_t)blockIdx.x * 2 * kFloats;
-  const float* first = rest + slot * kFloats;
   float m, l, v[E];
-  if (parts <= 8) {
-    float m1[1], l1[1], v1[1][E];
-    c4_gather<D, 1, 4>(first, rest, 2 * kFloats, kRows, blockIdx.y * 4 + w, 0, parts, lane, m1, l1, v1);
-    m = m1[0], l = l1[0];
+  c4_gather<D>(rest + slot * kFloats, rest, 2 * kFloats, kRows, row, 0, parts, lane, m, l, v);
+  c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l);
+}
+
+// Joins those of calls with few segments of many records: a row a workgroup, a
+// quarter of the records a wave.  Where the records stand follows from the
+// lengths alone, as in the attention.
+template <int D, int RT>
+__global__ __launch_bounds__(256) void k_attention_cache4_join_long(C4AttnArgs A) {
+  constexpr int kRows = RT * 16, E = D / 64;
+  constexpr int64_t kFloats = C4Rec<D, RT>::kFloats;
+  __shared__ float vs[4][D], ms[4], ls[4];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t per = (A.B + 63) / 64, HR = A.cache.heads * A.row_blocks;
+  const int32_t b = blockIdx.x / HR, hr = blockIdx.x % HR, row = blockIdx.y;
+  const int32_t h = hr / A.row_blocks, r = hr % A.row_blocks * kRows + row, i = r / A.G;
+  int64_t before;
+  const int64_t share = c4_share(c4_plan(A, lane, per, before) * HR);
+  bool bad;
+  int64_t at = c4_lane(before, b / per);
+  for (int32_t x = b / per * per; x < b; ++x) at += c4_weight(c4_pages<true>(A, x, bad));
+  const int32_t pages = c4_pages<true>(A, b, bad);
+  const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
+  if (pages == 0 || r >= A.T * A.G || i >= nnew) return;
+  const int64_t seg = at * HR + hr * c4_weight(pages);
+  // the workgroups that hold its first and last page
+  const int32_t w0 = c4_div(seg + kC4SegCost, (int32_t)share);
+  const int32_t parts = c4_div(seg + kC4SegCost + pages - 1, (int32_t)share) - w0 + 1;
+  if (parts == 1) return;  // written whole
+  const float* rest = A.parts + (int64_t)w0 * 2 * kFloats;
+  const float* first = rest + (seg > w0 * share ? kFloats : 0);
+  float m, l, v[E];
+  const int32_t quarter = (parts + 3) / 4;
+  c4_gather<D>(first, rest, 2 * kFloats, kRows, row, w * quarter, min(parts, w * quarter + quarter), lane, m, l, v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = v1[0][e];
-  } else {
-    float m4[4], l4[4], v4[4][E];
-    const int32_t per = (parts + 3) / 4;
-    c4_gather<D, 4, 4>(first, rest, 2 * kFloats, kRows, blockIdx.y * 4, w * per, min(parts, w * per + per),
-                       lane, m4, l4, v4);
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) vs[w][y][lane * E + e] = v4[y][e];
-      if (lane == 0) {
-        ms[w][y] = m4[y];
-        ls[w][y] = l4[y];
-      }
-    }
-    __syncthreads();
-    m = fmaxf(fmaxf(ms[0][w], ms[1][w]), fmaxf(ms[2][w], ms[3][w]));
-    l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.f;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const float f = __builtin_amdgcn_exp2f(ms[x][w] - m);
-      l += ls[x][w] * f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] += vs[x][w][lane * E + e] * f;
-    }
+  for (int e = 0; e < E; ++e) vs[w][lane * E + e] = v[e];
+  if (lane == 0) {
+    ms[w] = m;
+    ls[w] = l;
   }
-  const int32_t h = hr / A.row_blocks, r = hr % A.row_blocks * kRows + blockIdx.y * 4 + w, i = r / A.G;
-  if (r < A.T * A.G && i < nnew) c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l);
+  __syncthreads();
+  if (w) return;
+  m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const float f = __builtin_amdgcn_exp2f(ms[x] - m);
+    l += ls[x] * f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] += vs[x][lane * E + e] * f;
+  }
+  c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l);
 }
 
 }  // namespace sv

@@ -113,6 +113,9 @@ void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
 // Sequences of at most this many pages are not cut: the pass that joins cut
 // ones costs more than a workgroup's time over four pages a wave.
 constexpr int32_t kAttnWhole = 16;
+// Up to this many segments (sequences x heads x blocks of rows) each is in eight
+// records or more on average, and their rows are joined by a workgroup each.
+constexpr int64_t kAttnFew = sv::kC4Grid / 8;
 
 int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
   if (B < 1 || T < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads) return SPEC_ERR_INVALID_ARG;
@@ -132,7 +135,11 @@ size_t attention_workspace(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t
 template <int D, int RT>
 void launch_attention(const sv::C4AttnArgs& A, hipStream_t st) {
   hipLaunchKernelGGL((sv::k_attention_cache4<D, RT>), dim3(sv::kC4Grid), dim3(256), 0, st, A);
-  if (A.split)
+  if (!A.split) return;
+  const int64_t segments = int64_t(A.B) * A.cache.heads * A.row_blocks;
+  if (segments <= kAttnFew)
+    hipLaunchKernelGGL((sv::k_attention_cache4_join_long<D, RT>), dim3(unsigned(segments), RT * 16), dim3(256), 0, st, A);
+  else
     hipLaunchKernelGGL((sv::k_attention_cache4_join<D, RT>), dim3(sv::kC4Grid, RT * 4), dim3(256), 0, st, A);
 }
 template <int D>
