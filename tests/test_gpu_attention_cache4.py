@@ -252,3 +252,85 @@ def test_captured_calls():
             want = sv.attention_cache4(qq, pages, t, start, return_lse=True)
             assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     assert len(pages) == n
+
+
+@pytest.mark.parametrize("B,T,Hq,H,D,lo,hi,kind", [
+    (40, 6, 16, 2, 128, 0, 1500, "chain"),     # sequences of one page beside ones over several workgroups
+    (24, 21, 16, 4, 64, 1000, 1400, "tree"),   # two blocks of rows to a head
+    (5, 9, 16, 8, 256, 900, 2200, "chain"),    # few segments, each over many workgroups
+    (33, 2, 2, 2, 64, 0, 1300, "counts"),      # some without a new token
+    (3, 40, 8, 2, 128, 0, 9000, "tree"),
+    (70, 3, 4, 2, 128, 1100, 1500, "faults"),  # ill-formed ones and pages outside the pool between them
+    (6, 3, 8, 2, 128, 3000, 6000, "faults"),
+])
+def test_sequences_cut_over_workgroups(B, T, Hq, H, D, lo, hi, kind):
+    rs = np.random.default_rng([B, T, D])
+    start = rs.integers(lo, hi + 1, B)
+    q, pages, table = _case(11, B, T, Hq, H, D, list(start))
+    count, see = [T] * B, np.tril(np.ones((T, T), bool))[None].repeat(B, 0)
+    kw, gone = {}, []
+    if kind == "tree":
+        par = [-1] + [int(rs.integers(0, i)) for i in range(1, T)]
+        one = np.zeros((T, T), bool)
+        for i in range(T):
+            one[i] = one[par[i]] if i else one[i]
+            one[i, i] = True
+        see, kw["mask"] = one[None].repeat(B, 0), sv.tree_mask(par).to(DEV)
+    if kind == "counts":
+        count = rs.integers(0, T + 1, B).tolist()
+    if kind == "faults":
+        count = rs.integers(0, T + 1, B).tolist()
+        gone = [0, 2, B - 1]
+        start[0], count[2], count[B - 1] = -1, T + 1, 2
+        table[B - 1, int(start[B - 1]) // 128] = len(pages)
+    out, lse = _run(q, pages, table, list(start), count if "mask" not in kw else None, **kw)
+    new = [T if b in gone[:2] else count[b] for b in range(B)]
+    live = torch.arange(T, device=DEV)[None] < _i32(new)[:, None]
+    assert (out[~live] == 7).all() and (lse[~live] == 7).all()
+    for b in gone:
+        assert torch.isnan(out[b][live[b]]).all() and torch.isnan(lse[b][live[b]]).all()
+        live[b] = False
+        table[b], start[b] = 0, 0
+    K, V = sv.cache4_read(pages, _i32(table), _i32([0] * B), table.shape[1] * 64, D, dtype=torch.float32)
+    L = int((start + T).max())
+    x = torch.arange(L, device=DEV)[None, None] - _i32(start)[:, None, None]
+    sees = (x < 0) | (torch.gather(torch.tensor(see, device=DEV), 2, x.clamp(0, T - 1).expand(B, T, L)) & (x < T))
+    for b in range(B):
+        kb, vb = (y[b, :L].double().repeat_interleave(Hq // H, 1).transpose(0, 1).contiguous() for y in (K, V))
+        qb = q[b].double().transpose(0, 1).contiguous()  # [Hq][T][D]
+        s = (qb @ kb.transpose(1, 2).contiguous() / D ** 0.5).masked_fill(~sees[b][None], -float("inf"))
+        p = torch.softmax(s, -1)
+        want, mag = p @ vb, p @ vb.abs()
+        most = (qb.abs() @ kb.abs().transpose(1, 2).contiguous()).max() / D ** 0.5
+        few = most * 2 * (D + 2) * 2.0 ** -24 + 2.0 ** -21 + L * 2.0 ** -24
+        off = (out[b].double().transpose(0, 1) - want).abs()
+        ok = off <= (2.0 ** -8 + few) * (mag * (1 + 2.0 ** -8) + want.abs())
+        assert ok[:, live[b]].all(), b
+        l = torch.logsumexp(s, -1)
+        ok = (lse[b].double().t() - l).abs() <= few + l.abs() * 2.0 ** -21
+        assert ok[:, live[b]].all(), b
+
+
+@pytest.mark.parametrize("T,Hq,H,D", [(256, 2, 1, 64), (1, 128, 1, 128), (2, 96, 2, 256)])
+def test_many_rows_to_a_head(T, Hq, H, D):
+    start = [70]
+    q, pages, table = _case(12, 1, T, Hq, H, D, start)
+    _check(q, pages, table, start, None, _chain, _run(q, pages, table, start))
+
+
+def test_a_pool_past_32_bits():
+    """Records past 4 GiB of a pool, read and written there as in a small one."""
+    B, T, Hq, H, D, start = 2, 3, 16, 8, 256, [1200, 70]
+    q, pages, table = _case(13, B, T, Hq, H, D, start)
+    n, P = 40000, table.shape[1]
+    big = torch.empty(n, H, 68 * D, dtype=torch.uint8, device=DEV)
+    far = n - 1 - np.arange(B * P).reshape(B, P)
+    big[torch.tensor(far, device=DEV).view(-1)] = pages[torch.tensor(table, device=DEV).long().view(-1)]
+    k, v = (torch.randn(B, T, H, D, device=DEV).bfloat16() for _ in range(2))
+    for pool, t in ((pages, table), (big, far)):
+        sv.cache4_write(pool, _i32(t), _i32(start), k, v)
+    for a, b in zip(_run(q, pages, table, start), _run(q, big, far, start)):
+        assert torch.equal(a, b)
+    for a, b in zip(sv.cache4_read(pages, _i32(table), _i32(start), T, D),
+                    sv.cache4_read(big, _i32(far), _i32(start), T, D)):
+        assert torch.equal(a, b)

@@ -122,3 +122,56 @@ def test_logits_go_to_verify():
     u = torch.full((B, k + 1), 0.5, device=DEV)
     acc2, out2 = sv.verify_stochastic(logits, logits[:, :k].contiguous(), top[:, :k].contiguous(), u, top_k=1)
     assert acc2.tolist() == [k] * B and torch.equal(out2[:, k], top[:, k])
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,rows,V,d", [
+    (1, 1, 515, 4096), (2, 8, 515, 4096),    # rows of weights a multiple of 4,096 bytes apart
+    (1, 9, 300, 4224), (1, 16, 131, 8192),   # longer rows of hidden states
+    (1, 3, 200, 8320),                       # longer than the kernel of few rows takes
+    (43, 3, 257, 128), (100, 5, 300, 160), (52, 5, 300, 96), (30, 35, 600, 64),
+])
+def test_logits_of_other_sizes(B, rows, V, d, out_dtype):
+    h, q, s = _head(5, B, rows, V, d, torch.bfloat16)
+    _check(h, q, s, sv.lmhead_fp8(h, q, s, out_dtype=out_dtype))
+
+
+@pytest.mark.parametrize("B,rows", [(1, 1), (1, 40), (2, 100)])
+def test_weights_past_32_bits(B, rows):
+    """The last entries of 4.9 GiB of weights, as in a head of those alone (the sums' order may differ)."""
+    V, d, tail = 640000, 8192, 1000 // 128 * 128
+    q = torch.zeros(V, d, dtype=torch.uint8, device=DEV)
+    q[V - tail:] = torch.randint(0, 120, (tail, d), device=DEV, dtype=torch.uint8)
+    q = q.view(torch.float8_e4m3fn)
+    s = torch.full((V // 128, d // 128), 2.0 ** -9, device=DEV)
+    h = torch.rand(B, rows, d, device=DEV).bfloat16()  # nothing cancels: the sums are the magnitudes
+    got = sv.lmhead_fp8(h, q, s)
+    want = sv.lmhead_fp8(h, q[V - tail:], s[-(tail // 128):].contiguous())
+    assert (got[..., : V - tail] == 0).all()
+    assert ((got[..., V - tail:] - want).abs() <= 2 * (d + 160) * 2.0 ** -24 * want).all()
+
+
+def test_captured_and_on_two_streams():
+    """Heads captured on two streams and replayed at once, with new hidden states between the
+    replays: the eager call's bits each time."""
+    jobs = []
+    for B in (3, 50):
+        h, q, s = _head(6, B, 4, 515, 288, torch.bfloat16)
+        g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            sv.lmhead_fp8(h, q, s)
+        torch.cuda.current_stream().wait_stream(st)
+        with torch.cuda.graph(g):
+            out = sv.lmhead_fp8(h, q, s)
+        jobs.append((h, q, s, g, out, st))
+    for turn in range(3):
+        for h, *_ in jobs:
+            h.mul_(-1.5)
+        torch.cuda.synchronize()
+        for *_, g, _, st in jobs:
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for h, q, s, _, out, _ in jobs:
+            assert torch.equal(out, sv.lmhead_fp8(h, q, s))

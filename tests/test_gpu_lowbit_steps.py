@@ -98,3 +98,48 @@ def test_tree_step():
         # up to its lag, so bf16 probabilities may round apart
         assert (chain.double() - tree[:, path].double()).abs().max() <= 2.0 ** -6
         assert (l2 - lse[:, path]).abs().max() <= 1e-5
+
+
+def test_a_captured_step():
+    """Write, attention, head and verify as one graph, replayed on the lengths that each replay
+    leaves, against the same step called one by one on a pool of its own."""
+    rs = np.random.default_rng(5)
+    B, k, H, G, D, V = 2, 2, 2, 4, 64, 515
+    T, dm = k + 1, H * G * D
+    emb, wq, wk, wv = _weights(rs, V, dm), _weights(rs, dm, dm), _weights(rs, H * D, dm), _weights(rs, H * D, dm)
+    head, scale = sv.quantize_fp8(_weights(rs, V, dm))
+    table = torch.arange(B * 2, dtype=torch.int32, device=DEV).view(B, 2)
+    pools = [sv.cache4_alloc(B * 2, H, D, DEV) for _ in range(2)]
+    starts = [torch.tensor([0, 62], dtype=torch.int32, device=DEV) for _ in range(2)]
+    tokens = [torch.tensor([[5, 6, 7], [8, 9, 10]], device=DEV) for _ in range(2)]
+    old = torch.tensor(rs.normal(0, 1, (B, 62, H, D)), dtype=torch.float32, device=DEV)
+    for p in pools:
+        sv.cache4_write(p, table, torch.zeros_like(starts[0]), old, -old)
+
+    def step(pages, start, tok):
+        x = emb[tok]
+        sv.cache4_write(pages, table, start, *((x @ w.t()).view(B, T, H, D).bfloat16() for w in (wk, wv)))
+        o = sv.attention_cache4((x @ wq.t()).view(B, T, H * G, D).bfloat16(), pages, table, start)
+        acc, out = sv.verify_greedy(sv.lmhead_fp8(o.view(B, T, dm), head, scale), tok[:, 1:].int())
+        start.add_(acc + 1)
+        tok[:, :1] = out.gather(1, acc.long()[:, None])
+        tok[:, 1:] = out[:, :k].clamp_min(0)
+        return acc, out
+
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    begun = [x.clone() for x in (pools[1], starts[1], tokens[1])]
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step(pools[1], starts[1], tokens[1])
+    torch.cuda.current_stream().wait_stream(st)
+    with torch.cuda.graph(g):
+        made = step(pools[1], starts[1], tokens[1])
+    for x, y in zip((pools[1], starts[1], tokens[1]), begun):
+        x.copy_(y)
+    for _ in range(6):
+        want = step(pools[0], starts[0], tokens[0])
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(made[0], want[0]) and torch.equal(made[1], want[1])
+        assert torch.equal(pools[0], pools[1]) and torch.equal(starts[0], starts[1])
+    assert int(starts[0][1]) > 64  # over a page's end
