@@ -3,6 +3,7 @@
 // include/specverify_lowbit.h for the contract of every entry point.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -17,6 +18,7 @@ constexpr int32_t kMaxB = 1 << 16;         // sequences of a cache call
 constexpr int32_t kMaxNew = 1 << 24;       // new tokens of a sequence in a cache call
 constexpr int32_t kMaxTableCols = 1 << 24;  // positions stay below 2^30
 constexpr int32_t kMaxQHeads = 16384;
+constexpr int64_t kMaxWeightStride = 1 << 22;  // a tile's 256 rows have 32-bit offsets
 
 size_t elem_size(int dtype) { return dtype == SPEC_DTYPE_BF16 ? 2 : 4; }
 bool dtype_ok(int dtype) { return dtype == SPEC_DTYPE_F32 || dtype == SPEC_DTYPE_BF16; }
@@ -47,12 +49,27 @@ int check_heads(const spec_heads_t& x) {
   return SPEC_OK;
 }
 
-// Rows that are written must not share elements: every stride of an axis
-// longer than one is at least a head's width.
+// Whether rows of `width` elements along axes of n steps lie apart: with the
+// axes by stride, each steps over all that the ones before it cover.
+struct Axis {
+  int64_t n, stride;
+};
+template <int N>
+bool apart(Axis (&x)[N], int64_t width) {
+  std::sort(x, x + N, [](const Axis& a, const Axis& b) { return a.stride < b.stride; });
+  __int128 covered = width;
+  for (const Axis& a : x) {
+    if (a.n == 1) continue;
+    if (a.stride < covered) return false;
+    covered += __int128(a.n - 1) * a.stride;
+  }
+  return true;
+}
+
+// Rows that are written must not share elements.
 int check_written(const spec_heads_t& x, int64_t B, int64_t T, int64_t heads, int64_t d) {
-  if ((B > 1 && x.seq_stride < d) || (T > 1 && x.pos_stride < d) || (heads > 1 && x.head_stride < d))
-    return SPEC_ERR_INVALID_ARG;
-  return SPEC_OK;
+  Axis axes[] = {{B, x.seq_stride}, {T, x.pos_stride}, {heads, x.head_stride}};
+  return apart(axes, d) ? SPEC_OK : SPEC_ERR_INVALID_ARG;
 }
 
 int check_new(int32_t B, int32_t T, const int32_t* start) {
@@ -313,14 +330,15 @@ int spec_lmhead_fp8(spec_logits_t hidden, int32_t B, int32_t rows, int32_t d, co
   if (B > (1 << 24) || rows > 2 * SPEC_MAX_K + 1) return SPEC_ERR_UNSUPPORTED;
   if ((rc = check_head(weight, weight_stride, V, d)) != SPEC_OK) return rc;
   if (weight_stride < d || !scale || !aligned(scale, 4)) return SPEC_ERR_INVALID_ARG;
+  if (weight_stride > kMaxWeightStride) return SPEC_ERR_UNSUPPORTED;
   if (!dtype_ok(hidden.dtype) || !dtype_ok(logits.dtype)) return SPEC_ERR_UNSUPPORTED;
   const int64_t per = int64_t(16 / elem_size(hidden.dtype));
   if (!hidden.data || !aligned(hidden.data, 16) || hidden.seq_stride < 0 || hidden.pos_stride < 0 ||
       hidden.seq_stride % per || hidden.pos_stride % per)
     return SPEC_ERR_INVALID_ARG;
   // written rows must not share elements
-  if (!logits.data || !aligned(logits.data, elem_size(logits.dtype)) ||
-      (rows > 1 && logits.pos_stride < V) || (B > 1 && logits.seq_stride < V))
+  Axis axes[] = {{B, logits.seq_stride}, {rows, logits.pos_stride}};
+  if (!logits.data || !aligned(logits.data, elem_size(logits.dtype)) || !apart(axes, V))
     return SPEC_ERR_INVALID_ARG;
   const int64_t M = int64_t(B) * rows, dp = padded(d);
   const int64_t rounding = (M * (dp / 128) + 15) / 16;

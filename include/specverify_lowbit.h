@@ -71,7 +71,9 @@ typedef struct {
 /* Heads of positions: element (b, i, h, x) at
  *   data[b * seq_stride + i * pos_stride + h * head_stride + x]
  * (strides in elements).  data and the byte sizes of all strides are
- * multiples of 16. */
+ * multiples of 16; the stride of an axis of one step is not used.  Rows that a
+ * call writes lie apart: with the axes in the order of their strides, each
+ * steps over all that the ones before it cover. */
 typedef struct {
   void* data;
   int32_t dtype; /* spec_dtype_t */
@@ -114,7 +116,8 @@ int spec_cache4_read(spec_cache4_t cache, spec_heads_t k, spec_heads_t v, int32_
  *         the normaliser are F32
  *   lse   [B][T][q_heads] F32 or NULL
  * Rows i >= count[b] of out and lse are left as they were.
- * Limits: q_heads a multiple of heads, at most 16384; T <= SPEC_CACHE4_MAX_T.
+ * Limits: q_heads a multiple of heads, at most 16384; T <= SPEC_CACHE4_MAX_T;
+ * B (table_cols + 6) heads ceil(T q_heads / heads / 32) below 2^40.
  * workspace: spec_attention_cache4_workspace bytes, 256-byte aligned. */
 #define SPEC_CACHE4_MAX_T 256
 size_t spec_attention_cache4_workspace(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
@@ -142,9 +145,11 @@ int spec_quantize_fp8(const void* weight, int32_t dtype, int64_t weight_stride, 
  * where h8 is the hidden row rounded to e4m3 in blocks of 128 with a
  * power-of-two scale each, by the rule of spec_quantize_fp8.
  *   hidden  [B][rows][d] F32 or BF16, strides in elements; rows 16-byte aligned
- *   weight  [V][d] e4m3, row v at v * weight_stride bytes (a multiple of 16)
+ *   weight  [V][d] e4m3, row v at v * weight_stride bytes (a multiple of 16, at
+ *           most 2^22)
  *   scale   [ceil(V/128)][ceil(d/128)] F32, any finite values, contiguous
- *   logits  [B][rows][V] F32 or BF16 (spec_logits_t addressing, written)
+ *   logits  [B][rows][V] F32 or BF16 (spec_logits_t addressing, written; its
+ *           rows lie apart)
  * F32 logits are sums held in F32.  BF16 logits may be summed by the 8-bit
  * matrix instructions, which add neighbouring products to about 14 bits
  * before the F32 sum; their rounding to BF16 is the larger one.

@@ -334,3 +334,14 @@ def test_a_pool_past_32_bits():
     for a, b in zip(sv.cache4_read(pages, _i32(table), _i32(start), T, D),
                     sv.cache4_read(big, _i32(far), _i32(start), T, D)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("start", [[0, 5], [1100, 70]])
+def test_no_new_tokens(start):
+    q, pages, table = _case(14, 2, 2, 2, 1, 64, start)
+    out, lse = _run(q, pages, table, start, [0, 0])
+    assert (out == 7).all() and (lse == 7).all()
+    K = torch.ones(2, 2, 1, 64, device=DEV)
+    before = pages.clone()
+    sv.cache4_write(pages, _i32(table), _i32(start), K, K, count=_i32([0, 0]))
+    assert torch.equal(pages, before)

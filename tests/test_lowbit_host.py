@@ -113,6 +113,38 @@ def test_attention_refusals():
     assert call(w=None) == WS and call(wb=16) == WS and call(w=ctypes.c_void_p((1 << 20) + 16)) == WS
 
 
+def test_refusals_of_written_rows_that_meet():
+    """Strides that are each wide enough and yet put two rows in one place."""
+    L, p, ws = sv.lib(), ctypes.c_void_p(1 << 16), ctypes.c_void_p(1 << 20)
+
+    def read(k, B=2, T=3):
+        return L.spec_cache4_read(_cache(), k, _heads(), B, T, p, None, None)
+
+    def head(out, B=2, rows=5):
+        return L.spec_lmhead_fp8(sv.spec_logits_t(1 << 16, 0, 0, 1280, 256), B, rows, 256, p, 256, p, 300, out, ws,
+                                 1 << 30, None)
+
+    for kw in (dict(seq=128), dict(seq=512), dict(pos=128), dict(seq=256, pos=256), dict(seq=1 << 62, pos=128)):
+        assert read(_heads(**kw)) == BAD, kw
+    assert head(sv.spec_logits_t(1 << 16, 0, 0, 300, 300)) == BAD
+    assert head(sv.spec_logits_t(1 << 16, 0, 0, 1499, 300)) == BAD
+    assert head(sv.spec_logits_t(1 << 16, 0, 0, 300, 599)) == BAD
+
+
+def test_limits():
+    L, p, ws = sv.lib(), ctypes.c_void_p(1 << 16), ctypes.c_void_p(1 << 20)
+    x = sv.spec_logits_t(1 << 16, 0, 0, 1500, 300)
+    for stride, want in (((1 << 22) + 16, UNSUP), (1 << 40, UNSUP), (1 << 22, WS)):
+        assert L.spec_lmhead_fp8(sv.spec_logits_t(1 << 16, 0, 0, 1280, 256), 2, 5, 256, p, stride, p, 300, x, ws, 0,
+                                 None) == want
+    cols = 1 << 24
+    cache = _cache(cols=cols, stride=cols, heads=1024)
+    wide = _heads(seq=1 << 40, pos=1 << 20, head=128)
+    for B, want in ((1 << 16, UNSUP), (1, WS)):
+        assert L.spec_attention_cache4(cache, wide, B, 1, 1024, p, None, None, 0, 0, 0.1, wide, None, ws, 0,
+                                       None) == want
+
+
 def test_head_refusals():
     L, p = sv.lib(), ctypes.c_void_p(1 << 16)
     ws = ctypes.c_void_p(1 << 20)
