@@ -134,6 +134,7 @@ struct F8HeadArgs {
   int32_t v_tiles, m_tiles;
 };
 
+typedef int f8_i32x4 __attribute__((ext_vector_type(4)));
 typedef int f8_i32x8 __attribute__((ext_vector_type(8)));
 
 // Bytes 8 h .. 8 h + 7 of a lane's 16 as bf16 times `scale` (a power of two).
@@ -279,28 +280,28 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_rows(F8HeadArgs A) {
   }
 }
 
-// More rows: a matrix product in tiles of BV entries x BM rows, eight waves in
+// More rows: a matrix product in tiles of BV entries x BM rows, WAVES waves in
 // WV x WM, the operands' blocks of 128 columns (one row of 128 bytes each)
-// through two LDS buffers that the memory pipeline fills by itself
+// through two LDS buffers each that the memory pipeline fills by itself
 // (buffer_load ... lds, 16 bytes a lane) while the matrix instructions work on
 // the other.  A row's eight 16-byte chunks are stored in the order
 // c ^ (row / 2 % 8), by permuting the addresses that the lanes load from, so that
 // the 16 rows a quarter of a fragment read touches (256 bytes) fall on the 64
 // banks without conflict.
-template <typename TO, bool F8, int BV, int BM, int WV>
-__global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
-  constexpr int WM = 8 / WV, TV = BV / WV / 16, TM = BM / WM / 16;  // a wave's tiles of 16
+template <typename TO, bool F8, int BV, int BM, int WV, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
+  constexpr int WM = WAVES / WV, TV = BV / WV / 16, TM = BM / WM / 16;  // a wave's tiles of 16
   static_assert(TV * WV * 16 == BV && TM * WM * 16 == BM, "whole tiles");
-  static_assert(BV % 64 == 0 && BM % 64 == 0, "8 rows a wave and load");
+  constexpr int kStep = 8 * WAVES;  // rows that one load of each wave brings
+  static_assert(BV % kStep == 0 && BM % kStep == 0, "whole loads");
   static_assert(128 % (BV / WV) == 0, "a wave's entries lie in one block of 128");
   static_assert(TV <= 4, "a column's tiles are added in four steps");
-  constexpr int kTiles = 256;  // a buffer: the rows' exponents, then the bytes of [weights | hidden]
-  static_assert(BM <= 256, "room");
-  constexpr int kBuf = kTiles + (BV + BM) * 128;
-  // two arrays, each named where it is used, so that the compiler can tell a
-  // fragment read of one from the fill of the other and does not wait for it
-  __shared__ __attribute__((aligned(16))) uint8_t buf0[kBuf];
-  __shared__ __attribute__((aligned(16))) uint8_t buf1[kBuf];
+  constexpr int kExps = 256;  // before the hidden rows' bytes: their exponents
+  static_assert(BM <= kExps, "room");
+  // arrays of their own, each named where it is used, so that the compiler can
+  // tell a fragment read of one from the fill of another and does not wait for it
+  __shared__ __attribute__((aligned(16))) uint8_t w0[BV * 128], w1[BV * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t h0[kExps + BM * 128], h1[kExps + BM * 128];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n16 = lane & 15, q = lane >> 4;
   // the workgroups of one XCD (blockIdx % 8) take neighbouring tiles, rows
@@ -324,28 +325,28 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
   const int row = 8 * w + lane / 8, chunk = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
   const int32_t woff = row * ws + chunk, hoff = row * A.dp + chunk;
   typedef __attribute__((address_space(3))) void* Lds;
-  // Load x of block kb's kLoads: eight rows of the weights or the hidden rows,
-  // and last (the first wave's) the exponents.
-  constexpr int kLoads = BV / 64 + BM / 64;
-  auto stage = [&](int32_t kb, uint8_t* to, int x) {
-    // one register per operand: the rows' offsets are added here, not kept
-    int32_t wo = woff, ho = hoff;
-    asm volatile("" : "+v"(wo), "+v"(ho));
-    if (x < BV / 64) {
-      // a column past d: the hidden row's zeros meet a zero
-      const bool in = kb * 128 + chunk < A.d;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc, (Lds)(to + kTiles + (64 * x + 8 * w) * 128), 16,
-                                               in ? wo + (kb * 128 + 64 * x * ws) : 0x7FFFFFFF, 0, 0, 0);
-    } else {
-      const int y = x - BV / 64;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(hsrc, (Lds)(to + kTiles + (BV + 64 * y + 8 * w) * 128), 16,
-                                               ho + (kb * 128 + 64 * y * A.dp), 0, 0, 0);
-    }
-    if (x == kLoads - 1 && w == 0)
+  // Load x of block kb's weights, and of its hidden rows, eight rows a wave; with
+  // the last one the first wave's load of the exponents.  The rows' offsets are
+  // added here, not kept in a register each.
+  constexpr int kWLoads = BV / kStep, kHLoads = BM / kStep;
+  auto stage_w = [&](int32_t kb, uint8_t* to, int x) {
+    int32_t wo = woff;
+    asm volatile("" : "+v"(wo));
+    // a column past d: the hidden row's zeros meet a zero
+    const bool in = kb * 128 + chunk < A.d;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wsrc, (Lds)(to + (kStep * x + 8 * w) * 128), 16,
+                                             in ? wo + (kb * 128 + kStep * x * ws) : 0x7FFFFFFF, 0, 0, 0);
+  };
+  auto stage_h = [&](int32_t kb, uint8_t* to, int x) {
+    int32_t ho = hoff;
+    asm volatile("" : "+v"(ho));
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(hsrc, (Lds)(to + kExps + (kStep * x + 8 * w) * 128), 16,
+                                             ho + (kb * 128 + kStep * x * A.dp), 0, 0, 0);
+    if (x == kHLoads - 1 && w == 0)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(esrc, (Lds)to, 4, (int32_t)(kb * A.m_pitch) + 4 * lane, 0, 0, 0);
   };
   auto chunk_of = [&](const uint8_t* from, int r, int c) {
-    return *reinterpret_cast<const uint4*>(from + kTiles + r * 128 + ((c ^ ((r >> 1) & 7)) * 16));
+    return *reinterpret_cast<const uint4*>(from + r * 128 + ((c ^ ((r >> 1) & 7)) * 16));
   };
 
   f8_f32x4 acc[TV][TM];
@@ -358,16 +359,26 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
   const auto* sp = (const __attribute__((address_space(4))) float*)(
       A.scale + min((v0 + vw) / 128, (A.V - 1) / 128) * blocks);
 
-  // Computes block kb and starts the loads of the next one: spread over the
-  // columns, for issued together they hold the wave (and, after a barrier, all
-  // of them) for 700 to 1,200 cycles of a block's 4,000.
-  auto compute = [&](int32_t kb, const uint8_t* from, uint8_t* to) {
+  // A barrier behind this wave's reads of LDS (__syncthreads would wait for all
+  // loads that are on their way to LDS too).
+  auto meet = [] {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  // Computes block kb from wa and ha and starts the loads of the next one's
+  // hidden rows (into hb) and, when every wave has its weights in registers, of
+  // the weights of the one after that (into wa): spread over the columns, for
+  // issued together they hold the wave (and, after a barrier, all of them) for
+  // 700 to 1,200 cycles of a block's 4,000.
+  constexpr int kH = TM / 2;  // columns with the hidden rows' loads
+  auto compute = [&](int32_t kb, uint8_t* wa, const uint8_t* ha, uint8_t* hn) {
     const float s = sp[kb];
     uint4 wf[TV][2];
 #pragma unroll
     for (int i = 0; i < TV; ++i)
 #pragma unroll
-      for (int y = 0; y < 2; ++y) wf[i][y] = chunk_of(from, vw + 16 * i + n16, 4 * y + q);
+      for (int y = 0; y < 2; ++y) wf[i][y] = chunk_of(wa, vw + 16 * i + n16, 4 * y + q);
     f8_bf16x8 wb[F8 ? 1 : TV][4];
     if constexpr (!F8)
 #pragma unroll
@@ -387,16 +398,22 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
     uint32_t e[2];
     auto rows = [&](int j) {
 #pragma unroll
-      for (int y = 0; y < 2; ++y) hf[j & 1][y] = chunk_of(from, BV + mw + 16 * j + n16, 4 * y + q);
-      e[j & 1] = from[mw + 16 * j + n16];
+      for (int y = 0; y < 2; ++y) hf[j & 1][y] = chunk_of(ha + kExps, mw + 16 * j + n16, 4 * y + q);
+      e[j & 1] = ha[mw + 16 * j + n16];
     };
     rows(0);
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
+      if (j == 1) meet();  // every wave has its weights
       if (j + 1 < TM) rows(j + 1);
-      if (kb + 1 < blocks) {
+      if (j < kH) {
 #pragma unroll
-        for (int x = kLoads * j / TM; x < kLoads * (j + 1) / TM; ++x) stage(kb + 1, to, x);
+        for (int x = kHLoads * j / kH; x < kHLoads * (j + 1) / kH; ++x) stage_h(kb + 1, hn, x);
+      }
+      if (j >= kH) {
+#pragma unroll
+        for (int x = kWLoads * (j - kH) / (TM - kH); x < kWLoads * (j + 1 - kH) / (TM - kH); ++x)
+          stage_w(kb + 2, wa, x);
       }
       if constexpr (F8) {
         const f8_i32x8 hb = f8_join(hf[j & 1][0], hf[j & 1][1]);
@@ -432,40 +449,52 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  // At each barrier the block to compute has arrived for every wave (each
-  // waits for its own loads first), and every wave is done with the buffer
-  // that the next one goes to.
-  auto arrive = [] {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+  // At each barrier the block to compute has arrived for every wave (each waits
+  // for its own loads first, but for those of the next block's weights, which
+  // are the last), and every wave is done with the buffers that are filled next.
+  // Loads past the last block read zeros or a row's next bytes and are not used:
+  // with a branch around them the compiler would wait for all.
+  auto arrive = [&] {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kWLoads) : "memory");
+    meet();
   };
 #pragma unroll
-  for (int x = 0; x < kLoads; ++x) stage(0, buf0, x);
+  for (int x = 0; x < kWLoads; ++x) stage_w(0, w0, x);
+#pragma unroll
+  for (int x = 0; x < kHLoads; ++x) stage_h(0, h0, x);
+#pragma unroll
+  for (int x = 0; x < kWLoads; ++x) stage_w(1, w1, x);
   int32_t kb = 0;
   for (; kb + 1 < blocks; kb += 2) {
     arrive();
-    compute(kb, buf0, buf1);
+    compute(kb, w0, h0, h1);
     arrive();
-    compute(kb + 1, buf1, buf0);
+    compute(kb + 1, w1, h1, h0);
   }
   if (kb < blocks) {
     arrive();
-    compute(kb, buf0, buf1);
+    compute(kb, w0, h0, h1);
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   // The tile leaves through LDS, so that a row's entries leave together: kOut
   // rows at a time, 512 bytes of a row (its 16-byte chunks in the order
   // c ^ (row % 32), for the banks), then 16 bytes a lane, or one entry a lane
-  // where the rows do not start at multiples of 16 bytes (240 rows of 128,003
-  // F32 entries: stored from the registers 0.26 ms, so 0.19).
-  constexpr int kOut = kBuf >= 128 * 512 ? 128 : kBuf >= 64 * 512 ? 64 : 32;
-  static_assert(BV * sizeof(TO) == 512 && kOut * 512 <= kBuf, "room");
+  // where the rows do not start at multiples of 16 bytes (of 240 rows of
+  // 128,003 F32 entries over 2,080, stores from the registers took 8 % more).  BF16
+  // logits go past the caches: with the verify call that reads them 240 rows of
+  // 128,000 over 4,096 take 178 us, else 185, and 2,560 rows of 151,936 1.69 and
+  // 1.72 ms; for F32 ones of 240 rows of 151,936 over 2,080 it would be 274 and 266.
+  constexpr int kRowBytes = BV * sizeof(TO), kChunks = kRowBytes / 16;
+  constexpr int kOut = 256 / (int)sizeof(TO) < BM ? 256 / (int)sizeof(TO) : BM;
+  static_assert(kOut / 2 * kRowBytes <= BV * 128, "room");
+  auto out_chunk = [&](int r, int c) { return (r & 1 ? w1 : w0) + r / 2 * kRowBytes + (c ^ (r & (kChunks - 1))) * 16; };
   constexpr int kRound = kOut / WM / 16;  // a wave's columns of tiles each time
   static_assert(TM % kRound == 0, "whole rounds");
   const bool vec = ((uintptr_t)A.out | (uintptr_t)(A.o_seq * sizeof(TO)) | (uintptr_t)(A.o_pos * sizeof(TO))) % 16 == 0;
 #pragma unroll
   for (int g = 0; g < TM / kRound; ++g) {
-    __syncthreads();  // every wave is done with the buffer
+    __syncthreads();  // every wave is done with the buffers
 #pragma unroll
     for (int j = 0; j < kRound; ++j) {
       const int r = (w % WM) * (kRound * 16) + 16 * j + n16;
@@ -473,31 +502,34 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
       for (int i = 0; i < TV; ++i) {
         const f8_f32x4 x = acc[i][g * kRound + j];
         const int at = (vw + 16 * i + 4 * q) * (int)sizeof(TO);  // 8 or 16 bytes
-        uint8_t* to = buf0 + r * 512 + (((at / 16) ^ (r & 31)) * 16) + at % 16;
+        uint8_t* to = out_chunk(r, at / 16) + at % 16;
         if constexpr (sizeof(TO) == 4) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
         else *reinterpret_cast<uint2*>(to) = f8_bf16x4(x);
       }
     }
     __syncthreads();
     if (vec) {
-      const int c = threadIdx.x & 31;
+      const int c = threadIdx.x % kChunks;
+      constexpr int kPass = 64 * WAVES / kChunks;
 #pragma unroll
-      for (int k = 0; k < kOut / 16; ++k) {
-        const int r = 16 * k + (threadIdx.x >> 5);
+      for (int k = 0; k < kOut / kPass; ++k) {
+        const int r = kPass * k + threadIdx.x / kChunks;
         const int64_t m = m0 + (r / (kRound * 16)) * (BM / WM) + g * kRound * 16 + r % (kRound * 16);
         constexpr int kPer = 16 / sizeof(TO);
         const int64_t v = v0 + c * kPer;
         if (m >= A.M || v >= A.V) continue;
         TO* row = f8_out_row<TO>(A, m);
-        const uint8_t* from = buf0 + r * 512 + ((c ^ (r & 31)) * 16);
+        const uint8_t* from = out_chunk(r, c);
         if (v + kPer <= A.V) {
-          *reinterpret_cast<uint4*>(row + v) = *reinterpret_cast<const uint4*>(from);
+          const f8_i32x4 x = *reinterpret_cast<const f8_i32x4*>(from);
+          if constexpr (sizeof(TO) == 2) __builtin_nontemporal_store(x, reinterpret_cast<f8_i32x4*>(row + v));
+          else *reinterpret_cast<f8_i32x4*>(row + v) = x;
         } else {
           for (int e = 0; v + e < A.V; ++e) row[v + e] = reinterpret_cast<const TO*>(from)[e];
         }
       }
     } else {
-      for (int r = w; r < kOut; r += 8) {
+      for (int r = w; r < kOut; r += WAVES) {
         const int64_t m = m0 + (r / (kRound * 16)) * (BM / WM) + g * kRound * 16 + r % (kRound * 16);
         if (m >= A.M) continue;
         TO* row = f8_out_row<TO>(A, m);
@@ -505,7 +537,7 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
         for (int k = 0; k < BV / 64; ++k) {
           const int x = 64 * k + lane, at = x * (int)sizeof(TO);
           if (v0 + x < A.V)
-            row[v0 + x] = *reinterpret_cast<const TO*>(buf0 + r * 512 + (((at / 16) ^ (r & 31)) * 16) + at % 16);
+            row[v0 + x] = *reinterpret_cast<const TO*>(out_chunk(r, at / 16) + at % 16);
         }
       }
     }

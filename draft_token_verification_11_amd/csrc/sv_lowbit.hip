@@ -178,34 +178,46 @@ int check_head(const void* weight, int64_t row_bytes, int32_t V, int32_t d) {
 
 int64_t padded(int32_t d) { return (int64_t(d) + 127) / 128 * 128; }
 
-template <typename TO, bool F8, int BV, int BM, int WV>
+template <typename TO, bool F8, int BV, int BM, int WV, int WAVES>
 void launch_head_tile(sv::F8HeadArgs A, hipStream_t st) {
   A.v_tiles = int32_t((A.V + BV - 1) / BV);
   A.m_tiles = int32_t((A.M + BM - 1) / BM);
   const int64_t tiles = int64_t(A.v_tiles) * A.m_tiles;
-  hipLaunchKernelGGL((sv::k_lmhead_fp8_tile<TO, F8, BV, BM, WV>), dim3(unsigned((tiles + 7) / 8 * 8)),
-                     dim3(512), 0, st, A);
+  hipLaunchKernelGGL((sv::k_lmhead_fp8_tile<TO, F8, BV, BM, WV, WAVES>), dim3(unsigned((tiles + 7) / 8 * 8)),
+                     dim3(64 * WAVES), 0, st, A);
 }
 // One workgroup per compute unit of the kernel for up to 16 rows.
 constexpr unsigned kHeadGrid = 256;
 
+// The kernel for M rows; times over 151,936 entries x 4,096.
 template <typename TO>
 void launch_head(const sv::F8HeadArgs& A, hipStream_t st) {
-  constexpr bool f8 = sizeof(TO) == 2;        // BF16 logits: the 8-bit instructions' sums do
-  constexpr int BV = 512 / int(sizeof(TO));   // 512 bytes of a row of logits
-  // Up to 16 rows whose LDS image fits (rows of 8,192).
+  constexpr bool f8 = sizeof(TO) == 2;  // BF16 logits: the 8-bit instructions' sums do
+  // Up to 16 rows whose LDS image fits (rows of 8,192): 0.124 ms, in tiles 0.134.
   if (A.M <= 16 && A.dp <= 8192) {
     if (A.dp <= 4096)
       hipLaunchKernelGGL((sv::k_lmhead_fp8_rows<TO, 32>), dim3(kHeadGrid), dim3(512), 0, st, A);
     else
       hipLaunchKernelGGL((sv::k_lmhead_fp8_rows<TO, 64>), dim3(kHeadGrid), dim3(512), 0, st, A);
-  } else if (A.M <= 64) {
-    launch_head_tile<TO, f8, BV, 64, f8 ? 8 : 4>(A, st);
-  } else if ((A.M + 127) / 128 * 128 < (A.M + 255) / 256 * 256) {  // fewer padded rows
-    launch_head_tile<TO, f8, BV, 128, f8 ? 4 : 2>(A, st);
-  } else {
-    launch_head_tile<TO, f8, BV, 256, f8 ? 4 : 2>(A, st);
+    return;
   }
+  // Up to 64 rows (24 rows over 32,000 entries: 0.034 ms, in tiles of 128 0.045).
+  if (A.M <= 64) {
+    launch_head_tile<TO, f8, 128, 64, 2, 4>(A, st);
+    return;
+  }
+  // Two workgroups of four waves a compute unit, which fill each other's waits
+  // (120 rows, F32: 0.188 ms, one of eight waves 0.224), and where the matrix
+  // instructions bind, one of eight with wave tiles of 64 x 128, which read LDS
+  // less (2,560 rows, BF16: 1.70 ms, in the small tiles 1.85), unless it pads
+  // more rows.  F32 logits need four times the instructions a block; there LDS
+  // does not bind (2,560 rows: 3.12 ms either way).
+  if constexpr (f8)
+    if ((A.M + 255) / 256 * 256 == (A.M + 127) / 128 * 128) {
+      launch_head_tile<TO, f8, 256, 256, 4, 8>(A, st);
+      return;
+    }
+  launch_head_tile<TO, f8, 128, 128, 2, 4>(A, st);
 }
 
 }  // namespace
@@ -343,7 +355,7 @@ int spec_lmhead_fp8(spec_logits_t hidden, int32_t B, int32_t rows, int32_t d, co
   const int64_t M = int64_t(B) * rows, dp = padded(d);
   const int64_t rounding = (M * (dp / 128) + 15) / 16;
   const int64_t tiles = ((int64_t(V) + 127) / 128) * ((M + 63) / 64);  // of the smallest kind, and a round of 8
-  if (!grid_fits(rounding, 256) || !grid_fits(tiles + 8, 512)) return SPEC_ERR_UNSUPPORTED;
+  if (!grid_fits(rounding, 256) || !grid_fits(tiles + 8, 256)) return SPEC_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < spec_lmhead_fp8_workspace(B, rows, d))
     return SPEC_ERR_WORKSPACE;
   auto st = static_cast<hipStream_t>(stream);
