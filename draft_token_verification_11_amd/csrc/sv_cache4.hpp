@@ -45,11 +45,6 @@ struct C4View {
     const int32_t x = table[b * table_stride + p];
     return (uint32_t)x < (uint32_t)n_pages ? x : -1;
   }
-  // As page(), for a wave's common b and p.
-  __device__ __forceinline__ int32_t page_of_wave(int64_t b, int32_t p) const {
-    const int32_t x = c4_scalar(table + b * table_stride + p);
-    return (uint32_t)x < (uint32_t)n_pages ? x : -1;
-  }
   template <int D>
   __host__ __device__ __forceinline__ uint8_t* record(int32_t page, int32_t h) const {
     return pages + ((int64_t)page * heads + h) * C4<D>::kRecord;
@@ -284,10 +279,8 @@ __global__ __launch_bounds__(256) void k_cache4_read(C4MoveArgs A) {
 // workgroup whose range cuts one of them leaves its rows' maximum, sum and
 // unnormalised output in the workspace, and k_attention_cache4_join adds those
 // up in order, so that results do not depend on the order of workgroups.
-// Workgroups of a call: two for each of 256 compute units, which is what fits
-// one.  Where fewer pages do not need them the rest end at once.
-constexpr int32_t kC4Grid = 512;
-
+// Of the workgroups of a call (as many as are in flight at once, see C4Shape)
+// those that its pages do not need end at once.
 struct C4AttnArgs {
   C4View cache;
   const uint16_t* q;
@@ -302,8 +295,8 @@ struct C4AttnArgs {
   int32_t B, T, G, row_blocks;
   float c;                // scale log2 e
   int32_t split;          // 0: no segment is cut, and there is nothing to join
-  struct C4Cut* cuts;     // [kC4Grid] the segment that a workgroup begins and others end
-  float* parts;           // [2 kC4Grid] records of a workgroup's first and last cut segment
+  struct C4Cut* cuts;     // [workgroups] the segment that a workgroup begins and others end
+  float* parts;           // [2 x workgroups] records of a workgroup's first and last cut segment
 };
 
 struct C4Cut {
@@ -397,8 +390,9 @@ __device__ __forceinline__ int64_t c4_find(const C4AttnArgs& A, int lane, int32_
 
 // The weight of each workgroup's range: an equal share, at least one page per
 // wave and a segment's cost.
+template <int GRID>
 __device__ __forceinline__ int64_t c4_share(int64_t weight) {
-  const int64_t s = (weight + kC4Grid - 1) / kC4Grid;
+  const int64_t s = (weight + GRID - 1) / GRID;
   return s < 4 + kC4SegCost ? 4 + kC4SegCost : s;
 }
 // Page of a segment of `pages` at which weight `x` from its begin lies.
@@ -644,14 +638,22 @@ template <int D, int RT>
 struct C4Shape {
   // whether the rows' operand stays in registers (else LDS, read per pair)
   static constexpr bool kQRegs = D * RT <= 256;
-  static constexpr int kPairs = D * RT <= 256 && D <= 128 ? 2 : 1;
+  // Waves a SIMD, or workgroups a compute unit: as many as registers and LDS
+  // hold, for a wave waits much on itself (scores, exponentials, their sum and
+  // the second product follow each other).  Three where 168 registers do without
+  // spills: 96 x 16 heads of 64, 5 rows over 0 to 2,045 tokens 41 us with two,
+  // 36 with three; 25 rows 58 and 46; 64 x 8 heads of 128 in tiles of 16 rows 84
+  // and 70 (32 rows a tile: 62 and, 11 registers spilled, 66).  Workgroups of a
+  // call: that many for each of 256 compute units.
+  static constexpr int kWaves = D * RT <= 128 ? 3 : D == 256 && RT == 2 ? 1 : 2;
+  static constexpr int kGrid = 256 * kWaves;
+  static constexpr int kPairs = D == 64 || (D == 128 && RT == 2) ? 2 : 1;
   static constexpr int kCodes = 2 * 16 * D / 2;        // bytes of a pair's keys, or values
   static constexpr int kKeyExps = (D == 256 ? 2 : 1) * 256;
   static constexpr int kUnit = 2 * kCodes + kKeyExps + 512;
   static constexpr int kBuf = kPairs * kUnit;           // a wave's part of a buffer
   // memory instructions of a pair
   static constexpr int kLoads = 2 * kCodes / 1024 + kKeyExps / 256 + 2;
-  static constexpr int kWaves = D == 256 && RT == 2 ? 1 : 2;  // a SIMD's
 };
 
 // Starts the loads of pair `half` of the record into `to`.
@@ -733,7 +735,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   const int32_t HR = A.cache.heads * A.row_blocks;
   int64_t before;
   const int64_t all = c4_plan(A, lane, per, before) * HR;  // weight of all segments
-  const int64_t share = c4_share(all);
+  const int64_t share = c4_share<Sh::kGrid>(all);
   const int64_t lo = (int64_t)blockIdx.x * share;
   const int64_t hi = min(lo + share, all);
   int32_t cut_b = 0, cut_hr = 0, cut_new = 0, cut_parts = 0, cut_slot = 0;
@@ -991,7 +993,7 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join_long(C4AttnArgs A
   const int32_t b = blockIdx.x / HR, hr = blockIdx.x % HR, row = blockIdx.y;
   const int32_t h = hr / A.row_blocks, r = hr % A.row_blocks * kRows + row, i = r / A.G;
   int64_t before;
-  const int64_t share = c4_share(c4_plan(A, lane, per, before) * HR);
+  const int64_t share = c4_share<C4Shape<D, RT>::kGrid>(c4_plan(A, lane, per, before) * HR);
   bool bad;
   int64_t at = c4_lane(before, b / per);
   for (int32_t x = b / per * per; x < b; ++x) at += c4_weight(c4_pages<true>(A, x, bad));

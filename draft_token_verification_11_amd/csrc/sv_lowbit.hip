@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "specverify_lowbit.h"
 #include "sv_cache4.hpp"
@@ -130,9 +131,9 @@ void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
 // Sequences of at most this many pages are not cut: the pass that joins cut
 // ones costs more than a workgroup's time over four pages a wave.
 constexpr int32_t kAttnWhole = 16;
-// Up to this many segments (sequences x heads x blocks of rows) each is in eight
+// Up to this many segments (sequences x heads x blocks of rows) each is in four
 // records or more on average, and their rows are joined by a workgroup each.
-constexpr int64_t kAttnFew = sv::kC4Grid / 8;
+constexpr int64_t kAttnFew = 64;
 
 int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
   if (B < 1 || T < 1 || kv_heads < 1 || q_heads < 1 || q_heads % kv_heads) return SPEC_ERR_INVALID_ARG;
@@ -142,31 +143,46 @@ int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_head
   return SPEC_OK;
 }
 
+// Calls f with the shape of a head dimension and its row tiles.
+template <int D, typename F>
+void with_shape(int tiles, F f) {
+  if (tiles == 1) f(std::integral_constant<int, D>(), std::integral_constant<int, 1>());
+  else if (tiles == 2) f(std::integral_constant<int, D>(), std::integral_constant<int, 2>());
+  else if constexpr (D < 256) {
+    if (tiles == 3) f(std::integral_constant<int, D>(), std::integral_constant<int, 3>());
+    else if constexpr (D == 64) f(std::integral_constant<int, D>(), std::integral_constant<int, 4>());
+  }
+}
+template <typename F>
+void with_shape(int32_t d, int tiles, F f) {
+  if (d == 64) with_shape<64>(tiles, f);
+  else if (d == 128) with_shape<128>(tiles, f);
+  else with_shape<256>(tiles, f);
+}
+
 size_t attention_workspace(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
   int tiles;
   int64_t blocks;
   row_blocks(int64_t(T) * (q_heads / kv_heads), d, &tiles, &blocks);
-  return size_t(sv::kC4Grid) * (sizeof(sv::C4Cut) + 2 * size_t(tiles) * 16 * size_t(d + 2) * 4);
+  size_t bytes = 0;
+  with_shape(d, tiles, [&](auto D, auto RT) {
+    bytes = size_t(sv::C4Shape<D, RT>::kGrid) * (sizeof(sv::C4Cut) + 2 * sizeof(float) * size_t(sv::C4Rec<D, RT>::kFloats));
+  });
+  return bytes;
 }
 
 template <int D, int RT>
-void launch_attention(const sv::C4AttnArgs& A, hipStream_t st) {
-  hipLaunchKernelGGL((sv::k_attention_cache4<D, RT>), dim3(sv::kC4Grid), dim3(256), 0, st, A);
+void launch_attention(sv::C4AttnArgs& A, void* workspace, hipStream_t st) {
+  constexpr int kGrid = sv::C4Shape<D, RT>::kGrid;
+  A.cuts = static_cast<sv::C4Cut*>(workspace);
+  A.parts = reinterpret_cast<float*>(A.cuts + kGrid);
+  hipLaunchKernelGGL((sv::k_attention_cache4<D, RT>), dim3(kGrid), dim3(256), 0, st, A);
   if (!A.split) return;
   const int64_t segments = int64_t(A.B) * A.cache.heads * A.row_blocks;
   if (segments <= kAttnFew)
     hipLaunchKernelGGL((sv::k_attention_cache4_join_long<D, RT>), dim3(unsigned(segments), RT * 16), dim3(256), 0, st, A);
   else
-    hipLaunchKernelGGL((sv::k_attention_cache4_join<D, RT>), dim3(sv::kC4Grid, RT * 4), dim3(256), 0, st, A);
-}
-template <int D>
-void launch_attention(int tiles, const sv::C4AttnArgs& A, hipStream_t st) {
-  if (tiles == 1) launch_attention<D, 1>(A, st);
-  else if (tiles == 2) launch_attention<D, 2>(A, st);
-  else if constexpr (D < 256) {
-    if (tiles == 3) launch_attention<D, 3>(A, st);
-    else if constexpr (D == 64) launch_attention<D, 4>(A, st);
-  }
+    hipLaunchKernelGGL((sv::k_attention_cache4_join<D, RT>), dim3(kGrid, RT * 4), dim3(256), 0, st, A);
 }
 
 int check_head(const void* weight, int64_t row_bytes, int32_t V, int32_t d) {
@@ -294,14 +310,10 @@ int spec_attention_cache4(spec_cache4_t cache, spec_heads_t q, int32_t B, int32_
   sv::C4AttnArgs A{view(cache), static_cast<const uint16_t*>(q.data), q.seq_stride, q.pos_stride,
                    q.head_stride, static_cast<uint16_t*>(out.data), out.seq_stride, out.pos_stride,
                    out.head_stride, lse, start, count, mask, mask_seq_stride, mask_pos_stride, B, T, G,
-                   int32_t(blocks), c, cache.table_cols > kAttnWhole,
-                   static_cast<sv::C4Cut*>(workspace),
-                   reinterpret_cast<float*>(static_cast<sv::C4Cut*>(workspace) + sv::kC4Grid)};
+                   int32_t(blocks), c, cache.table_cols > kAttnWhole, nullptr, nullptr};
   auto st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  if (cache.head_dim == 64) launch_attention<64>(tiles, A, st);
-  else if (cache.head_dim == 128) launch_attention<128>(tiles, A, st);
-  else launch_attention<256>(tiles, A, st);
+  with_shape(cache.head_dim, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(A, workspace, st); });
   return finish_launch();
 }
 
