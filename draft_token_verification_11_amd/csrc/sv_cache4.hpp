@@ -645,7 +645,7 @@ struct C4Shape {
   // 36 with three; 25 rows 58 and 46; 64 x 8 heads of 128 in tiles of 16 rows 84
   // and 70 (32 rows a tile: 62 and, 11 registers spilled, 66).  Workgroups of a
   // call: that many for each of 256 compute units.
-  static constexpr int kWaves = D * RT <= 128 ? 3 : D == 256 && RT == 2 ? 1 : 2;
+  static constexpr int kWaves = D * RT <= 128 ? 3 : 2;
   static constexpr int kGrid = 256 * kWaves;
   static constexpr int kPairs = D == 64 || (D == 128 && RT == 2) ? 2 : 1;
   static constexpr int kCodes = 2 * 16 * D / 2;        // bytes of a pair's keys, or values

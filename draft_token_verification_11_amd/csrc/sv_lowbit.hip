@@ -119,20 +119,33 @@ void launch_read(int32_t d, unsigned grid, const sv::C4MoveArgs& A, hipStream_t 
   else hipLaunchKernelGGL((sv::k_cache4_read<T, 256>), dim3(grid), dim3(256), 0, st, A);
 }
 
-// Row tiles of 16 a workgroup keeps (its accumulators grow with them), and
-// how many such blocks hold the rows of a kv head.
-int max_tiles(int32_t d) { return d == 256 ? 2 : d == 128 ? 3 : 4; }
+// Row tiles of 16 a workgroup keeps, and how many such blocks hold the rows of a
+// kv head.  More tiles convert the cache's codes less often, but their
+// accumulators leave room for fewer waves.  Times of the whole call:
+//   heads of 128  48 rows, 16 x 8 heads over up to 8,155 tokens: 46 us in tiles
+//                 of 1, 46 of 2, 42 of 3; four leave one wave a SIMD (168 rows:
+//                 102 us in blocks of 3, 171 of 4)
+//   heads of 64   48 rows, 96 x 16 heads over up to 2,045: 92, 93, 87; 64 rows:
+//                 120, 100 and in blocks of four 104; 176 rows, 16 x 8 heads over
+//                 up to 8,155: 73 in blocks of 2, 72 of 3, 70 of 4
+//   heads of 256  32 rows, 32 x 4 heads over up to 8,000: 60 in tiles of 1, 64 of
+//                 2; 168 rows, 16 x 4 heads: 127 and 153
+int max_tiles(int32_t d) { return d == 256 ? 1 : d == 128 ? 3 : 4; }
 void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
   const int64_t t = (rows + 15) / 16;
   *blocks = (t + max_tiles(d) - 1) / max_tiles(d);
   *tiles = int((t + *blocks - 1) / *blocks);
 }
 
-// Sequences of at most this many pages are not cut: the pass that joins cut
-// ones costs more than a workgroup's time over four pages a wave.
-constexpr int32_t kAttnWhole = 16;
+// Tables of at most this many pages a sequence are not cut: the pass that joins
+// cut ones costs about 5 us.  16 pages, 8 sequences of 8 heads: 10.9 us whole, 14.9
+// cut; 96 of 16: 25.7 and 28.7; 24 pages: 13.7 and 15.9, 35.8 and 33.3; 32 pages,
+// one sequence of 8 heads: 16.0 and 13.2.
+constexpr int32_t kAttnWhole = 20;
 // Up to this many segments (sequences x heads x blocks of rows) each is in four
-// records or more on average, and their rows are joined by a workgroup each.
+// records or more on average, and their rows are joined by a workgroup each (4 x 8
+// heads over 4,000 to 16,000 tokens: 25.6 us, by a wave each 28.4; 8 x 8: 36.3 and
+// 37.6; 16 x 8: it would be 60.5 and 56.2).
 constexpr int64_t kAttnFew = 64;
 
 int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
@@ -147,9 +160,9 @@ int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_head
 template <int D, typename F>
 void with_shape(int tiles, F f) {
   if (tiles == 1) f(std::integral_constant<int, D>(), std::integral_constant<int, 1>());
-  else if (tiles == 2) f(std::integral_constant<int, D>(), std::integral_constant<int, 2>());
   else if constexpr (D < 256) {
-    if (tiles == 3) f(std::integral_constant<int, D>(), std::integral_constant<int, 3>());
+    if (tiles == 2) f(std::integral_constant<int, D>(), std::integral_constant<int, 2>());
+    else if (tiles == 3) f(std::integral_constant<int, D>(), std::integral_constant<int, 3>());
     else if constexpr (D == 64) f(std::integral_constant<int, D>(), std::integral_constant<int, 4>());
   }
 }

@@ -259,6 +259,8 @@ def test_captured_calls():
     (24, 21, 16, 4, 64, 1000, 1400, "tree"),   # two blocks of rows to a head
     (5, 9, 16, 8, 256, 900, 2200, "chain"),    # few segments, each over many workgroups
     (33, 2, 2, 2, 64, 0, 1300, "counts"),      # some without a new token
+    (33, 2, 2, 2, 64, 0, 2600, "counts"),
+    (7, 3, 16, 1, 256, 900, 3000, "chain"),    # three blocks of rows to a head of 256
     (3, 40, 8, 2, 128, 0, 9000, "tree"),
     (70, 3, 4, 2, 128, 1100, 1500, "faults"),  # ill-formed ones and pages outside the pool between them
     (6, 3, 8, 2, 128, 3000, 6000, "faults"),
