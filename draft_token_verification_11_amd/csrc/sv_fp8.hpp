@@ -38,7 +38,8 @@ __device__ __forceinline__ uint32_t f8_pack4(const float* x, float scale) {
 
 // Weights: a workgroup takes one 128 x 128 block, 16 threads to a row of 128.
 // The block's values stay in registers between the maximum and the rounding,
-// so each is read once.
+// so each is read once.  Bound by memory: 151,936 x 4,096 BF16 (1.87 GB in and out)
+// in 342 us, 5.5 TB/s; 32,003 x 1,056 F32 (169 MB) in 34 us, 5.0 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_quantize_fp8(const T* __restrict__ weight, int64_t stride,
                                                       int64_t V, int32_t d, int32_t d_blocks,
@@ -76,6 +77,7 @@ __global__ __launch_bounds__(256) void k_quantize_fp8(const T* __restrict__ weig
 // Hidden rows rounded to e4m3 in blocks of 128, a block's exponent byte beside
 // them.  16 threads to a block; columns past d up to a multiple of 128 are zero,
 // which makes whatever the head's partial last block is multiplied with vanish.
+// 2,560 rows of 4,096: 11 us; nine: 5 us, a launch.
 struct F8HiddenArgs {
   const void* hidden;
   int64_t seq, pos;
@@ -192,7 +194,8 @@ __device__ __forceinline__ bool f8_vec_out(const F8HeadArgs& A) {
 // Up to 16 hidden rows: bound by the weights' bytes.  The hidden rows stand in
 // LDS whole, in the order in which lanes take them; a wave goes through units of
 // 16 vocabulary entries, their blocks of 128 columns straight from memory to
-// registers, kFly blocks in flight also from one unit into the next.
+// registers, kFly blocks in flight also from one unit into the next.  Nine rows
+// over 151,936 x 4,096, F32 logits: 120 us, 5.2 TB/s of weights and logits.
 template <typename TO, int BLOCKS>  // BLOCKS: the most blocks a row may have
 __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_rows(F8HeadArgs A) {
   constexpr int kFly = 6;
@@ -287,7 +290,11 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_rows(F8HeadArgs A) {
 // the other.  A row's eight 16-byte chunks are stored in the order
 // c ^ (row / 2 % 8), by permuting the addresses that the lanes load from, so that
 // the 16 rows a quarter of a fragment read touches (256 bytes) fall on the 64
-// banks without conflict.
+// banks without conflict.  2,560 rows over 151,936 x 4,096 to BF16 logits: 1.50 ms,
+// 2.1 PFLOP/s (the matrix units busy for 53 % of it; LDS reads and fills take as
+// many cycles, and the chip's clock falls to 2.0 GHz); 240 rows over 128,003 x
+// 2,080 to F32: 0.17 to 0.20 ms, of which rows that do not start at multiples of 16
+// bytes cost a tenth or more (over 128,000 entries: 0.16 to 0.18).
 template <typename TO, bool F8, int BV, int BM, int WV, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
   constexpr int WM = WAVES / WV, TV = BV / WV / 16, TM = BM / WM / 16;  // a wave's tiles of 16
