@@ -273,7 +273,7 @@ __global__ __launch_bounds__(256) void k_cache4_read(C4MoveArgs A) {
 // groups), so rescaling O' by a new maximum is one factor per lane.  The
 // maximum is raised only when a score passes it by 2^8 (P' stays below 2^8,
 // far from any limit of bf16 or fp32), so most pages skip the rescaling.  P' is
-// rounded to bf16 for the product (2^-9 relative at most, the size of the
+// rounded to bf16 for the product (2^-8 relative at most, the size of the
 // output's own rounding); the normaliser sums the unrounded fp32 values.
 //
 // Bound by the cache's bytes where rows are few and sequences long (64 x 8 heads
