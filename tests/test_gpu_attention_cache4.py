@@ -347,3 +347,47 @@ def test_no_new_tokens(start):
     before = pages.clone()
     sv.cache4_write(pages, _i32(table), _i32(start), K, K, count=_i32([0, 0]))
     assert torch.equal(pages, before)
+
+
+@pytest.mark.parametrize("Hq,H,start", [(1024, 1024, [5]), (16384, 1, [2])])
+def test_the_most_heads(Hq, H, start):
+    q, pages, table = _case(15, 1, 1, Hq, H, 64, start)
+    _check(q, pages, table, start, None, _chain, _run(q, pages, table, start))
+
+
+def test_the_most_heads_over_cut_pages():
+    """Every kv head holds the same values as the first: so do its query heads' outputs."""
+    H, start = 1024, [1290]
+    q, one, table = _case(15, 1, 1, 2, 1, 64, start)
+    got = _run(q.repeat(1, 1, H, 1), one.expand(-1, H, -1).contiguous(), table, start)
+    _check(q, one, table, start, None, _chain, tuple(x[:, :, :2].contiguous() for x in got))
+    for x in got:
+        x = x.view(H, 2, -1)
+        assert (x - x[:1]).abs().max() <= 2.0 ** -7  # cut at other pages: a step of bf16 below 2
+
+
+def test_the_most_sequences():
+    """65,536 sequences, without and with new tokens, on pages that many of them share."""
+    B, D = 65536, 64
+    rs = np.random.default_rng(16)
+    q, pages, _ = _case(16, 1, 1, 1, 1, D, [0], spare=2)
+    n = len(pages)
+    q = torch.tensor(rs.normal(0, 1, (B, 1, 1, D)), dtype=torch.float32).bfloat16().to(DEV)
+    table, start, count = rs.integers(0, n, (B, 1)), rs.integers(0, 63, B), rs.integers(0, 2, B)
+    out, lse = _run(q, pages, table, list(start), list(count))
+    K, V = sv.cache4_read(pages, _i32(np.arange(n)[:, None]), _i32([0] * n), 64, D, dtype=torch.float32)
+    for b0 in range(0, B, 8192):
+        part = slice(b0, b0 + 8192)
+        t, c = torch.tensor(table[part, 0], device=DEV), torch.tensor(count[part], device=DEV).bool()
+        k, v = K[t, :, 0].double(), V[t, :, 0].double()
+        s = (k * q[part, :, 0].double()).sum(-1) / D ** 0.5
+        s = s.masked_fill(torch.arange(64, device=DEV) > torch.tensor(start[part], device=DEV)[:, None], -float("inf"))
+        p = torch.softmax(s, -1)[..., None]
+        want, mag = (p * v).sum(1), (p * v.abs()).sum(1)
+        most = (k.abs() * q[part, :, 0].double().abs()).sum(-1).max() / D ** 0.5
+        few = most * 2 * (D + 2) * 2.0 ** -24 + 2.0 ** -21 + 64 * 2.0 ** -24
+        off = (out[part, 0, 0].double() - want).abs()
+        assert (off <= (2.0 ** -8 + few) * (mag * (1 + 2.0 ** -8) + want.abs()))[c].all()
+        l = torch.logsumexp(s, -1)
+        assert ((lse[part, 0, 0].double() - l).abs() <= few + l.abs() * 2.0 ** -21)[c].all()
+        assert (out[part][~c] == 7).all() and (lse[part][~c] == 7).all()
