@@ -277,12 +277,12 @@ __global__ __launch_bounds__(256) void k_cache4_read(C4MoveArgs A) {
 // output's own rounding); the normaliser sums the unrounded fp32 values.
 //
 // Bound by the cache's bytes where rows are few and sequences long (64 x 8 heads
-// of 128, 24 rows over 1,500 to 4,091 tokens, 201 MB: 61 us, 3.3 TB/s; once under
-// way 5.2 TB/s, the rest being the launch and the first loads, about 6 us, 5 us for
-// each segment's end, and workgroups that end before others), by the conversions,
-// exponentials and products of a wave following each other where they are many
-// (16 x 8 heads, 168 rows over 37 to 8,155 tokens: 102 us, matrix units busy for a
-// quarter of them), by the launch for one short sequence (10 us).
+// of 128, 24 rows over 1,500 to 4,091 tokens, 201 MB: 55 us, 3.6 TB/s; the launch
+// and the first loads take about 6 of them, each segment's end 5, and workgroups
+// end at different times), by the conversions, exponentials and products of a wave
+// following each other where they are many (16 x 8 heads, 168 rows over 37 to
+// 8,155 tokens: 81 us, matrix units busy for a third of them), by the launch for
+// one short sequence (10 us).
 //
 // Work split: the pages of all (sequence, kv head, block of rows) are laid end
 // to end and cut into one equal range per workgroup, whatever the sequences'
@@ -456,6 +456,9 @@ __device__ __forceinline__ uint32_t c4_sees(const C4AttnArgs& A, int64_t b, int3
   return sh == 0 ? word(k) : (word(k) >> sh) | (word(k + 1) << (32 - sh));
 }
 
+typedef uint32_t C4U2 __attribute__((ext_vector_type(2)));
+typedef uint32_t C4U4 __attribute__((ext_vector_type(4)));
+
 // The codes and exponents of a pair of 16-token tiles in a lane's registers.
 template <int D>
 struct C4Unit {
@@ -465,20 +468,6 @@ struct C4Unit {
   uint32_t ke[D == 256 ? 2 : 1];      // byte `tile`: this lane's token
   uint32_t ve[2];                     // byte j: token 4 q + j of the tile
 };
-
-template <int N>
-__device__ __forceinline__ void c4_load_words(const uint8_t* p, uint32_t* out) {
-  if constexpr (N == 2) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    out[0] = a.x, out[1] = a.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p + 16 * i);
-      out[4 * i] = a.x, out[4 * i + 1] = a.y, out[4 * i + 2] = a.z, out[4 * i + 3] = a.w;
-    }
-  }
-}
 
 __device__ __forceinline__ uint32_t c4_cvt(uint32_t w, float scale, int byte) {
   // the byte select is an immediate; `byte` is constant at every call
@@ -503,28 +492,108 @@ struct C4State {
   float m[RT], l[RT];
 };
 
-// One pair of tiles.  masked (of the wave): some of its 32 positions are not
-// seen by some row; sees[] then has this lane's rows' bits, and `valid` those
-// of the positions that hold tokens.  q_of(rt, j): the rows' operand.
-template <int D, int RT, typename Q>
-__device__ __forceinline__ void c4_unit(C4Unit<D>& R, Q q_of, C4State<D, RT>& S, float c, int lane,
-                                        bool masked, const uint32_t (&sees)[RT], uint32_t valid) {
-  const int q = lane >> 4;
-  if (masked) {  // what stands past the last token is not a value: zeros with an exponent of 1
+// Takes the keys, and the values, of pair `half` of a page out of its buffer, by
+// instructions that the compiler does not know to read LDS: it would wait for
+// every load under way at each, for along some branches it cannot tell which of
+// them they need (131,003 tokens, 36 rows: 55.8 us, so 50.7).
+template <int D>
+__device__ __forceinline__ void c4_take_keys(const uint8_t* from, int half, int lane, C4Unit<D>& R) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)from;
+  const uint32_t at4 = base + lane * 4;
+  if constexpr (D == 64) {
+    C4U2 k0, k1;
+    asm volatile(
+        "ds_read_b64 %0, %3\n\tds_read_b64 %1, %3 offset:512\n\tds_read_b32 %2, %4 offset:2048\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(k0), "=&v"(k1), "=&v"(R.ke[0])
+        : "v"(base + (lane & 15) * 32 + (lane >> 4) * 8), "v"(at4)
+        : "memory");
+#pragma unroll
+    for (int x = 0; x < 2; ++x) R.k[0][x] = k0[x], R.k[1][x] = k1[x];
+  } else if constexpr (D == 128) {
+    C4U4 k0, k1;
+    asm volatile(
+        "ds_read_b128 %0, %3\n\tds_read_b128 %1, %3 offset:1024\n\tds_read_b32 %2, %4 offset:4096\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(k0), "=&v"(k1), "=&v"(R.ke[0])
+        : "v"(base + lane * 16), "v"(at4)
+        : "memory");
+#pragma unroll
+    for (int x = 0; x < 4; ++x) R.k[0][x] = k0[x], R.k[1][x] = k1[x];
+  } else {
+    C4U4 k[4];
+    asm volatile(
+        "ds_read_b128 %0, %6\n\tds_read_b128 %1, %6 offset:1024\n\t"
+        "ds_read_b128 %2, %6 offset:2048\n\tds_read_b128 %3, %6 offset:3072\n\t"
+        "ds_read_b32 %4, %7 offset:8192\n\tds_read_b32 %5, %7 offset:8448\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(k[0]), "=&v"(k[1]), "=&v"(k[2]), "=&v"(k[3]), "=&v"(R.ke[0]), "=&v"(R.ke[1])
+        : "v"(base + lane * 16), "v"(at4)
+        : "memory");
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (!((valid >> (16 * i + 4 * q + j)) & 1)) {
-          R.ve[i] = (R.ve[i] & ~(0xFFu << (8 * j))) | (127u << (8 * j));
-#pragma unroll
-          for (int x = 0; x < (D + 127) / 128; ++x) {
-            // token j's D / 32 bytes of this lane's codes
-            if constexpr (D == 64) R.v[i][j / 2] &= j % 2 ? 0xFFFFu : 0xFFFF0000u;
-            else R.v[i][D / 128 * j + x] = 0u;
-          }
-        }
+      for (int x = 0; x < 8; ++x) R.k[i][x] = k[2 * i + x / 4][x % 4];
   }
+#pragma unroll
+  for (int x = 0; x < (D == 256 ? 2 : 1); ++x) R.ke[x] >>= 16 * half;
+#endif
+}
+template <int D>
+__device__ __forceinline__ void c4_take_values(const uint8_t* from, int lane, C4Unit<D>& R) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const uint32_t base = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)from;
+  const uint32_t at4 = base + lane * 4;
+  if constexpr (D == 64) {
+    C4U2 v0, v1;
+    asm volatile(
+        "ds_read_b64 %0, %4 offset:1024\n\tds_read_b64 %1, %4 offset:1536\n\t"
+        "ds_read_b32 %2, %5 offset:2304\n\tds_read_b32 %3, %5 offset:2560\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v0), "=&v"(v1), "=&v"(R.ve[0]), "=&v"(R.ve[1])
+        : "v"(base + lane * 8), "v"(at4)
+        : "memory");
+#pragma unroll
+    for (int x = 0; x < 2; ++x) R.v[0][x] = v0[x], R.v[1][x] = v1[x];
+  } else if constexpr (D == 128) {
+    C4U4 v0, v1;
+    asm volatile(
+        "ds_read_b128 %0, %4 offset:2048\n\tds_read_b128 %1, %4 offset:3072\n\t"
+        "ds_read_b32 %2, %5 offset:4352\n\tds_read_b32 %3, %5 offset:4608\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v0), "=&v"(v1), "=&v"(R.ve[0]), "=&v"(R.ve[1])
+        : "v"(base + lane * 16), "v"(at4)
+        : "memory");
+#pragma unroll
+    for (int x = 0; x < 4; ++x) R.v[0][x] = v0[x], R.v[1][x] = v1[x];
+  } else {
+    C4U4 v[4];
+    asm volatile(
+        "ds_read_b128 %0, %6 offset:4096\n\tds_read_b128 %1, %6 offset:5120\n\t"
+        "ds_read_b128 %2, %6 offset:6144\n\tds_read_b128 %3, %6 offset:7168\n\t"
+        "ds_read_b32 %4, %7 offset:8704\n\tds_read_b32 %5, %7 offset:8960\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(R.ve[0]), "=&v"(R.ve[1])
+        : "v"(base + lane * 16), "v"(at4)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) R.v[i][x] = v[2 * i + x / 4][x % 4];
+  }
+#endif
+}
+
+// One pair of tiles, from its buffer.  masked (of the wave): some of its 32 positions are not
+// seen by some row; sees[] then has this lane's rows' bits, and `valid` those
+// of the positions that hold tokens.  rows_of(j, qf): part j of the rows' operand.
+template <int D, int RT, typename Q>
+__device__ __forceinline__ void c4_unit(const uint8_t* from, int half, Q rows_of, C4State<D, RT>& S, float c, int lane,
+                                        bool masked, const uint32_t (&sees)[RT], uint32_t valid) {
+  const int q = lane >> 4;
+  C4Unit<D> R;
+  c4_take_keys<D>(from, half, lane, R);
   c4_f32x4 s[RT][2];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
@@ -543,13 +612,29 @@ __device__ __forceinline__ void c4_unit(C4Unit<D>& R, Q q_of, C4State<D, RT>& S,
       a.w = c4_cvt(R.k[i][j], sc, 3);
       kf[i] = __builtin_bit_cast(c4_bf16x8, a);
     }
+    c4_bf16x8 qf[RT];
+    rows_of(j, qf);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const c4_bf16x8 qf = q_of(rt, j);
+    for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        s[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], qf, s[rt][i], 0, 0, 0);
-    }
+        s[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf[i], qf[rt], s[rt][i], 0, 0, 0);
+  }
+  c4_take_values<D>(from, lane, R);
+  if (masked) {  // what stands past the last token is not a value: zeros with an exponent of 1
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (!((valid >> (16 * i + 4 * q + j)) & 1)) {
+          R.ve[i] = (R.ve[i] & ~(0xFFu << (8 * j))) | (127u << (8 * j));
+#pragma unroll
+          for (int x = 0; x < (D + 127) / 128; ++x) {
+            // token j's D / 32 bytes of this lane's codes
+            if constexpr (D == 64) R.v[i][j / 2] &= j % 2 ? 0xFFFFu : 0xFFFF0000u;
+            else R.v[i][D / 128 * j + x] = 0u;
+          }
+        }
   }
   c4_bf16x8 p[RT];  // P' of the pair, the second product's operand
 #pragma unroll
@@ -649,6 +734,7 @@ template <int D, int RT>
 struct C4Shape {
   // whether the rows' operand stays in registers (else LDS, read per pair)
   static constexpr bool kQRegs = D * RT <= 256;
+  static_assert(kQRegs || (D == 128 && RT == 3), "what c4_take_rows reads");
   // Waves a SIMD, or workgroups a compute unit: as many as registers and LDS
   // hold, for a wave waits much on itself (scores, exponentials, their sum and
   // the second product follow each other).  Three where 168 registers do without
@@ -659,6 +745,7 @@ struct C4Shape {
   static constexpr int kWaves = D * RT <= 128 ? 3 : 2;
   static constexpr int kGrid = 256 * kWaves;
   static constexpr int kPairs = D == 64 || (D == 128 && RT == 2) ? 2 : 1;
+  static_assert(kPairs <= 2, "as many waits");
   static constexpr int kCodes = 2 * 16 * D / 2;        // bytes of a pair's keys, or values
   static constexpr int kKeyExps = (D == 256 ? 2 : 1) * 256;
   static constexpr int kUnit = 2 * kCodes + kKeyExps + 512;
@@ -701,29 +788,25 @@ __device__ __forceinline__ void c4_fetch(const uint8_t* rec, int half, int lane,
 #endif
 }
 
-// Takes pair `half` of a page out of its buffer.
-template <int D>
-__device__ __forceinline__ void c4_take(const uint8_t* from, int half, int lane, C4Unit<D>& R) {
-  constexpr int kCodes = 16 * D, kParts = D == 256 ? 2 : 1;
-  const int n = lane & 15, q = lane >> 4;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if constexpr (D == 64) {
-      c4_load_words<2>(from + (16 * i + n) * 32 + q * 8, R.k[i]);
-      c4_load_words<2>(from + kCodes + i * 512 + lane * 8, R.v[i]);
-    } else {
-#pragma unroll
-      for (int x = 0; x < kParts; ++x) {
-        const int at = (i * kParts + x) * 1024 + lane * 16;
-        c4_load_words<4>(from + at, R.k[i] + 4 * x);
-        c4_load_words<4>(from + kCodes + at, R.v[i] + 4 * x);
-      }
-    }
-    R.ve[i] = *reinterpret_cast<const uint32_t*>(from + 2 * kCodes + 256 * (kParts + i) + lane * 4);
-  }
-#pragma unroll
-  for (int x = 0; x < kParts; ++x)
-    R.ke[x] = *reinterpret_cast<const uint32_t*>(from + 2 * kCodes + 256 * x + lane * 4) >> (16 * half);
+// Takes part j of the rows' operand, at p and two further tiles of 4 KiB, in the
+// same way.
+__device__ __forceinline__ void c4_take_rows(const uint4* p, c4_bf16x8 (&qf)[3]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("ds_read_b128 %0, %3\n\tds_read_b128 %1, %3 offset:4096\n\tds_read_b128 %2, %3 offset:8192\n\t"
+               "s_waitcnt lgkmcnt(0)"
+               : "=&v"(qf[0]), "=&v"(qf[1]), "=&v"(qf[2])
+               : "v"((uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint4*)p)
+               : "memory");
+#endif
+}
+
+// Waits until at most n vector memory operations are under way.
+template <int N>
+__device__ __forceinline__ void c4_wait() {
+  static_assert(N < 64, "six bits");
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4 | 15 << 8);  // the other counters as they are
+#endif
 }
 
 template <int D, int RT>
@@ -804,7 +887,9 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
 #pragma unroll
     for (int k = 0; k < 2 * N; ++k) first[k] = page_of(k);
 
-    c4_bf16x8 qf[Sh::kQRegs ? RT : 1][D / 32];
+    // The rows' operand, all on its way at once, before the first pairs.
+    constexpr int kQ = Sh::kQRegs ? D / 32 : D / 128;  // chunks a wave loads of a tile
+    uint4 qx[RT][kQ];
     int32_t tok[RT];  // this lane's rows' tokens; T past the last row
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -813,21 +898,36 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
       tok[rt] = r < R ? i : A.T;
       const uint16_t* qp = A.q + b * A.q_seq + i * A.q_pos + ((int64_t)h * A.G + g) * A.q_head;
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R && i < nnew && (Sh::kQRegs || j % 4 == w)) x = load16(qp + q * (D / 4) + 8 * j);
-        if constexpr (Sh::kQRegs) qf[rt][j] = __builtin_bit_cast(c4_bf16x8, x);
-        else if (j % 4 == w) qs[rt][j][lane] = x;
+      for (int j = 0; j < kQ; ++j) {
+        qx[rt][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < R && i < nnew) qx[rt][j] = load16(qp + q * (D / 4) + 8 * (Sh::kQRegs ? j : 4 * j + w));
       }
     }
+    // Waited for here, by an instruction that the compiler knows: at their first use,
+    // among the pairs, its wait would be for those too (64 x 8 heads of 128, 24 rows:
+    // 66.0 us, so 62.8).  Heads of 64 do better with the pairs sooner under way (96 x
+    // 16 heads, 60 rows: 109 us, so 105).
+    if constexpr (D > 64) c4_wait<0>();
 #pragma unroll
     for (int k = 0; k < 2 * N; ++k)
       if (k < nu) fetch(first[k], k < N ? ring0 : ring1, k % N);
     int32_t ahead = page_of(2 * N);  // the page of the next fetch
-    if constexpr (!Sh::kQRegs) __syncthreads();
-    auto q_of = [&](int rt, int j) {
-      if constexpr (Sh::kQRegs) return qf[rt][j];
-      else return __builtin_bit_cast(c4_bf16x8, qs[rt][j][lane]);
+    if constexpr (!Sh::kQRegs) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) qs[rt][4 * j + w][lane] = qx[rt][j];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // __syncthreads would wait for the pairs too
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
+    auto rows_of = [&](int j, c4_bf16x8(&qf)[RT]) {
+      if constexpr (Sh::kQRegs) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) qf[rt] = __builtin_bit_cast(c4_bf16x8, qx[rt][j]);
+      } else {
+        c4_take_rows(&qs[0][j][lane], qf);
+      }
     };
     C4State<D, RT> S;
 #pragma unroll
@@ -844,10 +944,11 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
         if (u >= nu) return;
         // this pair has arrived when no more than the later ones' loads are left
         // (loads return in order)
-        if (u + 2 * N - 1 < nu) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((2 * N - 1) * Sh::kLoads) : "memory");
+        const int32_t later = nu - 1 - u;
+        if (later >= 2 * N - 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"((2 * N - 1) * Sh::kLoads) : "memory");
+        else if (N == 2 && later == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * Sh::kLoads) : "memory");
+        else if (N == 2 && later == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Sh::kLoads) : "memory");
         else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        C4Unit<D> U;
-        c4_take<D>(buf + w * Sh::kBuf + k * Sh::kUnit, half, lane, U);
         // the first of its positions relative to the new tokens'
         const int64_t base = (int64_t)(pw + 2 * u) * kC4Page + 32 * half - s0;
         const bool masked = base + 32 > 0;
@@ -858,9 +959,8 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
           const int64_t have = nnew - base;
           valid = have >= 32 ? ~0u : (1u << have) - 1u;
         }
-        c4_unit<D, RT>(U, q_of, S, A.c, lane, masked, sees, valid);
+        c4_unit<D, RT>(buf + w * Sh::kBuf + k * Sh::kUnit, half, rows_of, S, A.c, lane, masked, sees, valid);
         if (u + 2 * N < nu) {
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the buffer has been taken out
           fetch(ahead, buf, k);
           ahead = page_of(u + 2 * N + 1);
         }
