@@ -999,7 +999,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
 #pragma unroll
       for (int x = 0; x < 4; ++x) l += ls[x][row] * __builtin_amdgcn_exp2f(ms[x][row] - top);
       const int32_t r = r0 + row, i = r / A.G, head = h * A.G + (r - i * A.G);
-      const bool live = whole && r < R && i < nnew;
+      const bool live = r < R && i < nnew;
 #pragma unroll
       for (int x = 0; x < D / kCols; ++x) {
         // the buffers in turn: one barrier a time
@@ -1018,9 +1018,10 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
         for (int ww = 0; ww < 4; ++ww)
 #pragma unroll
           for (int e = 0; e < kRun; ++e) v[e] += oacc[(ww * 16 + rr) * kPad + grp * kRun + e];
-        if (live) {
+        if (!live) continue;
+        if (whole) {
           c4_finish<kRun>(A, b, i, head, d0, v, top, l);
-        } else if (!whole) {
+        } else {
 #pragma unroll
           for (int e = 0; e < kRun; ++e) part[row * D + d0 + e] = v[e];
           if (d0 == 0) {

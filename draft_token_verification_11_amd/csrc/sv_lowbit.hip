@@ -122,12 +122,12 @@ void launch_read(int32_t d, unsigned grid, const sv::C4MoveArgs& A, hipStream_t 
 // Row tiles of 16 a workgroup keeps, and how many such blocks hold the rows of a
 // kv head.  More tiles convert the cache's codes less often, but their
 // accumulators leave room for fewer waves.  Times of the whole call:
-//   heads of 128  48 rows, 16 x 8 heads over up to 8,155 tokens: 46 us in tiles
-//                 of 1, 46 of 2, 42 of 3; four leave one wave a SIMD (168 rows:
-//                 102 us in blocks of 3, 171 of 4)
-//   heads of 64   48 rows, 96 x 16 heads over up to 2,045: 92, 93, 87; 64 rows:
-//                 120, 100 and in blocks of four 104; 176 rows, 16 x 8 heads over
-//                 up to 8,155: 73 in blocks of 2, 72 of 3, 70 of 4
+//   heads of 128  48 rows, 16 x 8 heads over up to 8,155 tokens: 48 us in tiles
+//                 of 1, 49 of 2, 41 of 3; four leave one wave a SIMD (168 rows
+//                 took 171 us in blocks of four where three took 102)
+//   heads of 64   48 rows, 96 x 16 heads over up to 2,045: 97, 94, 87; 64 rows:
+//                 122, 100 and in blocks of four 103; 176 rows, 16 x 8 heads over
+//                 up to 8,155: 74 in blocks of 2, 73 of 3, 71 of 4
 //   heads of 256  32 rows, 32 x 4 heads over up to 8,000: 60 in tiles of 1, 64 of
 //                 2; 168 rows, 16 x 4 heads: 127 and 153
 int max_tiles(int32_t d) { return d == 256 ? 1 : d == 128 ? 3 : 4; }
@@ -138,14 +138,14 @@ void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
 }
 
 // Tables of at most this many pages a sequence are not cut: the pass that joins
-// cut ones costs about 5 us.  16 pages, 8 sequences of 8 heads: 10.9 us whole, 14.9
-// cut; 96 of 16: 25.7 and 28.7; 24 pages: 13.7 and 15.9, 35.8 and 33.3; 32 pages,
-// one sequence of 8 heads: 16.0 and 13.2.
+// cut ones costs about 5 us.  16 pages, 8 sequences of 8 heads: 11.2 us whole, 15.2
+// cut; 96 of 16: 26.0 and 29.5; 24 pages: 13.9 and 15.4, 35.8 and 33.4; 32 pages,
+// one sequence of 8 heads: 16.6 and 13.3.
 constexpr int32_t kAttnWhole = 20;
 // Up to this many segments (sequences x heads x blocks of rows) each is in four
 // records or more on average, and their rows are joined by a workgroup each (4 x 8
-// heads over 4,000 to 16,000 tokens: 25.6 us, by a wave each 28.4; 8 x 8: 36.3 and
-// 37.6; 16 x 8: it would be 60.5 and 56.2).
+// heads over 4,000 to 16,000 tokens: 26.1 us, by a wave each 29.0; 8 x 8: 36.2 and
+// 37.3; 16 x 8: it would be 58.3 and 53.2).
 constexpr int64_t kAttnFew = 64;
 
 int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
