@@ -331,9 +331,10 @@ __device__ __forceinline__ int32_t c4_pages(const C4AttnArgs& A, int64_t b, bool
 // Beginning and ending a segment (its rows, the first loads, joining the four
 // waves) costs a workgroup as much time as about this many pages; without it
 // in the shares a batch with short sequences waits for the workgroups that
-// hold many of them (16 sequences of 37 to 8,155 tokens with 168 rows: 0.39 ms
-// against 0.10 for equal lengths).
-constexpr int32_t kC4SegCost = 6;
+// hold many of them (16 sequences of 37 to 8,155 tokens, 8 heads of 128, 168 rows:
+// 124 us at 3 pages, 93 at 6, 92 at 8, 94 at 12; 96 x 16 heads of 64 over 0 to 2,045,
+// 48 rows: 85 at 6, 75 at 8; 7 x 8 heads over 5,000 to 9,000: 23.6 and 24.3).
+constexpr int32_t kC4SegCost = 8;
 
 // Weight of a segment of `pages`.
 __device__ __forceinline__ int64_t c4_weight(int32_t pages) {

@@ -117,7 +117,7 @@ int spec_cache4_read(spec_cache4_t cache, spec_heads_t k, spec_heads_t v, int32_
  *   lse   [B][T][q_heads] F32 or NULL
  * Rows i >= count[b] of out and lse are left as they were.
  * Limits: q_heads a multiple of heads, at most 16384; T <= SPEC_CACHE4_MAX_T;
- * B (table_cols + 6) heads ceil(T q_heads / heads / 16) below 2^40.
+ * B (table_cols + 8) heads ceil(T q_heads / heads / 16) below 2^40.
  * workspace: spec_attention_cache4_workspace bytes, 256-byte aligned. */
 #define SPEC_CACHE4_MAX_T 256
 size_t spec_attention_cache4_workspace(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
