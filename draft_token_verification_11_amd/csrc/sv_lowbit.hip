@@ -122,12 +122,12 @@ void launch_read(int32_t d, unsigned grid, const sv::C4MoveArgs& A, hipStream_t 
 // Row tiles of 16 a workgroup keeps, and how many such blocks hold the rows of a
 // kv head.  More tiles convert the cache's codes less often, but their
 // accumulators leave room for fewer waves.  Times of the whole call:
-//   heads of 128  48 rows, 16 x 8 heads over up to 8,155 tokens: 48 us in tiles
-//                 of 1, 49 of 2, 41 of 3; four leave one wave a SIMD (168 rows
+//   heads of 128  48 rows, 16 x 8 heads over up to 8,155 tokens: 47 us in tiles
+//                 of 1, 48 of 2, 40 of 3; four leave one wave a SIMD (168 rows
 //                 took 171 us in blocks of four where three took 102)
-//   heads of 64   48 rows, 96 x 16 heads over up to 2,045: 97, 94, 87; 64 rows:
-//                 122, 100 and in blocks of four 103; 176 rows, 16 x 8 heads over
-//                 up to 8,155: 74 in blocks of 2, 73 of 3, 71 of 4
+//   heads of 64   48 rows, 96 x 16 heads over up to 2,045: 94, 90, 75; 64 rows:
+//                 117, 94 and in blocks of four 95; 176 rows, 16 x 8 heads over
+//                 up to 8,155: 71 in blocks of 2, 69 of 3, 68 of 4
 //   heads of 256  32 rows, 32 x 4 heads over up to 8,000: 60 in tiles of 1, 64 of
 //                 2; 168 rows, 16 x 4 heads: 127 and 153
 int max_tiles(int32_t d) { return d == 256 ? 1 : d == 128 ? 3 : 4; }
@@ -138,14 +138,14 @@ void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
 }
 
 // Tables of at most this many pages a sequence are not cut: the pass that joins
-// cut ones costs about 5 us.  16 pages, 8 sequences of 8 heads: 11.2 us whole, 15.2
-// cut; 96 of 16: 26.0 and 29.5; 24 pages: 13.9 and 15.4, 35.8 and 33.4; 32 pages,
-// one sequence of 8 heads: 16.6 and 13.3.
+// cut ones costs about 5 us.  16 pages, 8 sequences of 8 heads: 11.2 us whole, 14.9
+// cut; 96 of 16: 25.3 and 28.1; 24 pages: 13.8 and 15.2, 34.3 and 32.7; 32 pages,
+// one sequence of 8 heads: 16.4 and 13.5.
 constexpr int32_t kAttnWhole = 20;
 // Up to this many segments (sequences x heads x blocks of rows) each is in four
 // records or more on average, and their rows are joined by a workgroup each (4 x 8
-// heads over 4,000 to 16,000 tokens: 26.1 us, by a wave each 29.0; 8 x 8: 36.2 and
-// 37.3; 16 x 8: it would be 58.3 and 53.2).
+// heads over 4,000 to 16,000 tokens: 25.5 us, by a wave each 28.8; 8 x 8: 35.6 and
+// 36.3; 16 x 8: it would be 57.2 and 52.3).
 constexpr int64_t kAttnFew = 64;
 
 int check_attention_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
@@ -198,10 +198,10 @@ void launch_attention(sv::C4AttnArgs& A, void* workspace, hipStream_t st) {
     hipLaunchKernelGGL((sv::k_attention_cache4_join<D, RT>), dim3(kGrid, RT * 4), dim3(256), 0, st, A);
 }
 
-int check_head(const void* weight, int64_t row_bytes, int32_t V, int32_t d) {
+int check_head(const void* weight, int64_t stride, int64_t elem, int32_t V, int32_t d) {
   if (!weight || V < 1 || d < 32 || d % 32) return SPEC_ERR_INVALID_ARG;
   if (V > SPEC_MAX_V || d > 65536) return SPEC_ERR_UNSUPPORTED;
-  if (!aligned(weight, 16) || row_bytes % 16) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(weight, 16) || stride % (16 / elem)) return SPEC_ERR_INVALID_ARG;
   return SPEC_OK;
 }
 
@@ -334,7 +334,7 @@ int spec_quantize_fp8(const void* weight, int32_t dtype, int64_t weight_stride, 
                       int32_t d, void* q, float* scale, void* stream) {
   if (!dtype_ok(dtype)) return SPEC_ERR_UNSUPPORTED;
   int rc;
-  if ((rc = check_head(weight, weight_stride * int64_t(elem_size(dtype)), V, d)) != SPEC_OK) return rc;
+  if ((rc = check_head(weight, weight_stride, int64_t(elem_size(dtype)), V, d)) != SPEC_OK) return rc;
   if (weight_stride < d || !q || !scale || !aligned(q, 16) || !aligned(scale, 4))
     return SPEC_ERR_INVALID_ARG;
   const int64_t db = padded(d) / 128, blocks = (int64_t(V) + 127) / 128 * db;
@@ -365,7 +365,7 @@ int spec_lmhead_fp8(spec_logits_t hidden, int32_t B, int32_t rows, int32_t d, co
   int rc;
   if (B < 1 || rows < 1) return SPEC_ERR_INVALID_ARG;
   if (B > (1 << 24) || rows > 2 * SPEC_MAX_K + 1) return SPEC_ERR_UNSUPPORTED;
-  if ((rc = check_head(weight, weight_stride, V, d)) != SPEC_OK) return rc;
+  if ((rc = check_head(weight, weight_stride, 1, V, d)) != SPEC_OK) return rc;
   if (weight_stride < d || !scale || !aligned(scale, 4)) return SPEC_ERR_INVALID_ARG;
   if (weight_stride > kMaxWeightStride) return SPEC_ERR_UNSUPPORTED;
   if (!dtype_ok(hidden.dtype) || !dtype_ok(logits.dtype)) return SPEC_ERR_UNSUPPORTED;
