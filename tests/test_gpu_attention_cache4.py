@@ -391,3 +391,21 @@ def test_the_most_sequences():
         l = torch.logsumexp(s, -1)
         assert ((lse[part, 0, 0].double() - l).abs() <= few + l.abs() * 2.0 ** -21)[c].all()
         assert (out[part][~c] == 7).all() and (lse[part][~c] == 7).all()
+
+
+@pytest.mark.parametrize("B,T,Hq,H,D,lo,hi", [(64, 6, 32, 8, 128, 100, 2000), (1, 9, 32, 8, 128, 20000, 20000),
+                                              (16, 21, 32, 4, 128, 37, 2000), (48, 40, 8, 8, 64, 0, 1500),
+                                              (8, 4, 16, 4, 256, 0, 3000)])
+def test_two_streams_at_once(B, T, Hq, H, D, lo, hi):
+    """The same bits from every call, whatever runs beside it."""
+    start = np.random.default_rng(17).integers(lo, hi + 1, B)
+    q, pages, table = _case(17, B, T, Hq, H, D, list(start))
+    t, s = _i32(table), _i32(start)
+    want = sv.attention_cache4(q, pages, t, s, return_lse=True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        got = [sv.attention_cache4(q, pages, t, s, return_lse=True, stream=st) for st in streams]
+        torch.cuda.synchronize()
+        for out, lse in got:
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
