@@ -341,13 +341,19 @@ __device__ __forceinline__ int64_t c4_weight(int32_t pages) {
   return pages ? pages + kC4SegCost : 0;
 }
 
-// floor(x / y) for 0 <= x < 2^52, 0 < y < 2^31, the quotient below 2^31.
-__device__ __forceinline__ int32_t c4_div(int64_t x, int32_t y) {
-  int32_t q = (int32_t)((double)x * __builtin_amdgcn_rcp((double)y));  // off by a few at most
-  int64_t r = x - (int64_t)q * y;
-  while (r < 0) --q, r += y;
-  while (r >= y) ++q, r -= y;
-  return q;
+// floor(x / y) for 0 <= x < 2^42, 0 < y < 2^42, from a reciprocal r of y good to
+// 2^-14: two Newton steps bring it to 2^-51, so that the product is less than
+// one off and its whole part at most one.  Shares and places among all
+// segments pass 32 bits in large calls.
+__host__ __device__ __forceinline__ int64_t c4_quotient(int64_t x, int64_t y, double r) {
+  const double d = (double)y;
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  const int64_t q = (int64_t)((double)x * r), rest = x - q * y;
+  return q - (rest < 0) + (rest >= y);
+}
+__device__ __forceinline__ int64_t c4_div(int64_t x, int64_t y) {
+  return c4_quotient(x, y, __builtin_amdgcn_rcp((double)y));
 }
 
 // Sum over the lanes up to and with this one.
@@ -847,7 +853,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   int64_t b = c4_find(A, lane, per, before, c4_div(lo, HR), seq_at);
   bool bad;
   int32_t pages = c4_pages<true>(A, b, bad);
-  int32_t hr = c4_div(lo - seq_at * HR, (int32_t)c4_weight(pages));
+  int32_t hr = (int32_t)c4_div(lo - seq_at * HR, c4_weight(pages));
   int64_t seg = seq_at * HR + hr * c4_weight(pages);  // where it begins
   const int32_t R = A.T * A.G;
   for (; seg < hi; seg += c4_weight(pages), ++hr) {
@@ -864,7 +870,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
     if (p0 == 0 && p1 < pages) {
       cut_b = (int32_t)b, cut_hr = hr, cut_new = nnew, cut_slot = seg > lo ? 1 : 0;
-      cut_parts = c4_div(seg + kC4SegCost + pages - 1, (int32_t)share) - blockIdx.x + 1;
+      cut_parts = (int32_t)c4_div(seg + kC4SegCost + pages - 1, share) - blockIdx.x + 1;
     }
 
     // The waves take the segment's pairs of tiles in turn, so that a wave's are
@@ -1115,8 +1121,8 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join_long(C4AttnArgs A
   if (pages == 0 || r >= A.T * A.G || i >= nnew) return;
   const int64_t seg = at * HR + hr * c4_weight(pages);
   // the workgroups that hold its first and last page
-  const int32_t w0 = c4_div(seg + kC4SegCost, (int32_t)share);
-  const int32_t parts = c4_div(seg + kC4SegCost + pages - 1, (int32_t)share) - w0 + 1;
+  const int32_t w0 = (int32_t)c4_div(seg + kC4SegCost, share);
+  const int32_t parts = (int32_t)c4_div(seg + kC4SegCost + pages - 1, share) - w0 + 1;
   if (parts == 1) return;  // written whole
   const float* rest = A.parts + (int64_t)w0 * 2 * kFloats;
   const float* first = rest + (seg > w0 * share ? kFloats : 0);
