@@ -77,10 +77,13 @@ struct C4MoveArgs {
 
 __device__ __forceinline__ float c4_exp_scale(uint32_t e) { return __uint_as_float(e << 23); }
 
-// Exponent byte of a group with the largest magnitude `amax` (finite).
+// Exponent byte of a group with the largest magnitude `amax` (finite).  252 at
+// most: 6 x 2^125 is the largest code times a power of two that fp32 and bf16
+// hold (4 x 2^126 would be 2^128), and the conversion holds what lies past it
+// as 6.
 __device__ __forceinline__ uint32_t c4_exponent(float amax) {
   const int32_t e = (int32_t)((__float_as_uint(amax) + 0x3FFFFFu) >> 23) - 2;
-  return (uint32_t)(e < 1 ? 1 : e);
+  return (uint32_t)(e < 1 ? 1 : e > 252 ? 252 : e);
 }
 
 __device__ __forceinline__ uint32_t c4_pack8(const float* x, float scale) {

@@ -32,8 +32,10 @@ extern "C" {
  * groups.  A group is held as 4-bit e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
  * their negatives, the OCP microscaling element) and one exponent byte e; code
  * c stands for c 2^(e-127).  2^(e-127) is the smallest power of two, at least
- * 2^-126, whose 6-fold holds the group's largest magnitude; values round to the
- * nearest code, ties to the even one.  A (token, head) whose key or value holds
+ * 2^-126 and at most 2^125, whose 6-fold holds the group's largest magnitude;
+ * values round to the nearest code, ties to the even one, and what passes
+ * 3 x 2^126, the largest such value that is finite in F32 and BF16, is held
+ * as it.  A (token, head) whose key or value holds
  * a NaN or an infinity is held as NaN: every key exponent byte is 255 and all
  * codes are 0.
  *

@@ -41,3 +41,91 @@ def test_more_pages_than_32_bits_count():
         assert (off <= (2.0 ** -8 + few) * (mag * (1 + 2.0 ** -8) + 2 * want.abs())).all()
         l = torch.logsumexp(s, -1) + np.log(P)
         assert ((lse[b0:b0 + 8192, 0, 0].double() - l).abs() <= few + l.abs() * 2.0 ** -21).all()
+
+
+def _held(x):
+    """(codes, exponent bytes, values) of finite x [D] in 4 bits: 3 x 2^126, the largest code times
+    a power of two that both types hold, is the largest magnitude."""
+    codes, exps = [], []
+    for g in np.asarray(x, np.float64).reshape(-1, 32):
+        e = min(plain.exponent(np.abs(g).max(), 6.0), 252)
+        codes.append(plain.nearest(g * 2.0 ** (127 - e), plain.E2M1) + 8 * np.signbit(g))
+        exps.append(e)
+    codes, exps = np.concatenate(codes).astype(int), np.array(exps)
+    return codes, exps, plain.value4(codes, exps)
+
+
+def _ends(dtype, D):
+    """Rows of finite values at the ends of the type's range, and between codes there."""
+    top = torch.finfo(dtype).max
+    rows = [[top], [-top, 1.0], [3.0 * 2.0 ** 126], [3.5 * 2.0 ** 126, -3.25 * 2.0 ** 126],
+            [3.96875 * 2.0 ** 126, 2.0 ** 126, 2.5 * 2.0 ** 125, 1e30], [1.5 * 2.0 ** 126, 1.75 * 2.0 ** 126],
+            [6.0 * 2.0 ** 125, -5.0 * 2.0 ** 125, 2.5 * 2.0 ** 125],
+            [2.0 ** -126, 2.0 ** -127, 2.0 ** -128, 1.5 * 2.0 ** -128], [2.0 ** -133, 1.75 * 2.0 ** -126],
+            [6.0 * 2.0 ** -126, 5.0 * 2.0 ** -126, -2.0 ** -127], [-0.0, 2.0 ** -129], [0.0]]
+    return torch.tensor(np.stack([np.resize(r, D) for r in rows]), dtype=torch.float64).to(dtype)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_every_finite_value_is_held_finite_and_read_exactly(D, dtype):
+    x = _ends(dtype, D)
+    n = len(x)
+    assert torch.isfinite(x).all()
+    k = torch.cat([x, x, torch.ones(2, D, dtype=dtype)])
+    v = torch.cat([x, x.flip(0), torch.ones(2, D, dtype=dtype)])
+    k[2 * n, 5], v[2 * n + 1, D - 1] = float("inf"), float("nan")  # in tokens of their own
+    T = 2 * n + 2
+    pages = torch.full((2, 1, 68 * D), 77, dtype=torch.uint8, device=DEV)
+    table, start = _i32([[1]]), _i32([3])
+    sv.cache4_write(pages, table, start, *(y.view(1, T, 1, D).to(DEV) for y in (k, v)))
+    raw = pages.cpu().numpy()[1, 0]
+    for out_dtype in (torch.float32, torch.bfloat16):
+        got = [y.cpu().double().numpy()[0, :, 0] for y in sv.cache4_read(pages, table, start, T, D, dtype=out_dtype)]
+        for y in got:
+            assert np.isnan(y[2 * n:]).all() and np.isfinite(y[:2 * n]).all()
+        for i in range(2 * n):
+            at = plain.offsets(3 + i, D)
+            for z, y, (code, exp) in zip((k, v), got, (at[:2], at[2:])):
+                c, e, want = _held(z[i].double().numpy())
+                assert np.array_equal(raw[code], c[0::2] + 16 * c[1::2]) and np.array_equal(raw[exp], e)
+                assert np.array_equal(y[i], want)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_what_is_not_seen_does_not_matter(D):
+    """Places that a row does not see hold NaN, the largest finite values, and bytes of any kind
+    behind the last token: the row's result is the formula's, and only rows that see a NaN get one."""
+    rs = np.random.default_rng([2, D])
+    T, H, G, start = 6, 2, 2, [70, 3, 33]
+    B, P = len(start), 2
+    pages = sv.cache4_alloc(B * P, H, D, DEV)
+    table = np.arange(B * P).reshape(B, P)
+    k, v = (torch.tensor(rs.normal(0, 1, (B, 128, H, D)), dtype=torch.float32, device=DEV) for _ in range(2))
+    sv.cache4_write(pages, _i32(table), _i32([0] * B), k, v)
+    raw = pages.cpu().numpy()
+    for b in range(B):  # behind the last token: noise, all bytes 255, noise with exponents 255
+        for x in range(start[b] + T, P * 64):
+            for j, at in enumerate(plain.offsets(x % 64, D)):
+                raw[table[b, x // 64], :, at] = 255 if b == 1 or (b == 2 and j % 2) else rs.integers(0, 256, (len(at), H))
+    pages = torch.from_numpy(raw).to(DEV)
+    # new token 2 as large as F32 goes, 4 not finite; nobody else sees the first, 5 alone the second
+    top = torch.finfo(torch.float32).max
+    big = torch.tensor(np.where(rs.integers(0, 2, (2, B, 1, H, D)), top, -top), dtype=torch.float32, device=DEV)
+    sv.cache4_write(pages, _i32(table), _i32(np.array(start) + 2), big[0], big[1])
+    odd = torch.ones(B, 1, H, D, device=DEV)
+    odd[:, 0, :, 7] = float("nan")
+    sv.cache4_write(pages, _i32(table), _i32(np.array(start) + 4), odd, torch.ones_like(odd))
+    see = np.tril(np.ones((T, T), bool))
+    see[:, 2] = see[:, 4] = False
+    see[2, 2] = see[4, 4] = see[5, 4] = True
+    words = _i32([[[int(sum(1 << j for j in range(T) if see[i, j]))] for i in range(T)]])
+    q = torch.tensor(rs.normal(0, 1, (B, T, H * G, D)), dtype=torch.float32).bfloat16().to(DEV)
+    out, lse = sv.attention_cache4(q, pages, _i32(table), _i32(start), mask=words, return_lse=True)
+    fine = [0, 1, 3]
+    want = plain.attention(q.double().cpu().numpy(), pages.cpu().numpy(), table, start, [T] * B,
+                           lambda b, i, j: see[i, j], plain.inv_sqrt(D))
+    for x, y, t in ((out, want[0], want[2]), (lse, want[1], want[3])):
+        x = x.double().cpu().numpy()
+        assert np.isnan(x[:, 4:]).all() and np.isfinite(x[:, fine]).all()
+        assert (np.abs(x - y)[:, fine] <= t[:, fine]).all()
