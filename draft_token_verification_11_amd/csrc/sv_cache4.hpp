@@ -277,7 +277,16 @@ __global__ __launch_bounds__(256) void k_cache4_read(C4MoveArgs A) {
 // maximum is raised only when a score passes it by 2^8 (P' stays below 2^8,
 // far from any limit of bf16 or fp32), so most pages skip the rescaling.  P' is
 // rounded to bf16 for the product (2^-8 relative at most, the size of the
-// output's own rounding); the normaliser sums the unrounded fp32 values.
+// output's own rounding).  The normaliser sums the rounded values, so that the
+// output is a weighted mean of what the row sees: values that agree come out as
+// they are, and the rounding of a probability that outweighs all others cancels.
+// The log-sum-exp takes the sum of the unrounded ones.  The second sum costs 1 to
+// 6 % (64 x 6 rows 62.6 us, so 63.9; trees of 168 rows 86.9, so 90.0; 64 rows of
+// heads of 64 39.3, so 41.6; summed by a matrix instruction 63.7, 89.4 and, spilled,
+// 42.6).  P' as the sum of two bf16 would bring the error against 64 bits
+// from 0.0017 to 0.0024 down to the output's own rounding, 0.0014 to 0.0017, in
+// another half of the matrix instructions: 67.5, 107 and 46.4 us, and 131,003
+// tokens x 36 rows 57.2 instead of 48.9.
 //
 // Bound by the cache's bytes where rows are few and sequences long (64 x 8 heads
 // of 128, 24 rows over 1,500 to 4,091 tokens, 201 MB: 55 us, 3.6 TB/s; the launch
@@ -423,9 +432,9 @@ __device__ __forceinline__ int32_t c4_cut(int64_t x, int32_t pages) {
 }
 
 template <int D, int RT>
-struct C4Rec {  // one cut segment: O [RT * 16][D], m and l [RT * 16]
+struct C4Rec {  // one cut segment: O [RT * 16][D], m, l and n [RT * 16]
   static constexpr int kRows = RT * 16;
-  static constexpr int kFloats = kRows * (D + 2);
+  static constexpr int kFloats = kRows * (D + 3);
 };
 
 __device__ __forceinline__ float c4_max_quads(float x) {  // over the four lane groups
@@ -499,7 +508,7 @@ __device__ __forceinline__ float c4_byte_scale(uint32_t w, int i) {
 template <int D, int RT>
 struct C4State {
   c4_f32x4 o[RT][D / 16];
-  float m[RT], l[RT];
+  float m[RT], l[RT], n[RT];  // maximum, sum of P' and of P' rounded
 };
 
 // Takes the keys, and the values, of pair `half` of a page out of its buffer, by
@@ -665,6 +674,7 @@ __device__ __forceinline__ void c4_unit(const uint8_t* from, int half, Q rows_of
       const float f = __builtin_amdgcn_exp2f(S.m[rt] - m);
       S.m[rt] = m;
       S.l[rt] *= f;
+      S.n[rt] *= f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) S.o[rt][i] *= f;
     }
@@ -678,6 +688,10 @@ __device__ __forceinline__ void c4_unit(const uint8_t* from, int half, Q rows_of
         p[rt][4 * i + r] = (__bf16)e;
       }
     S.l[rt] += sum;
+    constexpr c4_bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+    for (int r = 0; r < 8; r += 2)
+      S.n[rt] = __builtin_amdgcn_fdot2_f32_bf16(c4_bf16x2{p[rt][r], p[rt][r + 1]}, one, S.n[rt], false);
   }
   // V' of the pair: byte y of token j's codes gives that token's values of two
   // neighbouring d; tokens are paired for each d by a byte permutation
@@ -719,8 +733,8 @@ __device__ __forceinline__ void c4_unit(const uint8_t* from, int half, Q rows_of
 // the row's lse.
 template <int N>
 __device__ __forceinline__ void c4_finish(const C4AttnArgs& A, int64_t b, int32_t i, int32_t head,
-                                          int d0, const float* x, float m, float l) {
-  const float inv = l == 0.f ? 0.f : 1.0f / l;  // a NaN sum stays NaN
+                                          int d0, const float* x, float m, float l, float n) {
+  const float inv = n == 0.f ? 0.f : 1.0f / n;  // a NaN sum stays NaN
   typedef __bf16 Out __attribute__((ext_vector_type(N)));
   Out y;
 #pragma unroll
@@ -827,7 +841,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   // for the other's loads when it reads one.
   __shared__ __attribute__((aligned(16))) uint8_t ring0[4 * Sh::kBuf], ring1[4 * Sh::kBuf];
   __shared__ uint4 qs[Sh::kQRegs ? 1 : RT][Sh::kQRegs ? 1 : D / 32][Sh::kQRegs ? 1 : 64];
-  __shared__ float ms[4][kRows], ls[4][kRows];
+  __shared__ float ms[4][kRows], ls[4][kRows], ns[4][kRows];
   // After a segment the buffers hold O of 16 rows x kCols columns of each wave, in turn.
   constexpr int kCols = D == 64 ? 64 : N == 2 ? 128 : 64, kPad = kCols + 4, kRun = kCols / 16;
   static_assert(4 * 16 * kPad * 4 <= sizeof(ring0), "room");
@@ -943,7 +957,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       S.m[rt] = kC4Low;
-      S.l[rt] = 0.f;
+      S.l[rt] = S.n[rt] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) S.o[rt][i] = c4_f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -982,17 +996,18 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     }
     if (faulty) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) S.l[rt] = __builtin_nanf("");
+      for (int rt = 0; rt < RT; ++rt) S.l[rt] = S.n[rt] = __builtin_nanf("");
     }
     // The four waves' rows together, a tile of 16 rows x kCols columns at a
     // time: column group 4 q + y of a lane holds D / 16 columns, of which a run
     // of kRun goes each time.
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const float l = c4_sum_quads(S.l[rt]);
+      const float l = c4_sum_quads(S.l[rt]), n = c4_sum_quads(S.n[rt]);
       if (q == 0) {
         ms[w][16 * rt + n16] = S.m[rt];
         ls[w][16 * rt + n16] = l;
+        ns[w][16 * rt + n16] = n;
       }
     }
     __syncthreads();  // also: every wave has emptied its buffers
@@ -1005,9 +1020,13 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
           S.m[rt] - fmaxf(fmaxf(ms[0][mine], ms[1][mine]), fmaxf(ms[2][mine], ms[3][mine])));
       const int rr = tid >> 4, row = 16 * rt + rr;  // this thread's row of the sums
       const float top = fmaxf(fmaxf(ms[0][row], ms[1][row]), fmaxf(ms[2][row], ms[3][row]));
-      float l = 0.f;
+      float l = 0.f, n = 0.f;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) l += ls[x][row] * __builtin_amdgcn_exp2f(ms[x][row] - top);
+      for (int x = 0; x < 4; ++x) {
+        const float g = __builtin_amdgcn_exp2f(ms[x][row] - top);
+        l += ls[x][row] * g;
+        n += ns[x][row] * g;
+      }
       const int32_t r = r0 + row, i = r / A.G, head = h * A.G + (r - i * A.G);
       const bool live = r < R && i < nnew;
 #pragma unroll
@@ -1030,18 +1049,19 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
           for (int e = 0; e < kRun; ++e) v[e] += oacc[(ww * 16 + rr) * kPad + grp * kRun + e];
         if (!live) continue;
         if (whole) {
-          c4_finish<kRun>(A, b, i, head, d0, v, top, l);
+          c4_finish<kRun>(A, b, i, head, d0, v, top, l, n);
         } else {
 #pragma unroll
           for (int e = 0; e < kRun; ++e) part[row * D + d0 + e] = v[e];
           if (d0 == 0) {
             part[kRows * D + row] = top;
             part[kRows * D + kRows + row] = l;
+            part[kRows * D + 2 * kRows + row] = n;
           }
         }
       }
     }
-    __syncthreads();  // the buffers, ms and ls are free
+    __syncthreads();  // the buffers, ms, ls and ns are free
   }
   note();
 }
@@ -1050,20 +1070,21 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
 template <int D>
 __device__ __forceinline__ void c4_gather(const float* first, const float* rest, int64_t floats, int rows,
                                           int row, int32_t x0, int32_t x1, int lane, float& m, float& l,
-                                          float (&v)[D / 64]) {
+                                          float& n, float (&v)[D / 64]) {
   constexpr int E = D / 64, N = 8;
   m = kC4Low;
-  l = 0.f;
+  l = n = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.f;
   for (int32_t base = x0; base < x1; base += N) {
-    float pm[N], pl[N], o[N][E];
+    float pm[N], pl[N], pn[N], o[N][E];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int32_t x = min(base + k, x1 - 1);
       const float* p = x == 0 ? first : rest + x * floats;
       pm[k] = p[rows * D + row];
       pl[k] = p[rows * D + rows + row];
+      pn[k] = p[rows * D + 2 * rows + row];
 #pragma unroll
       for (int e = 0; e < E; ++e) o[k][e] = p[row * D + lane * E + e];
     }
@@ -1074,6 +1095,7 @@ __device__ __forceinline__ void c4_gather(const float* first, const float* rest,
         const float f = __builtin_amdgcn_exp2f(m - top), g = __builtin_amdgcn_exp2f(pm[k] - top);
         m = top;
         l = l * f + pl[k] * g;
+        n = n * f + pn[k] * g;
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = v[e] * f + o[k][e] * g;
       }
@@ -1097,9 +1119,9 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join(C4AttnArgs A) {
   const int32_t r = hr % A.row_blocks * kRows + row, i = r / A.G;
   if (r >= A.T * A.G || i >= nnew) return;
   const float* rest = A.parts + (int64_t)blockIdx.x * 2 * kFloats;
-  float m, l, v[E];
-  c4_gather<D>(rest + slot * kFloats, rest, 2 * kFloats, kRows, row, 0, parts, lane, m, l, v);
-  c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l);
+  float m, l, n, v[E];
+  c4_gather<D>(rest + slot * kFloats, rest, 2 * kFloats, kRows, row, 0, parts, lane, m, l, n, v);
+  c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l, n);
 }
 
 // Joins those of calls with few segments of many records: a row a workgroup, a
@@ -1109,7 +1131,7 @@ template <int D, int RT>
 __global__ __launch_bounds__(256) void k_attention_cache4_join_long(C4AttnArgs A) {
   constexpr int kRows = RT * 16, E = D / 64;
   constexpr int64_t kFloats = C4Rec<D, RT>::kFloats;
-  __shared__ float vs[4][D], ms[4], ls[4];
+  __shared__ float vs[4][D], ms[4], ls[4], ns[4];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t per = (A.B + 63) / 64, HR = A.cache.heads * A.row_blocks;
   const int32_t b = blockIdx.x / HR, hr = blockIdx.x % HR, row = blockIdx.y;
@@ -1129,29 +1151,31 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join_long(C4AttnArgs A
   if (parts == 1) return;  // written whole
   const float* rest = A.parts + (int64_t)w0 * 2 * kFloats;
   const float* first = rest + (seg > w0 * share ? kFloats : 0);
-  float m, l, v[E];
+  float m, l, n, v[E];
   const int32_t quarter = (parts + 3) / 4;
-  c4_gather<D>(first, rest, 2 * kFloats, kRows, row, w * quarter, min(parts, w * quarter + quarter), lane, m, l, v);
+  c4_gather<D>(first, rest, 2 * kFloats, kRows, row, w * quarter, min(parts, w * quarter + quarter), lane, m, l, n, v);
 #pragma unroll
   for (int e = 0; e < E; ++e) vs[w][lane * E + e] = v[e];
   if (lane == 0) {
     ms[w] = m;
     ls[w] = l;
+    ns[w] = n;
   }
   __syncthreads();
   if (w) return;
   m = fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3]));
-  l = 0.f;
+  l = n = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = 0.f;
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
     const float f = __builtin_amdgcn_exp2f(ms[x] - m);
     l += ls[x] * f;
+    n += ns[x] * f;
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] += vs[x][lane * E + e] * f;
   }
-  c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l);
+  c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l, n);
 }
 
 }  // namespace sv

@@ -113,9 +113,10 @@ int spec_cache4_read(spec_cache4_t cache, spec_heads_t k, spec_heads_t v, int32_
  *   mask  words [T][ceil(T / 32)] of sequence b at mask + b * mask_seq_stride,
  *         row i at + i * mask_pos_stride (words; seq stride 0 shares one mask)
  *   scale finite, > 0
- *   out   [B][T][q_heads][head_dim] BF16, rounded once; the products take
- *         probabilities in BF16 relative to the running maximum, the sums and
- *         the normaliser are F32
+ *   out   [B][T][q_heads][head_dim] BF16, rounded once; the products and the
+ *         normaliser take the same probabilities, in BF16 relative to the
+ *         running maximum, so that out is a weighted mean of the values seen;
+ *         scores, sums and lse are F32
  *   lse   [B][T][q_heads] F32 or NULL
  * Rows i >= count[b] of out and lse are left as they were.
  * Limits: q_heads a multiple of heads, at most 16384; T <= SPEC_CACHE4_MAX_T;

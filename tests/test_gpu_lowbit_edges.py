@@ -129,3 +129,25 @@ def test_what_is_not_seen_does_not_matter(D):
         x = x.double().cpu().numpy()
         assert np.isnan(x[:, 4:]).all() and np.isfinite(x[:, fine]).all()
         assert (np.abs(x - y)[:, fine] <= t[:, fine]).all()
+
+
+@pytest.mark.parametrize("B,T,Hq,H,D,start", [
+    (1, 1, 8, 8, 64, [200]), (2, 9, 16, 2, 64, [900, 40]), (1, 7, 8, 1, 128, [2500]), (2, 1, 4, 2, 128, [5, 700]),
+    (3, 21, 8, 2, 128, [300, 2100, 0]), (1, 3, 8, 1, 256, [20000]), (2, 2, 8, 4, 256, [77, 1300]),
+])
+def test_values_that_agree_come_out_as_they_are(B, T, Hq, H, D, start):
+    """The output is a weighted mean, whatever the weights are rounded to: where all positions of a
+    head hold one value, which BF16 holds, it is that value.  (Its two sums are F32's, some 2^-14
+    apart at most; BF16's half step is 2^-9.)"""
+    rs = np.random.default_rng([3, B, T, D])
+    P = (max(start) + T + 63) // 64
+    pages = sv.cache4_alloc(B * P, H, D, DEV)
+    table = _i32(np.arange(B * P).reshape(B, P))
+    k = torch.tensor(rs.normal(0, 1, (B, P * 64, H, D)), dtype=torch.float32, device=DEV)
+    v = torch.tensor(rs.normal(0, 1, (B, 1, H, D)), dtype=torch.float32, device=DEV).expand(B, P * 64, H, D)
+    sv.cache4_write(pages, table, _i32([0] * B), k, v)
+    held = sv.cache4_read(pages, table, _i32([0] * B), 1, D)[1].repeat_interleave(Hq // H, 2)
+    for loud in (0.3, 1.0, 3.0, 10.0):  # from even weights to a few that count
+        q = torch.tensor(rs.normal(0, loud, (B, T, Hq, D)), dtype=torch.float32).bfloat16().to(DEV)
+        out = sv.attention_cache4(q, pages, table, _i32(start))
+        assert torch.equal(out, held.expand(B, T, Hq, D)), loud
