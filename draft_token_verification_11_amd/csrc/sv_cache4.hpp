@@ -450,8 +450,16 @@ __device__ __forceinline__ float c4_sum_quads(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-constexpr float kC4Low = -3.0e38f;  // a maximum before any score
-constexpr float kC4Raise = 8.0f;    // a score passes the maximum by 2^8 before it is raised
+// s c - m, the product rounded as the maximum's is.
+__device__ __forceinline__ float c4_scaled_less(float s, float c, float m) {
+#pragma clang fp contract(off)
+  const float x = s * c;
+  return x - m;
+}
+
+constexpr float kC4Low = -3.402823466e38f;  // a maximum before any score: no finite one is below it
+constexpr float kC4Raise = 8.0f;     // a score passes the maximum by 2^8 before it is raised
+constexpr float kC4Exact = 0x1p24f;  // up to here half a step of a maximum is 1/2 at most
 
 // What a row's new token sees of the 32 positions from `base` on (relative to
 // start): bit x for position base + x.
@@ -509,6 +517,8 @@ template <int D, int RT>
 struct C4State {
   c4_f32x4 o[RT][D / 16];
   float m[RT], l[RT], n[RT];  // maximum, sum of P' and of P' rounded
+  float less[RT];             // what a score's product is taken less: m, or 0 for rows that are far
+  uint64_t far;               // lanes of rows whose maximum has passed kC4Exact
 };
 
 // Takes the keys, and the values, of pair `half` of a page out of its buffer, by
@@ -669,21 +679,36 @@ __device__ __forceinline__ void c4_unit(const uint8_t* from, int half, Q rows_of
     float top = fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3]));
 #pragma unroll
     for (int r = 0; r < 4; ++r) top = fmaxf(top, s[rt][1][r]);
-    if (__any(top * c > S.m[rt] + kC4Raise)) {  // rare: the lanes of a row agree on it here
+    // rare, but for a wave with far rows; the lanes of a row agree on it here
+    if (__ballot(top * c > S.less[rt] + kC4Raise) | S.far) {
       const float m = fmaxf(S.m[rt], c4_max_quads(top) * c);
       const float f = __builtin_amdgcn_exp2f(S.m[rt] - m);
-      S.m[rt] = m;
+      S.m[rt] = S.less[rt] = m;
       S.l[rt] *= f;
       S.n[rt] *= f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) S.o[rt][i] *= f;
+      // Below, the exact product less the maximum, which is a rounded one: where
+      // scores are equal, off by half a step of the maximum, which P' and its sums
+      // have in common.  For far rows that would leave their range: they round the
+      // products as they did the maximum.
+      const bool far = __builtin_fabsf(m) > kC4Exact && m > kC4Low;
+      S.far |= __ballot(far);
+      if (far) {
+        const float back = 1.0f / c;  // c is above 2^-104 where a row is far
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) s[rt][i][r] = c4_scaled_less(s[rt][i][r], c, m) * back;
+        S.less[rt] = 0.f;
+      }
     }
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i][r], c, -S.m[rt]));
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i][r], c, -S.less[rt]));
         sum += e;
         p[rt][4 * i + r] = (__bf16)e;
       }
@@ -954,9 +979,10 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
       }
     };
     C4State<D, RT> S;
+    S.far = 0;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      S.m[rt] = kC4Low;
+      S.m[rt] = S.less[rt] = kC4Low;
       S.l[rt] = S.n[rt] = 0.f;
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) S.o[rt][i] = c4_f32x4{0.f, 0.f, 0.f, 0.f};

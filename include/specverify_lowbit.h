@@ -116,7 +116,9 @@ int spec_cache4_read(spec_cache4_t cache, spec_heads_t k, spec_heads_t v, int32_
  *   out   [B][T][q_heads][head_dim] BF16, rounded once; the products and the
  *         normaliser take the same probabilities, in BF16 relative to the
  *         running maximum, so that out is a weighted mean of the values seen;
- *         scores, sums and lse are F32
+ *         scores, sums and lse are F32: a row whose scores times scale log2 e,
+ *         or whose sums of up to 2^8 |V| a position, pass its range gets no
+ *         meaningful result, and no other row is touched
  *   lse   [B][T][q_heads] F32 or NULL
  * Rows i >= count[b] of out and lse are left as they were.
  * Limits: q_heads a multiple of heads, at most 16384; T <= SPEC_CACHE4_MAX_T;

@@ -151,3 +151,33 @@ def test_values_that_agree_come_out_as_they_are(B, T, Hq, H, D, start):
         q = torch.tensor(rs.normal(0, loud, (B, T, Hq, D)), dtype=torch.float32).bfloat16().to(DEV)
         out = sv.attention_cache4(q, pages, table, _i32(start))
         assert torch.equal(out, held.expand(B, T, Hq, D)), loud
+
+
+@pytest.mark.parametrize("e", [3, 20, 25, 31, 33, 60, 127])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("D,start", [(64, 0), (64, 70), (64, 1500), (128, 700), (256, 300)])
+def test_scores_of_any_magnitude(D, start, sign, e):
+    """Scores of 1.3 x 2^e, up to 7 % below where F32 ends for their products with log2 e, of either
+    sign: one position's has twice the others', which all have the same."""
+    P, n, loud = start // 64 + 1, start + 1, start // 2
+    pages = sv.cache4_alloc(P, 1, D, DEV)
+    rs = np.random.default_rng(4)
+    k = torch.full((1, P * 64, 1, D), 2.0 ** 59, device=DEV)
+    k[0, loud] *= 2
+    v = torch.tensor(rs.normal(0, 1, (1, P * 64, 1, D)), dtype=torch.float32, device=DEV)
+    table = _i32([list(range(P))])
+    sv.cache4_write(pages, table, _i32([0]), k, v)
+    score = sign * 1.296875 * 2.0 ** e
+    q = torch.full((1, 1, 1, D), score / D * 2.0 ** -60, dtype=torch.float64).bfloat16().to(DEV)
+    out, lse = sv.attention_cache4(q, pages, table, _i32([start]), scale=1.0, return_lse=True)
+    V = sv.cache4_read(pages, table, _i32([0]), n, D, dtype=torch.float32)[1][0, :, 0].double()
+    s = torch.full((n,), score / 2, dtype=torch.float64, device=DEV)
+    s[loud] = score
+    p = torch.softmax(s, 0)
+    want, mag = p @ V, p @ V.abs()
+    # scores are exact, their products with log2 e rounded once: an e of 3 leaves 2^-20 of that
+    few = n * 2.0 ** -24 + 2.0 ** -18
+    assert ((out[0, 0, 0].double() - want).abs() <= (2.0 ** -8 + few) * (mag + 2 * want.abs())).all()
+    if p.max() > 1 - 2.0 ** -20:
+        assert torch.equal(out[0, 0, 0].double(), V[p.argmax()])
+    assert abs(lse.item() - torch.logsumexp(s, 0).item()) <= 2.0 ** -21 * abs(score) + few
