@@ -22,6 +22,15 @@ __device__ __forceinline__ uint32_t f8_exponent(float amax) {
 // 2^(e - 127) of an exponent field e in [1, 254].
 __device__ __forceinline__ float f8_scale(uint32_t e) { return __uint_as_float(e << 23); }
 
+// A uniform scale's power of two as the matrix instructions' operand, 2^(e - 127), and
+// what is left of it: 1 to 2, or the whole of one below F32's normal range.
+__device__ __forceinline__ float f8_part(float s, int& e) {
+  const uint32_t x = __float_as_uint(s);
+  e = (int)(x >> 23 & 255u);
+  const uint32_t part = e ? (x & 0x807FFFFFu) | 0x3F800000u : __float_as_uint(s * 0x1p127f);
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(part));
+}
+
 // |x| for a block's maximum: finite magnitudes only.
 __device__ __forceinline__ float f8_mag(float x) {
   const float a = __builtin_fabsf(x);
@@ -113,14 +122,15 @@ __global__ __launch_bounds__(256) void k_hidden_fp8(F8HiddenArgs A) {
 // The product.  A operand the weights, Bt the hidden rows, so that a lane of a
 // 16 x 16 tile holds four neighbouring vocabulary entries of one hidden row.
 // The products of a block of 128 are summed by the matrix instructions from
-// zero and added to the running F32 sum times the block's scale (one FMA per
-// value).  Two ways to sum a block:
-//   F8   v_mfma_scale_f32_16x16x128_f8f6f4 on the e4m3 bytes, the hidden
-//        row's power of two as its scale operand.  It adds neighbouring
-//        products to about 14 bits (2-norm error 1.5e-5 on normal data), so it
-//        serves BF16 logits only.
+// zero and added to the running F32 sum (one FMA per value), with both scales or
+// without either, for with one of them a block may leave F32's range where its part
+// of the logit does not.  Two ways to sum a block:
+//   F8   v_mfma_scale_f32_16x16x128_f8f6f4 on the e4m3 bytes, the scales' powers of
+//        two as its scale operands.  It adds neighbouring products to about 14 bits
+//        (2-norm error 1.5e-5 on normal data), so it serves BF16 logits only.
 //   BF16 four v_mfma_f32_16x16x32_bf16 on the bytes widened to bf16, exact for
-//        e4m3 and for e4m3 times a power of two; sums as exact as F32's.
+//        e4m3; sums as exact as F32's, from 2^-18 to 2^25, and the FMA takes them
+//        times the product of the scales.
 // Both take a lane's inner index in the same order: lane group q = l / 16 holds
 // columns 16 q .. + 16 and 64 + 16 q .. + 16 of the block, two 16-byte loads.
 struct F8HeadArgs {
@@ -139,14 +149,14 @@ struct F8HeadArgs {
 typedef int f8_i32x4 __attribute__((ext_vector_type(4)));
 typedef int f8_i32x8 __attribute__((ext_vector_type(8)));
 
-// Bytes 8 h .. 8 h + 7 of a lane's 16 as bf16 times `scale` (a power of two).
-__device__ __forceinline__ f8_bf16x8 f8_widen(const uint4& w, int h, float scale) {
+// Bytes 8 h .. 8 h + 7 of a lane's 16 as bf16.
+__device__ __forceinline__ f8_bf16x8 f8_widen(const uint4& w, int h) {
   const uint32_t a = h ? w.z : w.x, b = h ? w.w : w.y;
   uint4 f;
-  f.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false));
-  f.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true));
-  f.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false));
-  f.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true));
+  f.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false));
+  f.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true));
+  f.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false));
+  f.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true));
   return __builtin_bit_cast(f8_bf16x8, f);
 }
 __device__ __forceinline__ f8_i32x8 f8_join(const uint4& a, const uint4& b) {
@@ -259,17 +269,17 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_rows(F8HeadArgs A) {
 #pragma unroll
     for (int k = 0; k < kFly; ++k) {
       if (u >= units) break;
-      const float sh = f8_scale(es[kb * 16 + n16]);
+      const float s = ring[k].s * f8_scale(es[kb * 16 + n16]);
       f8_f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const uint4 h = *reinterpret_cast<const uint4*>(hs + (2 * kb + x) * 1024 + lane * 16);
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen(ring[k].w[x], y, 1.0f), f8_widen(h, y, sh), c, 0, 0, 0);
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f8_widen(ring[k].w[x], y), f8_widen(h, y), c, 0, 0, 0);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(c[r], ring[k].s, acc[r]);
+      for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(c[r], s, acc[r]);
       load(ring[k]);
       kb = kb + 1 == blocks ? 0 : kb + 1;
       if (--todo == 0) {
@@ -379,8 +389,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_lmhead_fp8_tile(F8HeadArgs A)
   // issued together they hold the wave (and, after a barrier, all of them) for
   // 700 to 1,200 cycles of a block's 4,000.
   constexpr int kH = TM / 2;  // columns with the hidden rows' loads
+  float next = sp[0];  // the scale of the block to come: the first product takes it
   auto compute = [&](int32_t kb, uint8_t* wa, const uint8_t* ha, uint8_t* hn) {
-    const float s = sp[kb];
+    const float s = next;
+    next = sp[min(kb + 1, blocks - 1)];
     uint4 wf[TV][2];
 #pragma unroll
     for (int i = 0; i < TV; ++i)
@@ -391,13 +403,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_lmhead_fp8_tile(F8HeadArgs A)
 #pragma unroll
       for (int i = 0; i < TV; ++i)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) wb[i][y] = f8_widen(wf[i][y / 2], y & 1, 1.0f);
+        for (int y = 0; y < 4; ++y) wb[i][y] = f8_widen(wf[i][y / 2], y & 1);
     // a tile is added to the running sums while the matrix unit works on the one
     // in its place of the next column
     f8_f32x4 c[2][TV];
+    // F8: the powers of two go to the instruction, and what is left of the weights'
+    // scale to the sum (2,560 rows 1,511 us; with a factor of both scales for each
+    // column 1,537); else that factor
+    int we = 0;
+    float both[2];
+    if constexpr (F8) both[0] = both[1] = f8_part(s, we);
     auto add = [&](int i, int j) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(c[j & 1][i][r], s, acc[i][j][r]);
+      for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(c[j & 1][i][r], both[j & 1], acc[i][j][r]);
       // keeps the products here: without a use they may move past the barrier
       asm volatile("" : "+v"(acc[i][j]));
     };
@@ -427,16 +445,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_lmhead_fp8_tile(F8HeadArgs A)
 #pragma unroll
         for (int i = 0; i < TV; ++i) {
           c[j & 1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              f8_join(wf[i][0], wf[i][1]), hb, f8_f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 127, 0, (int)e[j & 1]);
+              f8_join(wf[i][0], wf[i][1]), hb, f8_f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, we, 0, (int)e[j & 1]);
           __builtin_amdgcn_sched_barrier(0);  // the order here is the one meant
           if (j) add(i, j - 1);
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {
-        const float sh = f8_scale(e[j & 1]);
+        both[j & 1] = f8_scale(e[j & 1]) * s;
         f8_bf16x8 hb[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) hb[y] = f8_widen(hf[j & 1][y / 2], y & 1, sh);
+        for (int y = 0; y < 4; ++y) hb[y] = f8_widen(hf[j & 1][y / 2], y & 1);
 #pragma unroll
         for (int i = 0; i < TV; ++i) c[j & 1][i] = f8_f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll

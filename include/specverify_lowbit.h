@@ -152,7 +152,8 @@ int spec_quantize_fp8(const void* weight, int32_t dtype, int64_t weight_stride, 
  *   hidden  [B][rows][d] F32 or BF16, strides in elements; rows 16-byte aligned
  *   weight  [V][d] e4m3, row v at v * weight_stride bytes (a multiple of 16, at
  *           most 2^22)
- *   scale   [ceil(V/128)][ceil(d/128)] F32, any finite values, contiguous
+ *   scale   [ceil(V/128)][ceil(d/128)] F32, contiguous, any finite values whose
+ *           products with the hidden rows' scales are in F32's range
  *   logits  [B][rows][V] F32 or BF16 (spec_logits_t addressing, written; its
  *           rows lie apart)
  * F32 logits are sums held in F32.  BF16 logits may be summed by the 8-bit

@@ -181,3 +181,25 @@ def test_scores_of_any_magnitude(D, start, sign, e):
     if p.max() > 1 - 2.0 ** -20:
         assert torch.equal(out[0, 0, 0].double(), V[p.argmax()])
     assert abs(lse.item() - torch.logsumexp(s, 0).item()) <= 2.0 ** -21 * abs(score) + few
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [-130, 100, 119])
+@pytest.mark.parametrize("B,rows,V,d", [(1, 3, 130, 160), (5, 9, 300, 288), (30, 5, 200, 160), (52, 5, 270, 128)])
+def test_hidden_rows_of_any_magnitude(B, rows, V, d, e, dtype, out_dtype):
+    """Rows of 2^e against weights of 2^(-e / 2): the logits' magnitudes are far from F32's ends,
+    and so is their error."""
+    rs = np.random.default_rng([5, B, d])
+    q, s = plain.quantize8(rs.normal(0, 0.05, (V, d)))
+    s = (s * rs.uniform(0.5, 1.5, s.shape) * 2.0 ** (-e // 2)).astype(np.float32)
+    h = rs.normal(0, 1, (B, rows, d)) * np.exp2(rs.integers(-3, 4, (1, 1, d)))
+    h = torch.tensor(h * 2.0 ** e, dtype=torch.float64).to(dtype)
+    got = sv.lmhead_fp8(h.to(DEV), torch.tensor(q).to(torch.float8_e4m3fn).to(DEV), torch.tensor(s).to(DEV),
+                        out_dtype=out_dtype)
+    want, mag = plain.head8(h.double().numpy().reshape(-1, d), q, s.astype(np.float64))
+    off = np.abs(got.double().cpu().numpy().reshape(want.shape) - want)
+    bound = mag * (d + 160) * 2.0 ** -24
+    if out_dtype is torch.bfloat16:
+        bound = mag * 2.0 ** -12 + np.abs(want) * 2.0 ** -8 * 1.01
+    assert (off <= bound).all(), (off / bound).max()
