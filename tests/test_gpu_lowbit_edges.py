@@ -280,3 +280,98 @@ def test_weight_scales_of_any_magnitude(M, out_dtype):
     held = mag < 2.0 ** 127
     assert held[:, :384].all() and held[:, 512:].all() and (np.abs(got - want) <= few)[held].all()
     assert (got[:, 128:256] == 0).all() and np.abs(got[:, 256:384]).min(0).max() > 2.0 ** -115
+
+
+def test_the_quantiser_rounds_what_is_below_the_normal_range():
+    """Weights and blocks below F32's normal range, to the nearest of e4m3 times 2^-126, ties to even."""
+    m = np.array([1, 2, 3, 1.5, 0.5, 0.75, 0.25, 5, 7, 100, 448, 449.0])
+    w = torch.tensor(np.stack([np.resize(m * 2.0 ** -(126 + x), 128) for x in (9, 5, 1, 0)]), dtype=torch.float32)
+    want, p = plain.quantize8(w.double().numpy())
+    q, s = sv.quantize_fp8(w.to(DEV))
+    assert np.array_equal(q.double().cpu().numpy(), want) and s.item() == p[0, 0] == 2.0 ** -125
+    for row in w:  # alone, at the least scale
+        want, p = plain.quantize8(row[None].double().numpy())
+        q, s = sv.quantize_fp8(row[None].to(DEV))
+        assert np.array_equal(q.double().cpu().numpy(), want) and s.item() == p[0, 0]
+
+
+def test_a_sequence_of_the_most_positions():
+    """2^30 positions, the most a table's 2^24 columns hold: written at the end, read back there, and
+    attended to (pages of the pool come again and again: a closed form)."""
+    P, D, T, n = 1 << 24, 64, 6, 5
+    rs = np.random.default_rng(8)
+    pages = sv.cache4_alloc(n, 1, D, DEV)
+    k, v = (torch.tensor(rs.normal(0, 1, (n, 64, 1, D)), dtype=torch.float32, device=DEV) for _ in range(2))
+    sv.cache4_write(pages, _i32(np.arange(n)[:, None]), _i32([0] * n), k, v)
+    table = (torch.arange(P, device=DEV) % (n - 1)).int()[None].contiguous()
+    table[0, P - 1] = n - 1  # the last page is the new tokens' own
+    start = _i32([64 * P - T])
+    kn, vn = (torch.tensor(rs.normal(0, 1, (1, T, 1, D)), dtype=torch.float32, device=DEV) for _ in range(2))
+    sv.cache4_write(pages, table, start, kn, vn)
+    raw, want = pages.cpu().numpy(), [np.stack([plain.value4(*x) for x in part]) for part in
+                                      zip(*(plain.token4(a, b) for a, b in zip(kn[0, :, 0].cpu().numpy(),
+                                                                               vn[0, :, 0].cpu().numpy())))]
+    for got, x in zip(sv.cache4_read(pages, table, start, T, D, dtype=torch.float32), want):
+        assert np.array_equal(got[0, :, 0].double().cpu().numpy(), x)
+    q = torch.tensor(rs.normal(0, 1, (1, T, 1, D)), dtype=torch.float32).bfloat16().to(DEV)
+    out, lse = sv.attention_cache4(q, pages, table, start, return_lse=True)
+    K, V = (np.array([[plain.fetch(raw, np.arange(n)[:, None], b, 0, x, D)[j] for x in range(64)] for b in range(n)])
+            for j in range(2))
+    times = np.array([(P - 1 - b + n - 2) // (n - 1) for b in range(n - 1)] + [1.0])
+    assert times.sum() == P
+    for i in range(T):
+        s = K @ q[0, i, 0].double().cpu().numpy() / D ** 0.5
+        s[n - 1, 64 - T + i + 1:] = -np.inf
+        p = np.exp(s - s.max()) * times[:, None]
+        l = s.max() + np.log(p.sum())
+        p /= p.sum()
+        y, mag = (p[..., None] * V).sum((0, 1)), (p[..., None] * np.abs(V)).sum((0, 1))
+        # a wave adds up 1 / 1,536 of the pages' halves, 32 positions at a time
+        few = 2 * (D + 2) * 2.0 ** -24 * (np.abs(K) @ np.abs(q[0, i, 0].double().cpu().numpy())).max() / 8 + \
+            (P // 768 + 64) * 2.0 ** -24
+        assert (np.abs(out[0, i, 0].double().cpu().numpy() - y) <= (2.0 ** -8 + few) * (mag + 2 * np.abs(y))).all()
+        assert abs(lse[0, i, 0].item() - l) <= few + l * 2.0 ** -21
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,rows", [(1, 1), (1, 129)])
+def test_the_widest_rows(B, rows, out_dtype):
+    V, d = 130, 65536
+    rs = np.random.default_rng([9, rows])
+    w = torch.tensor(rs.normal(0, 0.05, (V, d)), dtype=torch.float32, device=DEV)
+    q, s = sv.quantize_fp8(w)
+    want, p = plain.quantize8(w[:, -256:].double().cpu().numpy())
+    assert np.array_equal(q[:, -256:].double().cpu().numpy(), want) and np.array_equal(s[:, -2:].cpu().numpy(), p)
+    h = torch.tensor(rs.normal(0, 1, (B * rows, d)), dtype=torch.float32)
+    got = sv.lmhead_fp8(h.view(B, rows, d).to(DEV), q, s, out_dtype=out_dtype).double().cpu().numpy()[0]
+    want, mag = plain.head8(h.double().numpy(), q.double().cpu().numpy(), s.double().cpu().numpy())
+    few = mag * (d / 128 + 160) * 2.0 ** -24
+    if out_dtype is torch.bfloat16:
+        few = few + 1.5 * 7 * 2.0 ** -13 * mag  # the eights' largest products are below their magnitudes
+        few = few + (np.abs(want) + few) * 2.0 ** -8
+    assert (np.abs(got - want) <= few).all()
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+def test_the_most_entries(rows):
+    """2^24 entries: the last ones, and some between, as in a head of those alone."""
+    V, d, n = 1 << 24, 32, 1280
+    g = torch.Generator(DEV).manual_seed(10)
+    q = torch.randint(0, 126, (V, d), generator=g, device=DEV, dtype=torch.uint8).view(torch.float8_e4m3fn)
+    s = torch.rand(V // 128, 1, generator=g, device=DEV) + 0.5
+    h = torch.randn(1, rows, d, generator=g, device=DEV)
+    got = sv.lmhead_fp8(h, q, s)
+    for v0 in (0, V // 2 - 640, V - n):
+        want = sv.lmhead_fp8(h, q[v0:v0 + n].contiguous(), s[v0 // 128:(v0 + n) // 128].contiguous())
+        assert torch.equal(got[..., v0:v0 + n], want)
+
+
+def test_the_most_rows():
+    """2^24 sequences of one row: some of them as in a call of those alone."""
+    B, V, d = 1 << 24, 3, 32
+    g = torch.Generator(DEV).manual_seed(11)
+    q, s = sv.quantize_fp8(torch.randn(V, d, generator=g, device=DEV))
+    h = torch.randn(B, 1, d, generator=g, device=DEV, dtype=torch.bfloat16)
+    got = sv.lmhead_fp8(h, q, s)
+    for b0 in (0, B // 2 - 77, B - 300):
+        assert torch.equal(got[b0:b0 + 300], sv.lmhead_fp8(h[b0:b0 + 300].contiguous(), q, s))
