@@ -64,7 +64,8 @@ struct C4Heads {
 // the wave together.  Bound by memory: each value is read once and written
 // once, and only the exponent bytes (1 of 17 stored) are scattered.  4 x 8,191
 // tokens of 8 heads of 128, BF16 (170 MB in and out): written in 46 us (3.7 TB/s),
-// read back in 29.5 us (5.8 TB/s); 64 x 6 tokens: 4 us each.  A wave over all four
+// read back in 29.7 us (5.7 TB/s); 4 x 4,095 tokens F32 35 and 29 us, heads of 256
+// BF16 49 and 31; 64 x 6 tokens: 4 us each.  A wave over all four
 // sixteens of a page, which stores key exponents as dwords, took 51 us.
 struct C4MoveArgs {
   C4View cache;
@@ -288,13 +289,22 @@ __global__ __launch_bounds__(256) void k_cache4_read(C4MoveArgs A) {
 // another half of the matrix instructions: 67.5, 107 and 46.4 us, and 131,003
 // tokens x 36 rows 57.2 instead of 48.9.
 //
-// Bound by the cache's bytes where rows are few and sequences long (64 x 8 heads
-// of 128, 24 rows over 1,500 to 4,091 tokens, 201 MB: 55 us, 3.6 TB/s; the launch
-// and the first loads take about 6 of them, each segment's end 5, and workgroups
-// end at different times), by the conversions, exponentials and products of a wave
-// following each other where they are many (16 x 8 heads, 168 rows over 37 to
-// 8,155 tokens: 81 us, matrix units busy for a third of them), by the launch for
-// one short sequence (10 us).
+// What bounds it (times of this kernel; where two times are compared elsewhere in
+// this file, both are of the build that the choice was made in).
+//   - Few rows, long sequences of one length: the cache's bytes (64 x 8 heads of
+//     128, 24 rows over 4,090 tokens, 292 MB: 65 us, 4.5 TB/s).
+//   - The same with ragged lengths: the ends of segments as well, about 5 us of a
+//     workgroup each, and workgroups that end at different times (1,500 to 4,091
+//     tokens, 201 MB: 58 us, 3.5 TB/s).
+//   - Many rows: the vector unit, which converts and permutes a page's codes anew
+//     for each block of rows, and the products that wait for it (16 x 8 heads, 168
+//     rows over 37 to 8,155 tokens: 90 to 93 us; vector instructions in 57 % of the
+//     busy cycles, matrix units in 28 %).
+//   - One short sequence: a chain of loads that wait for each other (lengths, table,
+//     pages) and few workgroups that go through its pages (777 tokens: 11 us, on 8 of
+//     768; a launch that does less, such as the cache write's, takes under 4).
+//   - Very many sequences: finding the shares, for which every wave reads all
+//     lengths (65,536 sequences: 0.67 ms, without any page; 1,000: nothing that shows).
 //
 // Work split: the pages of all (sequence, kv head, block of rows) are laid end
 // to end and cut into one equal range per workgroup, whatever the sequences'

@@ -304,10 +304,12 @@ __global__ __launch_bounds__(512, 2) void k_lmhead_fp8_rows(F8HeadArgs A) {
 // c ^ (row / 2 % 8), by permuting the addresses that the lanes load from, so that
 // the 16 rows a quarter of a fragment read touches (256 bytes) fall on the 64
 // banks without conflict.  2,560 rows over 151,936 x 4,096 to BF16 logits: 1.50 ms,
-// 2.1 PFLOP/s (the matrix units busy for 53 % of it; LDS reads and fills take as
-// many cycles, and the chip's clock falls to 2.0 GHz); 240 rows over 128,003 x
-// 2,080 to F32: 0.17 to 0.20 ms, of which rows that do not start at multiples of 16
-// bytes cost a tenth or more (over 128,000 entries: 0.16 to 0.18).
+// 2.1 PFLOP/s (the matrix units busy for 52 % of it, vector instructions for 57 %;
+// LDS reads and fills take as many cycles, and the chip's clock falls to 2.0 GHz);
+// 240 rows over 128,003 x 2,080 to F32: 0.17 ms, 0.20 where the weights come from
+// memory (matrix units busy for 40 %, vector instructions, which widen, for 51 %), of
+// which rows that do not start at multiples of 16 bytes cost a tenth or more (over
+// 128,000 entries: 0.16 to 0.18).
 template <typename TO, bool F8, int BV, int BM, int WV, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_lmhead_fp8_tile(F8HeadArgs A) {
   constexpr int WM = WAVES / WV, TV = BV / WV / 16, TM = BM / WM / 16;  // a wave's tiles of 16

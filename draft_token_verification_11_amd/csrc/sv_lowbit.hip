@@ -122,14 +122,15 @@ void launch_read(int32_t d, unsigned grid, const sv::C4MoveArgs& A, hipStream_t 
 // Row tiles of 16 a workgroup keeps, and how many such blocks hold the rows of a
 // kv head.  More tiles convert the cache's codes less often, but their
 // accumulators leave room for fewer waves.  Times of the whole call:
-//   heads of 128  48 rows, 16 x 8 heads over up to 8,155 tokens: 47 us in tiles
-//                 of 1, 48 of 2, 40 of 3; four leave one wave a SIMD (168 rows
-//                 took 171 us in blocks of four where three took 102)
-//   heads of 64   48 rows, 96 x 16 heads over up to 2,045: 94, 90, 75; 64 rows:
-//                 117, 94 and in blocks of four 95; 176 rows, 16 x 8 heads over
-//                 up to 8,155: 71 in blocks of 2, 69 of 3, 68 of 4
+//   heads of 128  48 rows, 16 x 8 heads over up to 8,155 tokens: 48 us in tiles
+//                 of 1, 47 of 2, 39 of 3; 168 rows: 133, 100, 91; four leave one
+//                 wave a SIMD (171 in an earlier build where three took 102)
+//   heads of 64   48 rows, 96 x 16 heads over up to 2,045: 95, 95, 81; 64 rows:
+//                 121, 100 and in a block of four 102; 176 rows, 16 x 8 heads
+//                 over up to 8,155: 83, in blocks of 2 or 3 73, of 4 72
 //   heads of 256  32 rows, 32 x 4 heads over up to 8,000: 60 in tiles of 1, 64 of
-//                 2; 168 rows, 16 x 4 heads: 127 and 153
+//                 2; 168 rows, 16 x 4 heads: 127 and 153 (both of an earlier
+//                 build; now 60 and 123)
 int max_tiles(int32_t d) { return d == 256 ? 1 : d == 128 ? 3 : 4; }
 void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
   const int64_t t = (rows + 15) / 16;
@@ -138,9 +139,12 @@ void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
 }
 
 // Tables of at most this many pages a sequence are not cut: the pass that joins
-// cut ones costs about 5 us.  16 pages, 8 sequences of 8 heads: 11.2 us whole, 14.9
-// cut; 96 of 16: 25.3 and 28.1; 24 pages: 13.8 and 15.2, 34.3 and 32.7; 32 pages,
-// one sequence of 8 heads: 16.4 and 13.5.
+// cut ones costs 4 us where there are few (one sequence of 8 heads) and up to 13 (16
+// x 8 heads, 168 rows).  Whole calls: 16 pages, 8 sequences of 8 heads 12.1 us whole,
+// 14.6 cut, 96 of 16 26.3 and 28.6; 20 pages 13.3 and 14.7, 30.9 and 31.5; 24 pages
+// 14.8 and 14.8, 35.2 and 34.2; 32 pages, one sequence of 8 heads 17.0 and 14.7.  The
+// rule sees the table's width, not the lengths, which stand in device memory: 777
+// tokens of one sequence take 11.9 us with a table of 13 columns, 14.0 with one of 512.
 constexpr int32_t kAttnWhole = 20;
 // Up to this many segments (sequences x heads x blocks of rows) each is in four
 // records or more on average, and their rows are joined by a workgroup each (4 x 8
@@ -222,7 +226,7 @@ constexpr unsigned kHeadGrid = 256;
 template <typename TO>
 void launch_head(const sv::F8HeadArgs& A, hipStream_t st) {
   constexpr bool f8 = sizeof(TO) == 2;  // BF16 logits: the 8-bit instructions' sums do
-  // Up to 16 rows whose LDS image fits (rows of 8,192): 0.124 ms, in tiles 0.134.
+  // Up to 16 rows whose LDS image fits (rows of 8,192): 0.122 ms, in tiles 0.134.
   if (A.M <= 16 && A.dp <= 8192) {
     if (A.dp <= 4096)
       hipLaunchKernelGGL((sv::k_lmhead_fp8_rows<TO, 32>), dim3(kHeadGrid), dim3(512), 0, st, A);
@@ -238,9 +242,13 @@ void launch_head(const sv::F8HeadArgs& A, hipStream_t st) {
   // Two workgroups of four waves a compute unit, which fill each other's waits
   // (120 rows, F32: 0.188 ms, one of eight waves 0.224), and where the matrix
   // instructions bind, one of eight with wave tiles of 64 x 128, which read LDS
-  // less (2,560 rows, BF16: 1.70 ms, in the small tiles 1.85), unless it pads
-  // more rows.  F32 logits need four times the instructions a block; there LDS
-  // does not bind (2,560 rows: 3.12 ms either way).
+  // less, unless it pads more rows.  Where it does, in tiles of 128 and of 256: 260
+  // rows 266 and 304 us, 520 441 and 432, 1,300 978 and 875, 2,565 1,932 and 1,654;
+  // over 32,003 x 2,080 520 rows 76 and 87, 1,300 146 and 138, 1,650 174 and 178.  So
+  // from about 1,280 rows on the small tiles lose mostly: the rule does not see that.
+  // (2,560 rows, which pad none: 1,510 to 1,530.)  F32 logits need four times the
+  // instructions a block; there LDS does not bind (2,560 rows: 3.03 ms, in an earlier
+  // build 3.12 either way).
   if constexpr (f8)
     if ((A.M + 255) / 256 * 256 == (A.M + 127) / 128 * 128) {
       launch_head_tile<TO, f8, 256, 256, 4, 8>(A, st);
