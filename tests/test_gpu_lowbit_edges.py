@@ -375,3 +375,45 @@ def test_the_most_rows():
     got = sv.lmhead_fp8(h, q, s)
     for b0 in (0, B // 2 - 77, B - 300):
         assert torch.equal(got[b0:b0 + 300], sv.lmhead_fp8(h[b0:b0 + 300].contiguous(), q, s))
+
+
+@pytest.mark.parametrize("D,T,G,start", [(64, 16, 4, 300), (64, 3, 8, 1500), (128, 12, 4, 200), (128, 7, 4, 2000), (256, 2, 8, 700)])
+def test_rows_of_all_magnitudes_together(D, T, G, start):
+    """Rows side by side whose scores are ordinary, large (softmax takes one position) and not finite:
+    each as if it stood alone."""
+    rs = np.random.default_rng([12, D, T])
+    P = (start + T + 63) // 64
+    pages = sv.cache4_alloc(P, 1, D, DEV)
+    table = np.arange(P)[None]
+    k, v = (torch.tensor(rs.normal(0, 1, (1, P * 64, 1, D)), dtype=torch.float32, device=DEV) for _ in range(2))
+    sv.cache4_write(pages, _i32(table), _i32([0]), k, v)
+    e = rs.permutation(np.resize([0, 0, 0, 12, 24, 30, 60, 100], T * G)).reshape(T, G)
+    q = torch.tensor(rs.normal(0, 1, (1, T, G, D)) * np.exp2(e)[None, :, :, None], dtype=torch.float32).bfloat16()
+    bad = rs.permutation(np.arange(T * G) == 0).reshape(T, G)
+    q[0][torch.tensor(bad)] = float("nan")
+    out, lse = (x.double().cpu().numpy()[0] for x in sv.attention_cache4(q.to(DEV), pages, _i32(table), _i32([start]),
+                                                                        return_lse=True))
+    K, V = (x[0, :, 0].double().cpu().numpy() for x in sv.cache4_read(pages, _i32(table), _i32([0]), P * 64, D,
+                                                                     dtype=torch.float32))
+    for i in range(T):
+        n = start + i + 1
+        for g in range(G):
+            if bad[i, g]:
+                assert np.isnan(out[i, g]).all() and np.isnan(lse[i, g])
+                continue
+            x = q[0, i, g].double().numpy()
+            s = K[:n] @ x / D ** 0.5
+            off = (np.abs(K[:n]) @ np.abs(x)).max() / D ** 0.5 * (D + 2) * 2.0 ** -24
+            p = np.exp(s - s.max())
+            l = s.max() + np.log(p.sum())
+            p /= p.sum()
+            assert abs(lse[i, g] - l) <= off + n * 2.0 ** -24 + abs(l) * 2.0 ** -21
+            few = 2 * off + 2.0 ** -21 + n * 2.0 ** -24
+            if few < 2.0 ** -6:
+                y, mag = p @ V[:n], p @ np.abs(V[:n])
+                assert (np.abs(out[i, g] - y) <= (2.0 ** -8 + few) * (mag + 2 * np.abs(y))).all()
+            else:  # one position, or several that F32 cannot tell apart
+                near = V[:n][s >= s.max() - 2 * off - 20]
+                # each of the others has e^-20 of the largest weight at most, whatever its score's error
+                slack = 2.0 ** -7 * np.abs(near).max(0) + n * np.exp(-20) * np.abs(V[:n]).max(0)
+                assert (out[i, g] >= near.min(0) - slack).all() and (out[i, g] <= near.max(0) + slack).all()
