@@ -29,6 +29,7 @@ __all__ = ["lib", "verify_stochastic", "verify_greedy", "logits_process", "works
            "verify_stochastic_noalloc", "NOALLOC_SCRATCH_BYTES",
            "CACHE4_PAGE", "cache4_record_bytes", "cache4_alloc", "cache4_write", "cache4_read",
            "attention_cache4", "tree_mask", "quantize_fp8", "lmhead_fp8",
+           "norm_rotate", "tree_depths", "attention_cache4_shared", "cache4_reserve", "cache4_slots",
            "library_path"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -71,6 +72,15 @@ class spec_heads_t(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("seq_stride", ctypes.c_int64),
                 ("pos_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class spec_rotate_t(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_dtype", ctypes.c_int32),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("depth", ctypes.c_void_p),
+                ("depth_stride", ctypes.c_int64)]
 
 
 class SpecError(RuntimeError):
@@ -155,6 +165,24 @@ def lib():
             L.spec_lmhead_fp8.argtypes = [spec_logits_t, i32, i32, i32, vp, i64, vp, i32,
                                           spec_logits_t, vp, sz, vp]
             L.spec_lmhead_fp8.restype = ctypes.c_int
+            L.spec_norm_rotate.argtypes = [spec_heads_t, spec_heads_t, i32, spec_heads_t,
+                                           spec_heads_t, i32, P(spec_rotate_t), i32, i32, vp, vp, vp]
+            L.spec_norm_rotate.restype = ctypes.c_int
+            L.spec_attention_cache4_window.argtypes = [spec_cache4_t, spec_heads_t, i32, i32, i32,
+                                                       vp, vp, vp, i64, i64, vp, i64, i32, i32,
+                                                       ctypes.c_float, spec_heads_t, vp, vp, sz, vp]
+            L.spec_attention_cache4_window.restype = ctypes.c_int
+            L.spec_attention_cache4_shared_workspace.argtypes = [i32] * 6
+            L.spec_attention_cache4_shared_workspace.restype = sz
+            L.spec_attention_cache4_shared.argtypes = [spec_cache4_t, vp, i64, i32, vp, i32,
+                                                       spec_heads_t, i32, i32, i32, vp, vp, vp, i64,
+                                                       i64, ctypes.c_float, spec_heads_t, vp, vp,
+                                                       sz, vp]
+            L.spec_attention_cache4_shared.restype = ctypes.c_int
+            L.spec_cache4_reserve.argtypes = [vp, i64, i32, vp, vp, i32, vp, i32, vp, vp]
+            L.spec_cache4_reserve.restype = ctypes.c_int
+            L.spec_cache4_slots.argtypes = [vp, i64, i32, i32, i32, i32, vp, vp, vp, vp]
+            L.spec_cache4_slots.restype = ctypes.c_int
             L.spec_status_string.argtypes = [ctypes.c_int]
             L.spec_status_string.restype = ctypes.c_char_p
             _lib = L
@@ -722,19 +750,46 @@ def _heads(t, what, shape=None) -> spec_heads_t:
                         0, s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
 
 
+def _table(table, what, rows, index):
+    """A page table [rows][cols], checked: (cols, the stride of its rows)."""
+    _device_tensor(table, what, (torch.int32,), 2, index)
+    n, cols = table.shape
+    if n != rows or (table.stride(1) != 1 and cols > 1):
+        raise ValueError("%s must be [%d][pages of a sequence] with a contiguous last axis" % (what, rows))
+    return cols, table.stride(0) if n > 1 else max(1, cols)
+
+
 def _cache4(pages, table, D, B, index=None):
     """(the cache's descriptor, its device's index)."""
     index = _device_tensor(pages, "pages", (torch.uint8,), 3, index)
-    _device_tensor(table, "table", (torch.int32,), 2, index)
     n, heads, record = pages.shape
     if record != 68 * D or not pages.is_contiguous():
         raise ValueError("pages must be contiguous [n_pages][heads][%d] for heads of %d, got %s"
                          % (68 * D, D, tuple(pages.shape)))
-    rows, cols = table.shape
-    if rows != B or (table.stride(1) != 1 and cols > 1):
-        raise ValueError("table must be [%d][pages of a sequence] with a contiguous last axis" % B)
-    return spec_cache4_t(pages.data_ptr(), table.data_ptr(),
-                         table.stride(0) if rows > 1 else max(1, cols), n, cols, heads, D), index
+    cols, stride = _table(table, "table", B, index)
+    return spec_cache4_t(pages.data_ptr(), table.data_ptr(), stride, n, cols, heads, D), index
+
+
+def _mask_words(mask, B, T, index):
+    """Mask words [B|1][T][ceil(T / 32)] or None: (pointer, sequence stride, row stride)."""
+    if mask is None:
+        return None, 0, 0
+    _device_tensor(mask, "mask", (torch.int32,), 3, index)
+    rows, words = mask.shape[0], (T + 31) // 32
+    if rows not in (1, B) or tuple(mask.shape[1:]) != (T, words) or \
+            (mask.stride(2) != 1 and words > 1):
+        raise ValueError("mask must be int32 words [B|1][%d][%d] with contiguous words" % (T, words))
+    return mask.data_ptr(), mask.stride(0) if rows > 1 else 0, mask.stride(1) if T > 1 else 0
+
+
+def _depths(depth, B, T, index):
+    """Depths [B|1][T] or None: (pointer, sequence stride)."""
+    if depth is None:
+        return None, 0
+    _device_tensor(depth, "depth", (torch.int32,), 2, index)
+    if depth.shape[0] not in (1, B) or depth.shape[1] != T or (depth.stride(1) != 1 and T > 1):
+        raise ValueError("depth must be int32 [B|1][%d] with a contiguous last axis" % T)
+    return depth.data_ptr(), depth.stride(0) if depth.shape[0] > 1 else 0
 
 
 def _per_sequence(t, what, B, index):
@@ -835,12 +890,27 @@ def tree_mask(parents) -> torch.Tensor:
     return torch.tensor([signed], dtype=torch.int32)
 
 
+def tree_depths(parents) -> torch.Tensor:
+    """The depths of a parent-pointer candidate tree's nodes (tree_branches), the
+    root's 0: int32 [1][N] on the CPU."""
+    par = [int(x) for x in (parents.tolist() if hasattr(parents, "tolist") else parents)]
+    if not par or par[0] != -1:
+        raise ValueError("a tree needs a root (parent -1)")
+    depth = [0] * len(par)
+    for i in range(1, len(par)):
+        if not 0 <= par[i] < i:
+            raise ValueError("node %d: parent must precede it" % i)
+        depth[i] = depth[par[i]] + 1
+    return torch.tensor([depth], dtype=torch.int32)
+
+
 def attention_cache4(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor,
                      start: torch.Tensor, *, count: torch.Tensor | None = None,
                      mask: torch.Tensor | None = None, scale: float | None = None,
                      return_lse: bool = False, out: torch.Tensor | None = None,
                      lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
-                     stream=None):
+                     stream=None, window: int | None = None, sinks: int = 0,
+                     depth: torch.Tensor | None = None):
     """Attention of new positions over a 4-bit cache that already holds their
     own keys and values (cache4_write with the same start and count).
     q [B][T][q_heads][D] bfloat16, q_heads a multiple of the cache's heads.
@@ -851,22 +921,30 @@ def attention_cache4(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor,
     and, with return_lse or an ``lse`` tensor, the log of the softmax's
     denominator [B][T][q_heads] float32.  Rows past count[b] are zero, or left
     as they were in the caller's tensors; a token that sees nothing gets 0 and
-    -inf; ill-formed sequences get NaN."""
+    -inf; ill-formed sequences get NaN.
+
+    With ``window`` a token sees only those cached tokens that are less than
+    ``window`` positions behind it, and the first ``sinks`` of the sequence; in a
+    chain that holds for the new tokens too, while a mask alone says what new
+    tokens see of each other.  Token i stands at start[b] + i, or at start[b] +
+    depth[b][i] with ``depth`` int32 [B|1][T] (tree_depths), which needs a mask.
+    Pages that no token sees are not read, and their table entries may hold
+    anything."""
     index = _device_tensor(q, "q", (torch.bfloat16,), 4)
     B, T, Hq, D = q.shape
     cache, _ = _cache4(pages, table, D, B, index)
     if start is None:
         raise ValueError("start is required")
+    if window is None and (sinks or depth is not None):
+        raise ValueError("sinks and depth need a window")
+    if window is not None and not (1 <= window < 1 << 31 and 0 <= sinks < 1 << 31):
+        raise ValueError("window must be at least 1 and sinks at least 0, got %s and %s" % (window, sinks))
+    if depth is not None and mask is None:
+        raise ValueError("depth needs a mask")
     s = _per_sequence(start, "start", B, index)
     n = _per_sequence(count, "count", B, index)
-    mp, ms, mr = None, 0, 0
-    if mask is not None:
-        _device_tensor(mask, "mask", (torch.int32,), 3, index)
-        rows, words = mask.shape[0], (T + 31) // 32
-        if rows not in (1, B) or tuple(mask.shape[1:]) != (T, words) or \
-                (mask.stride(2) != 1 and words > 1):
-            raise ValueError("mask must be int32 words [B|1][%d][%d] with contiguous words" % (T, words))
-        mp, ms, mr = mask.data_ptr(), mask.stride(0) if rows > 1 else 0, mask.stride(1) if T > 1 else 0
+    mp, ms, mr = _mask_words(mask, B, T, index)
+    dp, ds = _depths(depth, B, T, index)
     if lse is not None:
         _out_tensor(lse, (B, T, Hq), torch.float32, q.device, "lse")
     if out is not None:
@@ -884,12 +962,17 @@ def attention_cache4(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor,
         if return_lse and lse is None:
             lse = make((B, T, Hq), dtype=torch.float32, device=q.device)
         ws = _scratch(workspace, q.device, need)
-        rc = L.spec_attention_cache4(
-            cache, _heads(q, "q"), B, T, Hq, s, n, mp, ms, mr,
-            float(scale) if scale is not None else D ** -0.5, _heads(out, "out", q.shape),
-            lse.data_ptr() if lse is not None else None, ws.data_ptr(),
-            ws.numel() * ws.element_size(), st)
-    _check(rc, "spec_attention_cache4")
+        rest = (float(scale) if scale is not None else D ** -0.5, _heads(out, "out", q.shape),
+                lse.data_ptr() if lse is not None else None, ws.data_ptr(),
+                ws.numel() * ws.element_size(), st)
+        if window is None:
+            where = "spec_attention_cache4"
+            rc = L.spec_attention_cache4(cache, _heads(q, "q"), B, T, Hq, s, n, mp, ms, mr, *rest)
+        else:
+            where = "spec_attention_cache4_window"
+            rc = L.spec_attention_cache4_window(cache, _heads(q, "q"), B, T, Hq, s, n, mp, ms, mr, dp, ds,
+                                                int(window), int(sinks), *rest)
+    _check(rc, where)
     return (out, lse) if lse is not None else out
 
 
@@ -956,4 +1039,201 @@ def lmhead_fp8(hidden: torch.Tensor, weight: torch.Tensor, weight_scale: torch.T
                                weight_scale.data_ptr(), V, _logits(out, rows), ws.data_ptr(),
                                ws.numel() * ws.element_size(), st)
     _check(rc, "spec_lmhead_fp8")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The serving step around the cached pass (specverify_step.h): norms of queries
+# and keys with their rotation, attention behind shared prefixes, and pages.
+# They take and make tensors as the calls above do.
+
+
+def norm_rotate(q: torch.Tensor | None, k: torch.Tensor | None, start: torch.Tensor, *,
+                eps: float | None = None, q_weight: torch.Tensor | None = None,
+                k_weight: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None,
+                interleaved: bool = False, count: torch.Tensor | None = None,
+                depth: torch.Tensor | None = None, out=None, out_dtype: torch.dtype | None = None,
+                stream=None):
+    """Norms of queries and keys for each head and their rotation by position, in
+    one pass.  q [B][T][q_heads][D], k [B][T][heads][D] (float32 or bfloat16, D a
+    multiple of 16 up to 256; either may be None): with ``eps`` each head is
+    divided by sqrt(mean x^2 + eps) and multiplied by q_weight, k_weight [D] (None:
+    ones); with ``inv_freq`` float32 [n], n a multiple of 8, its first 2 n values
+    are turned in pairs (c, c + n), or (2 c, 2 c + 1) where ``interleaved``, by
+    (start[b] + i) * inv_freq[c], or start[b] + depth[b][i] with ``depth`` int32
+    [B|1][T] (tree_depths).  Returns (q, k) in out_dtype (default: the input's);
+    rows past count[b] are zero.  ``out`` = (q, k) takes the results instead and
+    keeps those rows; it may be the inputs themselves."""
+    B = T = D = index = dtype = None
+    heads = []
+    for t, what in ((q, "q"), (k, "k")):
+        if t is None:
+            heads.append(0)
+            continue
+        index = _device_tensor(t, what, _FLOATS if dtype is None else (dtype,), 4, index)
+        if dtype is not None and (t.shape[0], t.shape[1], t.shape[3]) != (B, T, D):
+            raise ValueError("q and k disagree on B, T or D")
+        B, T, h, D = t.shape
+        dtype = t.dtype
+        heads.append(h)
+        if h == 0:
+            raise ValueError("%s has no heads" % what)
+    if index is None:
+        raise ValueError("norm_rotate needs q or k")
+    if start is None:
+        raise ValueError("start is required")
+    s = _per_sequence(start, "start", B, index)
+    n = _per_sequence(count, "count", B, index)
+    dp, ds = _depths(depth, B, T, index)
+    rot = 0
+    if inv_freq is not None:
+        _device_tensor(inv_freq, "inv_freq", (torch.float32,), 1, index)
+        rot = 2 * inv_freq.shape[0]
+        if rot == 0 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float32 [rotated values / 2]")
+    if eps is None and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights need eps")
+    weights, w_dtype = [], None
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is None:
+            weights.append(None)
+            continue
+        _device_tensor(w, what, _FLOATS if w_dtype is None else (w_dtype,), 1, index)
+        if w.shape[0] != D or not w.is_contiguous():
+            raise ValueError("%s must be a contiguous [%d]" % (what, D))
+        w_dtype = w.dtype
+        weights.append(w.data_ptr())
+    st, ctx = _on(index, stream)
+    with ctx:
+        if out is None:
+            to = dtype if out_dtype is None else out_dtype
+            if to not in _FLOATS:
+                raise TypeError("out_dtype must be float32 or bfloat16, got %s" % to)
+            make = torch.empty if count is None else torch.zeros
+            out = [make(t.shape, dtype=to, device=t.device) if t is not None else None for t in (q, k)]
+        else:
+            to = None
+            for t, o, what in zip((q, k), out, ("out[0]", "out[1]")):
+                if t is not None:
+                    _device_tensor(o, what, _FLOATS if to is None else (to,), 4, index)
+                    to = o.dtype
+        none = spec_heads_t()
+        ins = [_heads(t, what) if t is not None else none for t, what in ((q, "q"), (k, "k"))]
+        outs = [_heads(o, what, t.shape) if t is not None else none
+                for t, o, what in ((q, out[0], "out[0]"), (k, out[1], "out[1]"))]
+        how = spec_rotate_t(D, rot, int(bool(interleaved)), int(eps is not None),
+                            float(eps) if eps is not None else 0.0,
+                            SPEC_DTYPE_BF16 if w_dtype is torch.bfloat16 else SPEC_DTYPE_F32,
+                            weights[0], weights[1],
+                            inv_freq.data_ptr() if inv_freq is not None else None, dp, ds)
+        rc = lib().spec_norm_rotate(ins[0], outs[0], heads[0], ins[1], outs[1], heads[1],
+                                    ctypes.byref(how), B, T, s, n, st)
+    _check(rc, "spec_norm_rotate")
+    return tuple(out)
+
+
+def attention_cache4_shared(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor,
+                            start: torch.Tensor, prefix_table: torch.Tensor,
+                            prefix_len: torch.Tensor, *, fan: int,
+                            count: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                            scale: float | None = None, return_lse: bool = False,
+                            out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None):
+    """attention_cache4 of branches behind shared prefixes: sequences fan g ..
+    fan g + fan - 1 see, before their own tokens (table, start, count, mask as
+    there), the prefix_len[g] tokens whose pages prefix_table [ceil(B / fan)][.]
+    names in the same pool.  A prefix is read once for all its branches.  A new
+    token's position in the text, for norm_rotate, is prefix_len + start + i."""
+    index = _device_tensor(q, "q", (torch.bfloat16,), 4)
+    B, T, Hq, D = q.shape
+    cache, _ = _cache4(pages, table, D, B, index)
+    if start is None or prefix_len is None:
+        raise ValueError("start and prefix_len are required")
+    if not 1 <= fan < 1 << 31:
+        raise ValueError("fan must be at least 1, got %s" % fan)
+    prefixes = (B + fan - 1) // fan
+    cols, stride = _table(prefix_table, "prefix_table", prefixes, index)
+    pl = _per_sequence(prefix_len, "prefix_len", prefixes, index)
+    s = _per_sequence(start, "start", B, index)
+    n = _per_sequence(count, "count", B, index)
+    mp, ms, mr = _mask_words(mask, B, T, index)
+    if lse is not None:
+        _out_tensor(lse, (B, T, Hq), torch.float32, q.device, "lse")
+    if out is not None:
+        _device_tensor(out, "out", (torch.bfloat16,), 4, index)
+    L = lib()
+    need = L.spec_attention_cache4_shared_workspace(B, T, Hq, cache.heads, D, fan)
+    if need == 0:
+        _check(SPEC_ERR_UNSUPPORTED if B and T and Hq and Hq % cache.heads == 0
+               else SPEC_ERR_INVALID_ARG, "spec_attention_cache4_shared_workspace")
+    st, ctx = _on(index, stream)
+    with ctx:
+        make = torch.empty if count is None else torch.zeros
+        if out is None:
+            out = make((B, T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        if return_lse and lse is None:
+            lse = make((B, T, Hq), dtype=torch.float32, device=q.device)
+        ws = _scratch(workspace, q.device, need)
+        rc = L.spec_attention_cache4_shared(
+            cache, prefix_table.data_ptr(), stride, cols, pl, fan, _heads(q, "q"), B, T, Hq, s, n,
+            mp, ms, mr, float(scale) if scale is not None else D ** -0.5,
+            _heads(out, "out", q.shape), lse.data_ptr() if lse is not None else None,
+            ws.data_ptr(), ws.numel() * ws.element_size(), st)
+    _check(rc, "spec_attention_cache4_shared")
+    return (out, lse) if lse is not None else out
+
+
+def cache4_reserve(table: torch.Tensor, held: torch.Tensor, need: torch.Tensor,
+                   free: torch.Tensor, free_count: torch.Tensor, *, stream=None) -> None:
+    """Brings every sequence to the pages that need[b] tokens take, in place:
+    table [B][P] holds its held[b] pages first, ``free`` [capacity] the
+    free_count[0] pages that are nobody's (all int32).  Pages too many go back on
+    the end of ``free``, their entries become -1; missing ones are taken from its
+    end, for one sequence after the other until one finds too few: it and all
+    after it that miss pages keep what they hold (held[b] tells)."""
+    index = _device_tensor(table, "table", (torch.int32,), 2)
+    cols, stride = _table(table, "table", table.shape[0], index)
+    B = table.shape[0]
+    if held is None or need is None:
+        raise ValueError("held and need are required")
+    h = _per_sequence(held, "held", B, index)
+    w = _per_sequence(need, "need", B, index)
+    _device_tensor(free, "free", (torch.int32,), 1, index)
+    if not free.is_contiguous():
+        raise ValueError("free must be contiguous")
+    c = _per_sequence(free_count, "free_count", 1, index)
+    if c is None:
+        raise ValueError("free_count is required")
+    st, ctx = _on(index, stream)
+    with ctx:
+        rc = lib().spec_cache4_reserve(table.data_ptr(), stride, cols, h, w, B, free.data_ptr(),
+                                       free.shape[0], c, st)
+    _check(rc, "spec_cache4_reserve")
+
+
+def cache4_slots(table: torch.Tensor, start: torch.Tensor, T: int, n_pages: int, *,
+                 count: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """Where new tokens stand in a pool of n_pages pages: int64 [B][T], 64 times
+    the page of position start[b] + i plus its place in it, -1 where there is no
+    new token (i >= count[b]) or no page.  For a caller's own caches that are laid
+    out by the same tables."""
+    index = _device_tensor(table, "table", (torch.int32,), 2)
+    B, T = table.shape[0], int(T)
+    cols, stride = _table(table, "table", B, index)
+    if start is None:
+        raise ValueError("start is required")
+    s = _per_sequence(start, "start", B, index)
+    n = _per_sequence(count, "count", B, index)
+    if not 1 <= n_pages < 1 << 31:
+        raise ValueError("n_pages must be at least 1, got %s" % n_pages)
+    st, ctx = _on(index, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty((B, T), dtype=torch.int64, device=table.device)
+        else:
+            _out_tensor(out, (B, T), torch.int64, table.device, "out")
+        rc = lib().spec_cache4_slots(table.data_ptr(), stride, cols, n_pages, B, T, s, n,
+                                     out.data_ptr(), st)
+    _check(rc, "spec_cache4_slots")
     return out

@@ -3,6 +3,8 @@
 // format of a page's record is stated in include/specverify_lowbit.h.
 #pragma once
 
+#include <type_traits>
+
 #include "sv_device.hpp"
 
 namespace sv {
@@ -332,22 +334,73 @@ struct C4AttnArgs {
   float* parts;           // [2 x workgroups] records of a workgroup's first and last cut segment
 };
 
+// A call whose cached tokens are seen through a window, but for a few first ones
+// (sinks).  Of a sequence's pages those that no new token sees are left out: the
+// pages that are read are counted through, and from `keep` on they stand `skip`
+// further back in the table.
+struct C4WindowArgs : C4AttnArgs {
+  int32_t window, sinks;
+  const int32_t* depth;  // or null: a new token's index
+  int64_t depth_seq;
+};
+
+// Branches that share a prefix: `fan` sequences in a row have one, whose pages
+// `cache.table` names and whose length stands in `start`; B counts prefixes,
+// and the rows of one are those of all its branches, (branch, token, head).  Each row
+// of the call has a record: O [D], and maximum, sum and rounded sum.
+struct C4PrefixArgs : C4AttnArgs {
+  int32_t fan, seqs;  // branches of a prefix, sequences of the call
+  int32_t dim;        // D
+  float* rec;         // [seqs][T][q_heads][D]
+  float* stat;        // [seqs][T][q_heads][4]
+};
+
+// A branch's own tokens; its rows end by taking the prefix's records in.
+struct C4OwnArgs : C4AttnArgs {
+  int32_t dim;  // D
+  const float* rec;
+  const float* stat;
+};
+
+template <typename Args> constexpr bool kC4Window = std::is_same<Args, C4WindowArgs>::value;
+template <typename Args> constexpr bool kC4Prefix = std::is_same<Args, C4PrefixArgs>::value;
+template <typename Args> constexpr bool kC4Own = std::is_same<Args, C4OwnArgs>::value;
+
 struct C4Cut {
   int32_t b, hr, nnew;  // its sequence, head and block of rows, and the sequence's new tokens
   int32_t parts, slot;  // workgroups that hold it, from this one on (0: none); its record in this one
   int32_t pad[3];
 };
 
+// Of a sequence with s cached and n > 0 new tokens the pages that are read
+// through a window: the first `keep`, and those `skip` behind them.
+struct C4Gap {
+  int32_t keep, skip;
+};
+__host__ __device__ __forceinline__ C4Gap c4_gap(int32_t window, int32_t sinks, int32_t s, int32_t n) {
+  // the first new token's window reaches furthest back: depths are not negative
+  const int32_t low = s >= window ? (s - window + 1) / kC4Page : 0;
+  const int32_t head = (int32_t)(((int64_t)(sinks < s + n ? sinks : s + n) + kC4Page - 1) / kC4Page);
+  const int32_t keep = head < low ? head : low;
+  return {keep, low - keep};
+}
+
 // Pages of sequence b that its new tokens attend to; 0 when it has no rows.
 // `bad`: ill-formed (one page then stands for the sequence, so that its rows
-// are visited).
-template <bool UNIFORM>
-__device__ __forceinline__ int32_t c4_pages(const C4AttnArgs& A, int64_t b, bool& bad) {
+// are visited).  A prefix without a token is visited for its rows' records.
+template <bool UNIFORM, typename Args>
+__device__ __forceinline__ int32_t c4_pages(const Args& A, int64_t b, bool& bad) {
   const int32_t s = UNIFORM ? c4_scalar(A.start + b) : A.start[b];
+  if constexpr (kC4Prefix<Args>) {
+    bad = !A.cache.fits(s, 0, 0);
+    return bad || s == 0 ? 1 : (s - 1) / kC4Page + 1;
+  }
   const int32_t n = !A.count ? A.T : UNIFORM ? c4_scalar(A.count + b) : A.count[b];
   bad = !A.cache.fits(s, n, A.T);
   if (bad) return 1;
-  return n == 0 ? 0 : (s + n + kC4Page - 1) / kC4Page;
+  const int32_t all = n == 0 ? 0 : (s + n + kC4Page - 1) / kC4Page;
+  if constexpr (kC4Window<Args>) return n == 0 ? 0 : all - c4_gap(A.window, A.sinks, s, n).skip;
+  return all;
 }
 
 // Beginning and ending a segment (its rows, the first loads, joining the four
@@ -395,7 +448,8 @@ __device__ __forceinline__ int64_t c4_lane(int64_t x, int l) {
 
 // Weight of all sequences' segments (of one head and row block): a lane sums a
 // run of `per` sequences; `before`: the weight before its run.
-__device__ __forceinline__ int64_t c4_plan(const C4AttnArgs& A, int lane, int32_t per, int64_t& before) {
+template <typename Args>
+__device__ __forceinline__ int64_t c4_plan(const Args& A, int lane, int32_t per, int64_t& before) {
   int64_t sum = 0;
   for (int32_t j = 0; j < per; ++j) {
     const int64_t b = (int64_t)lane * per + j;
@@ -408,7 +462,8 @@ __device__ __forceinline__ int64_t c4_plan(const C4AttnArgs& A, int lane, int32_
 }
 // The sequence in which weight x (below the total) lies, and the weight before
 // it: the lane's run, then 64 sequences of it at a time.
-__device__ __forceinline__ int64_t c4_find(const C4AttnArgs& A, int lane, int32_t per, int64_t before,
+template <typename Args>
+__device__ __forceinline__ int64_t c4_find(const Args& A, int lane, int32_t per, int64_t before,
                                            int64_t x, int64_t& at) {
   const int run = 63 - __builtin_clzll(__ballot(before <= x));
   at = c4_lane(before, run);
@@ -471,6 +526,11 @@ constexpr float kC4Low = -3.402823466e38f;  // a maximum before any score: no fi
 constexpr float kC4Raise = 8.0f;     // a score passes the maximum by 2^8 before it is raised
 constexpr float kC4Exact = 0x1p24f;  // up to here half a step of a maximum is 1/2 at most
 
+// The lowest n bits, and those from n on.
+__device__ __forceinline__ uint32_t c4_below(int64_t n) {
+  return n <= 0 ? 0 : n >= 32 ? ~0u : (1u << n) - 1u;
+}
+
 // What a row's new token sees of the 32 positions from `base` on (relative to
 // start): bit x for position base + x.
 __device__ __forceinline__ uint32_t c4_sees(const C4AttnArgs& A, int64_t b, int32_t i, int32_t n,
@@ -491,6 +551,20 @@ __device__ __forceinline__ uint32_t c4_sees(const C4AttnArgs& A, int64_t b, int3
   const int64_t k = base >> 5;            // floor: base may be negative
   const int sh = (int)(base & 31);
   return sh == 0 ? word(k) : (word(k) >> sh) | (word(k + 1) << (32 - sh));
+}
+
+// Of these, what its window and the sinks leave; low: the first position that
+// its window reaches, relative to start.  Mask words alone say what new tokens
+// see of each other.
+__device__ __forceinline__ uint32_t c4_in_window(const C4WindowArgs& A, int32_t s0, int64_t low, int64_t base) {
+  const uint32_t kept = ~c4_below(low - base) | c4_below((int64_t)A.sinks - s0 - base);
+  return A.mask ? kept | ~c4_below(-base) : kept;
+}
+// How far row token i stands behind start.
+__device__ __forceinline__ int32_t c4_depth(const C4WindowArgs& A, int64_t b, int32_t i) {
+  if (!A.depth || i >= A.T) return i;
+  const int32_t d = A.depth[b * A.depth_seq + i];
+  return d < 0 ? 0 : d >= A.T ? A.T - 1 : d;
 }
 
 typedef uint32_t C4U2 __attribute__((ext_vector_type(2)));
@@ -764,6 +838,41 @@ __device__ __forceinline__ void c4_unit(const uint8_t* from, int half, Q rows_of
   }
 }
 
+// The branch, token and query head of row r of kv head h; false if there is no
+// such row, or its token is none of the call's.
+template <typename Args>
+__device__ __forceinline__ bool c4_row(const Args& A, int32_t h, int32_t r, int32_t nnew, int64_t& b, int32_t& i,
+                                       int32_t& head) {
+  if constexpr (kC4Prefix<Args>) {
+    const int32_t of = r / (A.T * A.G), rest = r - of * (A.T * A.G);
+    b = b * A.fan + of;
+    i = rest / A.G;
+    head = h * A.G + (rest - i * A.G);
+    return of < A.fan && b < A.seqs && (!A.count || i < A.count[b]);
+  } else {
+    i = r / A.G;
+    head = h * A.G + (r - i * A.G);
+    return r < A.T * A.G && i < nnew;
+  }
+}
+// Rows of a kv head.
+template <typename Args>
+__device__ __forceinline__ int32_t c4_rows(const Args& A) {
+  if constexpr (kC4Prefix<Args>) return A.fan * A.T * A.G;
+  return A.T * A.G;
+}
+
+// A prefix's row: kept as it is.
+template <int N>
+__device__ __forceinline__ void c4_finish(const C4PrefixArgs& A, int64_t b, int32_t i, int32_t head, int d0,
+                                          const float* x, float m, float l, float n) {
+  const int64_t at = (b * A.T + i) * ((int64_t)A.G * A.cache.heads) + head;
+  const int D = A.dim;
+#pragma unroll
+  for (int e = 0; e < N; ++e) A.rec[at * D + d0 + e] = x[e];
+  if (d0 == 0) *reinterpret_cast<float4*>(A.stat + at * 4) = make_float4(m, l, n, 0.f);
+}
+
 // Writes N values of a finished row, normalised, or NaN; with the first ones
 // the row's lse.
 template <int N>
@@ -780,6 +889,20 @@ __device__ __forceinline__ void c4_finish(const C4AttnArgs& A, int64_t b, int32_
     const int64_t at = (b * A.T + i) * ((int64_t)A.G * A.cache.heads) + head;
     A.lse[at] = l == 0.f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * kLn2;
   }
+}
+
+// A branch's row joined with its prefix's.
+template <int N>
+__device__ __forceinline__ void c4_finish(const C4OwnArgs& A, int64_t b, int32_t i, int32_t head, int d0,
+                                          const float* x, float m, float l, float n) {
+  const int64_t at = (b * A.T + i) * ((int64_t)A.G * A.cache.heads) + head;
+  const float4 s = *reinterpret_cast<const float4*>(A.stat + at * 4);
+  const float top = fmaxf(m, s.x);
+  const float f = __builtin_amdgcn_exp2f(m - top), g = __builtin_amdgcn_exp2f(s.x - top);
+  float y[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = x[e] * f + A.rec[at * A.dim + d0 + e] * g;
+  c4_finish<N>(static_cast<const C4AttnArgs&>(A), b, i, head, d0, y, top, l * f + s.y * g, n * f + s.z * g);
 }
 
 // How the cached pages come: each wave fills two LDS buffers of its own with
@@ -868,8 +991,8 @@ __device__ __forceinline__ void c4_wait() {
 #endif
 }
 
-template <int D, int RT>
-__global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cache4(C4AttnArgs A) {
+template <int D, int RT, typename Args = C4AttnArgs>
+__global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cache4(Args A) {
   using Sh = C4Shape<D, RT>;
   constexpr int kRows = RT * 16, N = Sh::kPairs;
   // Two arrays, each named where it is used, so that the compiler does not wait
@@ -907,7 +1030,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   int32_t pages = c4_pages<true>(A, b, bad);
   int32_t hr = (int32_t)c4_div(lo - seq_at * HR, c4_weight(pages));
   int64_t seg = seq_at * HR + hr * c4_weight(pages);  // where it begins
-  const int32_t R = A.T * A.G;
+  const int32_t R = c4_rows(A);
   for (; seg < hi; seg += c4_weight(pages), ++hr) {
     if (hr == HR) {  // the next sequence with pages (seg is its begin)
       do pages = c4_pages<true>(A, ++b, bad);
@@ -919,7 +1042,12 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     if (p0 == p1) continue;  // its pages are another workgroup's
     const int32_t h = hr / A.row_blocks, r0 = hr % A.row_blocks * kRows;
     const int32_t s0 = c4_scalar(A.start + b);
-    const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
+    // a prefix has no new tokens of its own
+    const int32_t nnew = kC4Prefix<Args> ? 0 : bad || !A.count ? A.T : c4_scalar(A.count + b);
+    C4Gap gap{0, 0};
+    if constexpr (kC4Window<Args>)
+      if (!bad) gap = c4_gap(A.window, A.sinks, s0, nnew);
+    auto place = [&](int32_t p) { return kC4Window<Args> && p >= gap.keep ? p + gap.skip : p; };
     if (p0 == 0 && p1 < pages) {
       cut_b = (int32_t)b, cut_hr = hr, cut_new = nnew, cut_slot = seg > lo ? 1 : 0;
       cut_parts = (int32_t)c4_div(seg + kC4SegCost + pages - 1, share) - blockIdx.x + 1;
@@ -930,17 +1058,20 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     // stands for page 0 and marks the rows.
     bool faulty = bad;
     const int half = w & 1;
-    const int32_t end = bad ? p0 : p1, pw = p0 + (w >> 1);  // this wave's pages: pw, pw + 2, ..
+    const int32_t end = bad || (kC4Prefix<Args> && s0 == 0) ? p0 : p1;
+    const int32_t pw = p0 + (w >> 1);  // this wave's pages: pw, pw + 2, ..
     int32_t nu = end > pw ? (end - pw + 1) / 2 : 0;
     // the last page may hold no token in its second half
-    if (nu && (pw + 2 * (nu - 1)) * (int64_t)kC4Page + 32 * half >= (int64_t)s0 + nnew) --nu;
-    auto page_of = [&](int32_t u) { return u < nu ? c4_scalar(A.cache.table + b * A.cache.table_stride + pw + 2 * u) : 0; };
+    if (nu && place(pw + 2 * (nu - 1)) * (int64_t)kC4Page + 32 * half >= (int64_t)s0 + nnew) --nu;
+    auto page_of = [&](int32_t u) {
+      return u < nu ? c4_scalar(A.cache.table + b * A.cache.table_stride + place(pw + 2 * u)) : 0;
+    };
     auto fetch = [&](int32_t page, uint8_t* buf, int k) {
       if ((uint32_t)page >= (uint32_t)A.cache.n_pages) {
         faulty = true;
         page = 0;
       }
-      c4_fetch<D>(A.cache.record<D>(page, h), half, lane, buf + w * Sh::kBuf + k * Sh::kUnit);
+      c4_fetch<D>(A.cache.template record<D>(page, h), half, lane, buf + w * Sh::kBuf + k * Sh::kUnit);
     };
     int32_t first[2 * N];  // all on their way before the first is needed
 #pragma unroll
@@ -950,16 +1081,20 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     constexpr int kQ = Sh::kQRegs ? D / 32 : D / 128;  // chunks a wave loads of a tile
     uint4 qx[RT][kQ];
     int32_t tok[RT];  // this lane's rows' tokens; T past the last row
+    int64_t low[RT];  // the first position that their windows reach, relative to start
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int32_t r = r0 + 16 * rt + n16;
-      const int32_t i = r / A.G, g = r - i * A.G;
+      int64_t bb = b;
+      int32_t i, head;
+      const bool live = c4_row(A, h, r, nnew, bb, i, head);
       tok[rt] = r < R ? i : A.T;
-      const uint16_t* qp = A.q + b * A.q_seq + i * A.q_pos + ((int64_t)h * A.G + g) * A.q_head;
+      if constexpr (kC4Window<Args>) low[rt] = (int64_t)c4_depth(A, b, tok[rt]) - A.window + 1;
+      const uint16_t* qp = A.q + bb * A.q_seq + i * A.q_pos + (int64_t)head * A.q_head;
 #pragma unroll
       for (int j = 0; j < kQ; ++j) {
         qx[rt][j] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < R && i < nnew) qx[rt][j] = load16(qp + q * (D / 4) + 8 * (Sh::kQRegs ? j : 4 * j + w));
+        if (live) qx[rt][j] = load16(qp + q * (D / 4) + 8 * (Sh::kQRegs ? j : 4 * j + w));
       }
     }
     // Waited for here, by an instruction that the compiler knows: at their first use,
@@ -1010,12 +1145,18 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
         else if (N == 2 && later == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Sh::kLoads) : "memory");
         else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         // the first of its positions relative to the new tokens'
-        const int64_t base = (int64_t)(pw + 2 * u) * kC4Page + 32 * half - s0;
-        const bool masked = base + 32 > 0;
+        const int64_t base = (int64_t)place(pw + 2 * u) * kC4Page + 32 * half - s0;
+        bool masked = base + 32 > 0;
+        if constexpr (kC4Window<Args>)  // or the last token's window ends behind, and these are not all sinks
+          masked |= base <= (int64_t)A.T - 1 - A.window && base + s0 + 32 > A.sinks;
         uint32_t sees[RT] = {}, valid = 0;
         if (masked) {
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) sees[rt] = c4_sees(A, b, tok[rt], nnew, base);
+          for (int rt = 0; rt < RT; ++rt) {
+            if constexpr (kC4Prefix<Args>) sees[rt] = c4_below(-base);
+            else sees[rt] = c4_sees(A, b, tok[rt], nnew, base);
+            if constexpr (kC4Window<Args>) sees[rt] &= c4_in_window(A, s0, low[rt], base);
+          }
           const int64_t have = nnew - base;
           valid = have >= 32 ? ~0u : (1u << have) - 1u;
         }
@@ -1063,8 +1204,9 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
         l += ls[x][row] * g;
         n += ns[x][row] * g;
       }
-      const int32_t r = r0 + row, i = r / A.G, head = h * A.G + (r - i * A.G);
-      const bool live = r < R && i < nnew;
+      int64_t bb = b;
+      int32_t i, head;
+      const bool live = c4_row(A, h, r0 + row, nnew, bb, i, head);
 #pragma unroll
       for (int x = 0; x < D / kCols; ++x) {
         // the buffers in turn: one barrier a time
@@ -1085,7 +1227,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
           for (int e = 0; e < kRun; ++e) v[e] += oacc[(ww * 16 + rr) * kPad + grp * kRun + e];
         if (!live) continue;
         if (whole) {
-          c4_finish<kRun>(A, b, i, head, d0, v, top, l, n);
+          c4_finish<kRun>(A, bb, i, head, d0, v, top, l, n);
         } else {
 #pragma unroll
           for (int e = 0; e < kRun; ++e) part[row * D + d0 + e] = v[e];
@@ -1141,8 +1283,8 @@ __device__ __forceinline__ void c4_gather(const float* first, const float* rest,
 // Joins the cut segments of calls with many of them, of few records each: four
 // rows a workgroup, a wave each, for the segment that workgroup blockIdx.x of
 // the attention began, if others end it.
-template <int D, int RT>
-__global__ __launch_bounds__(256) void k_attention_cache4_join(C4AttnArgs A) {
+template <int D, int RT, typename Args = C4AttnArgs>
+__global__ __launch_bounds__(256) void k_attention_cache4_join(Args A) {
   constexpr int kRows = RT * 16, E = D / 64;  // E columns a lane
   constexpr int64_t kFloats = C4Rec<D, RT>::kFloats;
   const auto* cp = A.cuts + blockIdx.x;
@@ -1152,26 +1294,27 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join(C4AttnArgs A) {
   const int32_t nnew = c4_scalar(&cp->nnew);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t row = blockIdx.y * 4 + w, h = hr / A.row_blocks;
-  const int32_t r = hr % A.row_blocks * kRows + row, i = r / A.G;
-  if (r >= A.T * A.G || i >= nnew) return;
+  int64_t bb = b;
+  int32_t i, head;
+  if (!c4_row(A, h, hr % A.row_blocks * kRows + row, nnew, bb, i, head)) return;
   const float* rest = A.parts + (int64_t)blockIdx.x * 2 * kFloats;
   float m, l, n, v[E];
   c4_gather<D>(rest + slot * kFloats, rest, 2 * kFloats, kRows, row, 0, parts, lane, m, l, n, v);
-  c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l, n);
+  c4_finish<E>(A, bb, i, head, lane * E, v, m, l, n);
 }
 
 // Joins those of calls with few segments of many records: a row a workgroup, a
 // quarter of the records a wave.  Where the records stand follows from the
 // lengths alone, as in the attention.
-template <int D, int RT>
-__global__ __launch_bounds__(256) void k_attention_cache4_join_long(C4AttnArgs A) {
+template <int D, int RT, typename Args = C4AttnArgs>
+__global__ __launch_bounds__(256) void k_attention_cache4_join_long(Args A) {
   constexpr int kRows = RT * 16, E = D / 64;
   constexpr int64_t kFloats = C4Rec<D, RT>::kFloats;
   __shared__ float vs[4][D], ms[4], ls[4], ns[4];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t per = (A.B + 63) / 64, HR = A.cache.heads * A.row_blocks;
   const int32_t b = blockIdx.x / HR, hr = blockIdx.x % HR, row = blockIdx.y;
-  const int32_t h = hr / A.row_blocks, r = hr % A.row_blocks * kRows + row, i = r / A.G;
+  const int32_t h = hr / A.row_blocks;
   int64_t before;
   const int64_t share = c4_share<C4Shape<D, RT>::kGrid>(c4_plan(A, lane, per, before) * HR);
   bool bad;
@@ -1179,7 +1322,9 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join_long(C4AttnArgs A
   for (int32_t x = b / per * per; x < b; ++x) at += c4_weight(c4_pages<true>(A, x, bad));
   const int32_t pages = c4_pages<true>(A, b, bad);
   const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
-  if (pages == 0 || r >= A.T * A.G || i >= nnew) return;
+  int64_t bb = b;
+  int32_t i, head;
+  if (pages == 0 || !c4_row(A, h, hr % A.row_blocks * kRows + row, nnew, bb, i, head)) return;
   const int64_t seg = at * HR + hr * c4_weight(pages);
   // the workgroups that hold its first and last page
   const int32_t w0 = (int32_t)c4_div(seg + kC4SegCost, share);
@@ -1211,7 +1356,7 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join_long(C4AttnArgs A
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] += vs[x][lane * E + e] * f;
   }
-  c4_finish<E>(A, b, i, h * A.G + (r - i * A.G), lane * E, v, m, l, n);
+  c4_finish<E>(A, bb, i, head, lane * E, v, m, l, n);
 }
 
 }  // namespace sv

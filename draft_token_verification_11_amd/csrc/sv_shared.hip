@@ -1,0 +1,100 @@
+// sv_shared.hip -- the C ABI of attention behind shared prefixes: argument
+// validation and kernel launches for gfx950.  See include/specverify_step.h for
+// the contract.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "specverify_step.h"
+#include "sv_cache4_host.hpp"
+
+namespace {
+
+constexpr int64_t kMaxSharedRows = 1 << 30;  // of a prefix, over all heads
+
+bool shared_sizes_ok(int32_t B, int32_t T, int32_t q_heads, int32_t fan) {
+  return fan >= 1 && int64_t(std::min(fan, B)) * T <= kMaxSharedRows / q_heads;
+}
+
+// A call's workspace: the rows' records, and one attention's after the other.
+struct SharedSpace {
+  size_t rec, stat, scratch;
+  size_t bytes() const { return rec + stat + scratch; }
+};
+SharedSpace shared_space(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t fan) {
+  const size_t rows = size_t(B) * size_t(T) * size_t(q_heads);
+  int tiles;
+  int64_t blocks;
+  row_blocks(int64_t(std::min(fan, B)) * T * (q_heads / kv_heads), d, &tiles, &blocks);
+  return {align256(rows * size_t(d) * 4), align256(rows * 16),
+          std::max(attention_workspace(T, q_heads, kv_heads, d), shape_workspace(d, tiles))};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_attention_cache4_shared_workspace(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
+                                              int32_t head_dim, int32_t fan) {
+  if (check_attention_sizes(B, T, q_heads, heads, head_dim) != SPEC_OK || !shared_sizes_ok(B, T, q_heads, fan)) return 0;
+  return shared_space(B, T, q_heads, heads, head_dim, fan).bytes();
+}
+
+int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_table,
+                                 int64_t prefix_stride, int32_t prefix_cols,
+                                 const int32_t* prefix_len, int32_t fan, spec_heads_t q, int32_t B,
+                                 int32_t T, int32_t q_heads, const int32_t* start,
+                                 const int32_t* count, const uint32_t* mask,
+                                 int64_t mask_seq_stride, int64_t mask_pos_stride, float scale,
+                                 spec_heads_t out, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  sv::C4AttnArgs base;
+  int rc, tiles;
+  if (fan < 1) return SPEC_ERR_INVALID_ARG;
+  if ((rc = attention_args(cache, q, B, T, q_heads, start, count, mask, mask_seq_stride, mask_pos_stride, scale, out,
+                           lse, workspace, workspace_bytes, &base, &tiles)) != SPEC_OK)
+    return rc;
+  if (!shared_sizes_ok(B, T, q_heads, fan)) return SPEC_ERR_UNSUPPORTED;
+  spec_cache4_t prefix = cache;
+  prefix.table = prefix_table;
+  prefix.table_stride = prefix_stride;
+  prefix.table_cols = prefix_cols;
+  if ((rc = check_cache(prefix)) != SPEC_OK) return rc;
+  if (!prefix_len || !aligned(prefix_len, 4)) return SPEC_ERR_INVALID_ARG;
+  const int32_t d = cache.head_dim, each = std::min(fan, B), prefixes = (B + each - 1) / each;
+  int prefix_tiles;
+  int64_t blocks;
+  row_blocks(int64_t(each) * T * (q_heads / cache.heads), d, &prefix_tiles, &blocks);
+  if (prefixes * (int64_t(prefix_cols) + sv::kC4SegCost) * cache.heads >= (int64_t(1) << 40) / blocks)
+    return SPEC_ERR_UNSUPPORTED;
+  const SharedSpace space = shared_space(B, T, q_heads, cache.heads, d, fan);
+  if (workspace_bytes < space.bytes()) return SPEC_ERR_WORKSPACE;
+  auto* const rec = static_cast<float*>(workspace);
+  auto* const stat = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + space.rec);
+  void* const scratch = static_cast<uint8_t*>(workspace) + space.rec + space.stat;
+
+  sv::C4PrefixArgs P;
+  static_cast<sv::C4AttnArgs&>(P) = base;
+  P.cache = view(prefix);
+  P.start = prefix_len;
+  P.B = prefixes;
+  P.row_blocks = int32_t(blocks);
+  P.split = prefix_cols > kAttnWhole;
+  P.fan = each;
+  P.seqs = B;
+  P.dim = d;
+  P.rec = rec;
+  P.stat = stat;
+  sv::C4OwnArgs O;
+  static_cast<sv::C4AttnArgs&>(O) = base;
+  O.dim = d;
+  O.rec = rec;
+  O.stat = stat;
+  auto st = static_cast<hipStream_t>(stream);
+  (void)hipGetLastError();
+  with_shape(d, prefix_tiles, [&](auto D, auto RT) { launch_attention<D, RT>(P, scratch, st); });
+  with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(O, scratch, st); });
+  return finish_launch();
+}
+
+}  // extern "C"

@@ -1,0 +1,213 @@
+"""Attention of branches behind shared prefixes against the formula in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+import draft_token_verification_11_amd as sv
+from tests import lowbit_plain as low
+from tests import step_plain as plain
+from tests.test_gpu_attention_cache4 import _i32
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _case(seed, B, fan, T, Hq, H, D, start, prefix, slack=0):
+    """q, a pool of random values, the branches' tables and their prefixes'."""
+    rs = np.random.default_rng([seed, B, T, Hq, D])
+    P = max(1, -(-(max(start) + T) // 64)) + slack
+    PP = max(1, -(-max(prefix) // 64)) + slack
+    n = B * P + len(prefix) * PP + 2
+    order = rs.permutation(n).astype(np.int32)
+    table, ptable = order[: B * P].reshape(B, P), order[B * P: B * P + len(prefix) * PP].reshape(-1, PP)
+    pages = sv.cache4_alloc(n, H, D, DEV)
+    k, v = (torch.tensor(rs.normal(0, 1, (1, n * 64, H, D)), dtype=torch.float32, device=DEV) for _ in range(2))
+    sv.cache4_write(pages, _i32([list(range(n))]), _i32([0]), k, v)
+    q = torch.tensor(rs.normal(0, 1, (B, T, Hq, D)), dtype=torch.float32).bfloat16().to(DEV)
+    return q, pages, table.copy(), ptable.copy()
+
+
+def _run(q, pages, table, start, ptable, prefix, fan, count=None, **kw):
+    B, T, Hq, D = q.shape
+    out = torch.full((B, T, Hq, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((B, T, Hq), 7.0, device=DEV)
+    sv.attention_cache4_shared(q, pages, _i32(table), _i32(start), _i32(ptable), _i32(prefix), fan=fan,
+                               count=None if count is None else _i32(count), out=out, lse=lse, **kw)
+    return out, lse
+
+
+def _check(q, pages, table, start, ptable, prefix, fan, got, count=None, sees=None, rows=None):
+    out, lse = (x.double().cpu().numpy() for x in got)
+    B, T, Hq, D = q.shape
+    H = pages.shape[1]
+    a, pool = q.double().cpu().numpy(), pages.cpu().numpy()
+    for g in range(len(prefix)):
+        p_ok = 0 <= prefix[g] <= 64 * ptable.shape[1]
+        pk, pv, good = plain.held(pool, ptable[g], prefix[g] if p_ok else 0, D)
+        for b in range(g * fan, min(B, g * fan + fan)):
+            n = T if count is None else count[b]
+            if not low.fits(start[b], n, T, table.shape[1]):
+                assert np.isnan(out[b]).all() and np.isnan(lse[b]).all()
+                continue
+            assert (out[b, n:] == 7).all() and (lse[b, n:] == 7).all()
+            k, v, own = plain.held(pool, table[b], start[b] + n, D)
+            if not (p_ok and good and own):
+                assert np.isnan(out[b, :n]).all() and np.isnan(lse[b, :n]).all()
+                continue
+            see = plain.window_sees(start[b], n, T, sees or (lambda i, j: j <= i), None, True, 1 << 40, 0)
+            see = np.concatenate([np.ones((n, len(pk)), bool), see], 1)
+            k, v = np.concatenate([pk, k]), np.concatenate([pv, v])
+            for i in range(n):
+                for h in range(Hq):
+                    if rows is not None and not rows(b, i, h):
+                        continue
+                    kv = h // (Hq // H)
+                    want = plain.attend(a[b, i, h], k[:, kv], v[:, kv], see[i], D ** -0.5, 2.0 ** -20)
+                    assert np.isnan(want[1]) == np.isnan(lse[b, i, h])
+                    if np.isnan(want[1]):
+                        assert np.isnan(out[b, i, h]).all()
+                        continue
+                    off = np.abs(out[b, i, h] - want[0])
+                    assert (off <= want[2]).all(), (b, i, h, (off / want[2]).max())
+                    assert lse[b, i, h] == want[1] or abs(lse[b, i, h] - want[1]) <= want[3], (b, i, h)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,fan,T,Hq,H,start,prefix", [
+    (1, 1, 1, 1, 1, [0], [1]),
+    (1, 4, 1, 4, 2, [3], [0]),                             # fewer branches than fan; an empty prefix
+    (4, 4, 1, 8, 2, [0, 1, 63, 64], [777]),
+    (5, 2, 3, 7, 1, [0, 5, 130, 64, 9], [63, 64, 65]),     # a last group of one
+    (6, 3, 5, 8, 2, [0] * 6, [0, 128]),                    # 60 rows
+    (9, 9, 9, 8, 2, [7, 0, 1, 2, 3, 64, 65, 66, 300], [350]),  # 324 rows
+    (33, 16, 2, 4, 4, list(range(33)), [31, 95, 33]),
+])
+def test_branches(D, B, fan, T, Hq, H, start, prefix):
+    q, pages, table, ptable = _case(1, B, fan, T, Hq, H, D, start, prefix)
+    _check(q, pages, table, start, ptable, prefix, fan, _run(q, pages, table, start, ptable, prefix, fan))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_counts_and_wide_tables(D):
+    """Fewer new tokens than columns, none at all, tables wide enough for pages to be cut."""
+    B, fan, T = 7, 3, 6
+    start, count, prefix = [0, 70, 3, 1, 0, 200, 5], [6, 0, 1, 3, 0, 2, 6], [1000, 65, 300]
+    q, pages, table, ptable = _case(2, B, fan, T, 8, 2, D, start, prefix, slack=21)
+    _check(q, pages, table, start, ptable, prefix, fan, _run(q, pages, table, start, ptable, prefix, fan, count), count)
+
+
+@pytest.mark.parametrize("T", [5, 21, 40])
+def test_trees(T):
+    rs = np.random.default_rng(T)
+    par = [-1] + [int(rs.integers(0, i)) for i in range(1, T)]
+    see = np.zeros((T, T), bool)
+    for i in range(T):
+        see[i] = see[par[i]] if i else see[i]
+        see[i, i] = True
+    start, prefix = [0, 30, 64, 2, 0], [100, 0, 190]
+    q, pages, table, ptable = _case(3, 5, 2, T, 4, 1, 64, start, prefix)
+    got = _run(q, pages, table, start, ptable, prefix, 2, mask=sv.tree_mask(par).to(DEV))
+    _check(q, pages, table, start, ptable, prefix, 2, got, sees=lambda i, j: see[i, j])
+
+
+def test_rows_that_see_nothing_of_their_own():
+    T, start, prefix = 3, [0, 0, 0, 0], [70, 0]
+    q, pages, table, ptable = _case(4, 4, 2, T, 2, 1, 128, start, prefix)
+    none = torch.zeros(1, T, 1, dtype=torch.int32, device=DEV)
+    got = _run(q, pages, table, start, ptable, prefix, 2, mask=none)
+    _check(q, pages, table, start, ptable, prefix, 2, got, sees=lambda i, j: False)
+    assert (got[0][2:] == 0).all() and (got[1][2:] == -float("inf")).all()
+
+
+def test_bad_prefixes_sequences_and_pages():
+    B, fan, T = 10, 2, 2
+    start, count, prefix = [0, 3, 0, 0, 5, -1, 9, 1, 0, 0], [2, 2, 2, 2, 2, 2, 3, 2, 2, 2], [100, -1, 60, 9, 1 << 20]
+    q, pages, table, ptable = _case(5, B, fan, T, 2, 1, 64, [70] * B, [130] * 5)
+    ptable[0, 2] = -7   # behind the prefix's end: not looked at
+    ptable[2, 0] = 1 << 28
+    table[7, 0] = -1
+    got = _run(q, pages, table, start, ptable, prefix, fan, count)
+    _check(q, pages, table, start, ptable, prefix, fan, got, count)
+    nan = torch.isnan(got[0]).flatten(1).any(1).tolist()
+    assert nan == [False, False, True, True, True, True, True, True, True, True]
+
+
+def test_noise_behind_a_prefix_and_nan_in_it():
+    D, T, fan = 128, 2, 3
+    start, prefix = [0] * 6, [70, 70]
+    q, pages, table, ptable = _case(6, 6, fan, T, 4, 2, D, start, prefix)
+    raw = pages.cpu().numpy()
+    rs = np.random.default_rng(1)
+    for g in range(2):
+        for x in range(70, 128):
+            for at in low.offsets(x % 64, D):
+                raw[ptable[g, 1], :, at] = 255 if g else rs.integers(0, 256, (len(at), 2))
+    pages = torch.from_numpy(raw).to(DEV)
+    k = torch.zeros(1, 1, 2, D, device=DEV)
+    k[0, 0, 1, 0] = float("nan")
+    sv.cache4_write(pages, _i32(ptable[1:]), _i32([69]), k, torch.ones_like(k))
+    q[0, 1, 0, 5] = float("nan")
+    got = _run(q, pages, table, start, ptable, prefix, fan)
+    nan = torch.isnan(got[0]).any(-1)
+    want = torch.zeros(6, T, 4, dtype=torch.bool)
+    want[3:, :, 2:] = want[0, 1, 0] = True
+    assert torch.equal(nan.cpu(), want) and torch.equal(torch.isnan(got[1]).cpu(), want)
+    _check(q, pages, table, start, ptable, prefix, fan, got)
+
+
+@pytest.mark.parametrize("D,B,fan,T,Hq,H,prefix", [
+    (128, 64, 8, 5, 32, 8, [1500 + 313 * (g % 8) for g in range(8)]),   # 160 rows a head
+    (64, 96, 96, 2, 4, 4, [5000]),
+    (256, 12, 6, 9, 14, 2, [37, 1155]),                                  # 378 rows a head
+    (128, 300, 300, 1, 8, 1, [2500]),                                    # 2,400 rows
+    (64, 40, 40, 7, 8, 1, [801]),                                        # 2,240 rows
+    (128, 3, 3, 1, 2, 1, [9000]),                                        # six rows, a long prefix
+])
+def test_many_rows_and_long_prefixes(D, B, fan, T, Hq, H, prefix):
+    start = [(b * 37) % 150 for b in range(B)]
+    q, pages, table, ptable = _case(7, B, fan, T, Hq, H, D, start, prefix)
+    got = _run(q, pages, table, start, ptable, prefix, fan)
+    _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: (b * 7 + i * 3 + h) % 11 == 0)
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+
+
+def test_far_scores():
+    """Scores of ordinary and of large magnitude side by side, in the prefix and behind it."""
+    D, T, fan = 64, 1, 4
+    start, prefix = [3] * 4, [200]
+    q, pages, table, ptable = _case(8, 4, fan, T, 2, 1, D, start, prefix)
+    q = q * torch.tensor([1.0, 1e4, 1e9, 1e-9], device=DEV).view(4, 1, 1, 1).bfloat16()
+    got = _run(q, pages, table, start, ptable, prefix, fan)
+    _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: b in (0, 3))
+    # one position outweighs all others: its value, or the mean of those whose scores round alike
+    assert torch.isfinite(got[0]).all() and (got[0].abs() <= 64).all()
+
+
+def test_agrees_with_one_cache():
+    """A prefix of whole pages with each branch's own pages behind it, as one table."""
+    B, fan, T, Hq, H, D, n = 12, 4, 4, 8, 2, 128, 512
+    start, prefix = [(b * 29) % 90 for b in range(B)], [n] * 3
+    q, pages, table, ptable = _case(9, B, fan, T, Hq, H, D, start, prefix)
+    got = _run(q, pages, table, start, ptable, prefix, fan)
+    one = np.concatenate([np.repeat(ptable, fan, 0), table], 1)
+    out, lse = sv.attention_cache4(q, pages, _i32(one), _i32([n + s for s in start]), return_lse=True)
+    assert (got[1] - lse).abs().max() <= 2.0 ** -17
+    assert (got[0].float() - out.float()).abs().max() <= 2.0 ** -6
+
+
+def test_same_outputs_every_time_and_strided():
+    B, fan, T, Hq, H, D = 16, 8, 3, 8, 2, 128
+    start, prefix = [11] * B, [1999, 2345]
+    q, pages, table, ptable = _case(10, B, fan, T, Hq, H, D, start, prefix)
+    want = _run(q, pages, table, start, ptable, prefix, fan)
+    wide = torch.zeros(T, B, Hq + 3, D + 8, dtype=torch.bfloat16, device=DEV)
+    wide[:, :, :Hq, :D] = q.transpose(0, 1)
+    view = wide[:, :, :Hq, :D].transpose(0, 1)
+    target = torch.zeros(B, Hq, T, D, dtype=torch.bfloat16, device=DEV).transpose(1, 2)
+    ws = torch.full((sv.lib().spec_attention_cache4_shared_workspace(B, T, Hq, H, D, fan) + 512,), 255,
+                    dtype=torch.uint8, device=DEV)
+    off = -ws.data_ptr() % 256
+    for _ in range(3):
+        sv.attention_cache4_shared(view, pages, _i32(table), _i32(start), _i32(ptable), _i32(prefix), fan=fan, out=target,
+                                   workspace=ws[off:])
+        assert torch.equal(target, want[0])
