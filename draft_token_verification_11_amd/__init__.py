@@ -168,6 +168,8 @@ def lib():
             L.spec_norm_rotate.argtypes = [spec_heads_t, spec_heads_t, i32, spec_heads_t,
                                            spec_heads_t, i32, P(spec_rotate_t), i32, i32, vp, vp, vp]
             L.spec_norm_rotate.restype = ctypes.c_int
+            L.spec_attention_cache4_window_workspace.argtypes = [i32] * 5
+            L.spec_attention_cache4_window_workspace.restype = sz
             L.spec_attention_cache4_window.argtypes = [spec_cache4_t, spec_heads_t, i32, i32, i32,
                                                        vp, vp, vp, i64, i64, vp, i64, i32, i32,
                                                        ctypes.c_float, spec_heads_t, vp, vp, sz, vp]
@@ -950,7 +952,8 @@ def attention_cache4(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor,
     if out is not None:
         _device_tensor(out, "out", (torch.bfloat16,), 4, index)
     L = lib()
-    need = L.spec_attention_cache4_workspace(B, T, Hq, cache.heads, D)
+    size = L.spec_attention_cache4_workspace if window is None else L.spec_attention_cache4_window_workspace
+    need = size(B, T, Hq, cache.heads, D)
     if need == 0:
         _check(SPEC_ERR_UNSUPPORTED if B and T and Hq and Hq % cache.heads == 0
                else SPEC_ERR_INVALID_ARG, "spec_attention_cache4_workspace")

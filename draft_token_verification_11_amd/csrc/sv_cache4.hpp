@@ -412,8 +412,9 @@ __device__ __forceinline__ int32_t c4_pages(const Args& A, int64_t b, bool& bad)
 constexpr int32_t kC4SegCost = 8;
 
 // Weight of a segment of `pages`.
+template <int COST = kC4SegCost>
 __device__ __forceinline__ int64_t c4_weight(int32_t pages) {
-  return pages ? pages + kC4SegCost : 0;
+  return pages ? pages + COST : 0;
 }
 
 // floor(x / y) for 0 <= x < 2^42, 0 < y < 2^42, from a reciprocal r of y good to
@@ -448,13 +449,13 @@ __device__ __forceinline__ int64_t c4_lane(int64_t x, int l) {
 
 // Weight of all sequences' segments (of one head and row block): a lane sums a
 // run of `per` sequences; `before`: the weight before its run.
-template <typename Args>
+template <int COST = kC4SegCost, typename Args>
 __device__ __forceinline__ int64_t c4_plan(const Args& A, int lane, int32_t per, int64_t& before) {
   int64_t sum = 0;
   for (int32_t j = 0; j < per; ++j) {
     const int64_t b = (int64_t)lane * per + j;
     bool bad;
-    if (b < A.B) sum += c4_weight(c4_pages<false>(A, b, bad));
+    if (b < A.B) sum += c4_weight<COST>(c4_pages<false>(A, b, bad));
   }
   const int64_t incl = c4_prefix(sum, lane);
   before = incl - sum;
@@ -462,7 +463,7 @@ __device__ __forceinline__ int64_t c4_plan(const Args& A, int lane, int32_t per,
 }
 // The sequence in which weight x (below the total) lies, and the weight before
 // it: the lane's run, then 64 sequences of it at a time.
-template <typename Args>
+template <int COST = kC4SegCost, typename Args>
 __device__ __forceinline__ int64_t c4_find(const Args& A, int lane, int32_t per, int64_t before,
                                            int64_t x, int64_t& at) {
   const int run = 63 - __builtin_clzll(__ballot(before <= x));
@@ -471,7 +472,7 @@ __device__ __forceinline__ int64_t c4_find(const Args& A, int lane, int32_t per,
   for (int64_t b0 = (int64_t)run * per;; b0 += 64) {
     const int64_t b = b0 + lane;
     bool bad;
-    const int64_t wt = b < A.B ? c4_weight(c4_pages<false>(A, b, bad)) : 0;
+    const int64_t wt = b < A.B ? c4_weight<COST>(c4_pages<false>(A, b, bad)) : 0;
     const int64_t incl = c4_prefix(wt, lane);
     const uint64_t past = __ballot(at + incl > x);
     if (past) {
@@ -485,14 +486,15 @@ __device__ __forceinline__ int64_t c4_find(const Args& A, int lane, int32_t per,
 
 // The weight of each workgroup's range: an equal share, at least one page per
 // wave and a segment's cost.
-template <int GRID>
+template <int GRID, int COST = kC4SegCost>
 __device__ __forceinline__ int64_t c4_share(int64_t weight) {
   const int64_t s = (weight + GRID - 1) / GRID;
-  return s < 4 + kC4SegCost ? 4 + kC4SegCost : s;
+  return s < 4 + COST ? 4 + COST : s;
 }
 // Page of a segment of `pages` at which weight `x` from its begin lies.
+template <int COST = kC4SegCost>
 __device__ __forceinline__ int32_t c4_cut(int64_t x, int32_t pages) {
-  x -= kC4SegCost;
+  x -= COST;
   return x <= 0 ? 0 : (x >= pages ? pages : (int32_t)x);
 }
 
@@ -698,6 +700,82 @@ __device__ __forceinline__ void c4_take_values(const uint8_t* from, int lane, C4
 #endif
 }
 
+// Scores s of a row tile without those that its rows do not see; their largest in
+// this lane.
+__device__ __forceinline__ float c4_top(c4_f32x4 (&s)[2], int q, bool masked, uint32_t sees) {
+  if (masked) {
+    const uint32_t mine = sees >> (4 * q);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (!((mine >> (16 * i + r)) & 1)) s[i][r] = -__builtin_inff();
+  }
+  float top = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3]));
+#pragma unroll
+  for (int r = 0; r < 4; ++r) top = fmaxf(top, s[1][r]);
+  return top;
+}
+
+// Raises the maxima of row tile rt.
+template <int D, int RT>
+__device__ __forceinline__ void c4_raise(c4_f32x4 (&s)[2], C4State<D, RT>& S, int rt, float c, float top) {
+  const float m = fmaxf(S.m[rt], c4_max_quads(top) * c);
+  const float f = __builtin_amdgcn_exp2f(S.m[rt] - m);
+  S.m[rt] = S.less[rt] = m;
+  S.l[rt] *= f;
+  S.n[rt] *= f;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) S.o[rt][i] *= f;
+  // Below, the exact product less the maximum, which is a rounded one: where
+  // scores are equal, off by half a step of the maximum, which P' and its sums
+  // have in common.  For far rows that would leave their range: they round the
+  // products as they did the maximum.
+  const bool far = __builtin_fabsf(m) > kC4Exact && m > kC4Low;
+  S.far |= __ballot(far);
+  if (far) {
+    const float back = 1.0f / c;  // c is above 2^-104 where a row is far
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[i][r] = c4_scaled_less(s[i][r], c, m) * back;
+    S.less[rt] = 0.f;
+  }
+}
+
+// P' of row tile rt, and its sums.
+template <int D, int RT>
+__device__ __forceinline__ void c4_exps(const c4_f32x4 (&s)[2], C4State<D, RT>& S, int rt, float c, c4_bf16x8& p) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][r], c, -S.less[rt]));
+      sum += e;
+      p[4 * i + r] = (__bf16)e;
+    }
+  S.l[rt] += sum;
+  constexpr c4_bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+  for (int r = 0; r < 8; r += 2)
+    S.n[rt] = __builtin_amdgcn_fdot2_f32_bf16(c4_bf16x2{p[r], p[r + 1]}, one, S.n[rt], false);
+}
+
+// P' of a pair of tiles from its scores s, which this overwrites: the maximum is
+// raised where it has to be, the sums are kept.  masked, sees: as in c4_unit.
+template <int D, int RT>
+__device__ __forceinline__ void c4_probabilities(c4_f32x4 (&s)[RT][2], C4State<D, RT>& S, float c, int q, bool masked,
+                                                 const uint32_t (&sees)[RT], c4_bf16x8 (&p)[RT]) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const float top = c4_top(s[rt], q, masked, sees[rt]);
+    // rare, but for a wave with far rows; the lanes of a row agree on it here
+    if (__ballot(top * c > S.less[rt] + kC4Raise) | S.far) c4_raise(s[rt], S, rt, c, top);
+    c4_exps(s[rt], S, rt, c, p[rt]);
+  }
+}
+
 // One pair of tiles, from its buffer.  masked (of the wave): some of its 32 positions are not
 // seen by some row; sees[] then has this lane's rows' bits, and `valid` those
 // of the positions that hold tokens.  rows_of(j, qf): part j of the rows' operand.
@@ -750,58 +828,7 @@ __device__ __forceinline__ void c4_unit(const uint8_t* from, int half, Q rows_of
         }
   }
   c4_bf16x8 p[RT];  // P' of the pair, the second product's operand
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    if (masked) {
-      const uint32_t mine = sees[rt] >> (4 * q);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (!((mine >> (16 * i + r)) & 1)) s[rt][i][r] = -__builtin_inff();
-    }
-    float top = fmaxf(fmaxf(s[rt][0][0], s[rt][0][1]), fmaxf(s[rt][0][2], s[rt][0][3]));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) top = fmaxf(top, s[rt][1][r]);
-    // rare, but for a wave with far rows; the lanes of a row agree on it here
-    if (__ballot(top * c > S.less[rt] + kC4Raise) | S.far) {
-      const float m = fmaxf(S.m[rt], c4_max_quads(top) * c);
-      const float f = __builtin_amdgcn_exp2f(S.m[rt] - m);
-      S.m[rt] = S.less[rt] = m;
-      S.l[rt] *= f;
-      S.n[rt] *= f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) S.o[rt][i] *= f;
-      // Below, the exact product less the maximum, which is a rounded one: where
-      // scores are equal, off by half a step of the maximum, which P' and its sums
-      // have in common.  For far rows that would leave their range: they round the
-      // products as they did the maximum.
-      const bool far = __builtin_fabsf(m) > kC4Exact && m > kC4Low;
-      S.far |= __ballot(far);
-      if (far) {
-        const float back = 1.0f / c;  // c is above 2^-104 where a row is far
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s[rt][i][r] = c4_scaled_less(s[rt][i][r], c, m) * back;
-        S.less[rt] = 0.f;
-      }
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[rt][i][r], c, -S.less[rt]));
-        sum += e;
-        p[rt][4 * i + r] = (__bf16)e;
-      }
-    S.l[rt] += sum;
-    constexpr c4_bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
-#pragma unroll
-    for (int r = 0; r < 8; r += 2)
-      S.n[rt] = __builtin_amdgcn_fdot2_f32_bf16(c4_bf16x2{p[rt][r], p[rt][r + 1]}, one, S.n[rt], false);
-  }
+  c4_probabilities<D, RT>(s, S, c, q, masked, sees, p);
   // V' of the pair: byte y of token j's codes gives that token's values of two
   // neighbouring d; tokens are paired for each d by a byte permutation
   constexpr int NB = D / 32;  // bytes of a lane's codes of one token
@@ -1306,7 +1333,7 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join(Args A) {
 // Joins those of calls with few segments of many records: a row a workgroup, a
 // quarter of the records a wave.  Where the records stand follows from the
 // lengths alone, as in the attention.
-template <int D, int RT, typename Args = C4AttnArgs>
+template <int D, int RT, typename Args = C4AttnArgs, int GRID = C4Shape<D, RT>::kGrid>
 __global__ __launch_bounds__(256) void k_attention_cache4_join_long(Args A) {
   constexpr int kRows = RT * 16, E = D / 64;
   constexpr int64_t kFloats = C4Rec<D, RT>::kFloats;
@@ -1316,7 +1343,7 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join_long(Args A) {
   const int32_t b = blockIdx.x / HR, hr = blockIdx.x % HR, row = blockIdx.y;
   const int32_t h = hr / A.row_blocks;
   int64_t before;
-  const int64_t share = c4_share<C4Shape<D, RT>::kGrid>(c4_plan(A, lane, per, before) * HR);
+  const int64_t share = c4_share<GRID>(c4_plan(A, lane, per, before) * HR);
   bool bad;
   int64_t at = c4_lane(before, b / per);
   for (int32_t x = b / per * per; x < b; ++x) at += c4_weight(c4_pages<true>(A, x, bad));

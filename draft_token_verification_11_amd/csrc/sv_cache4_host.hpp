@@ -11,6 +11,7 @@
 
 #include "specverify_lowbit.h"
 #include "sv_cache4.hpp"
+#include "sv_cache4_wide.hpp"
 
 namespace {
 
@@ -169,6 +170,54 @@ void launch_attention(Args& A, void* workspace, hipStream_t st) {
     hipLaunchKernelGGL((sv::k_attention_cache4_join_long<D, RT, Args>), dim3(unsigned(segments), RT * 16), dim3(256), 0, st, A);
   else
     hipLaunchKernelGGL((sv::k_attention_cache4_join<D, RT, Args>), dim3(kGrid, RT * 4), dim3(256), 0, st, A);
+}
+
+// The same for many rows of a kv head, whose pages the waves of a workgroup
+// share: rows of a block, and blocks.
+template <typename F>
+void with_wide(int32_t d, F f) {
+  if (d == 64) f(std::integral_constant<int, 64>());
+  else if (d == 128) f(std::integral_constant<int, 128>());
+  else f(std::integral_constant<int, 256>());
+}
+void wide_blocks(int64_t rows, int32_t d, int32_t* block_rows, int64_t* blocks) {
+  with_wide(d, [&](auto D) {
+    const int64_t t = (rows + 15) / 16, most = sv::C4Wide<D>::kTiles;
+    *blocks = (t + most - 1) / most;
+    *block_rows = int32_t((t + *blocks - 1) / *blocks * 16);
+  });
+}
+size_t wide_workspace(int32_t d) {
+  size_t bytes = 0;
+  with_wide(d, [&](auto D) {
+    bytes = size_t(sv::C4Wide<D>::kGrid) * (sizeof(sv::C4Cut) + 2 * sizeof(float) * size_t(sv::C4Wide<D>::kFloats));
+  });
+  return bytes;
+}
+// Rows of a kv head that take more than one block of the other kernel are worth
+// this one where its workgroups have so many pages each: its ends cost more.
+constexpr int64_t kWidePages = 16;
+bool wide_pays(int64_t rows, int32_t d, int64_t seqs_heads, int64_t pages) {
+  if (rows <= 16 * max_tiles(d)) return false;
+  int32_t block_rows;
+  int64_t blocks, grid = 0;
+  wide_blocks(rows, d, &block_rows, &blocks);
+  with_wide(d, [&](auto D) { grid = sv::C4Wide<D>::kGrid; });
+  return seqs_heads * blocks >= (kWidePages * grid + pages - 1) / pages;
+}
+template <int D, typename Args>
+void launch_wide(Args& A, sv::C4Block K, void* workspace, hipStream_t st) {
+  using Sh = sv::C4Wide<D>;
+  constexpr int kGrid = Sh::kGrid;
+  A.cuts = static_cast<sv::C4Cut*>(workspace);
+  A.parts = reinterpret_cast<float*>(A.cuts + kGrid);
+  hipLaunchKernelGGL((sv::k_attention_cache4_wide<D, Args>), dim3(kGrid), dim3(64 * Sh::kWaves), 0, st, A, K);
+  if (!A.split) return;
+  const dim3 grid{unsigned(kGrid), unsigned(K.rows / 16)};
+  if (int64_t(A.B) * A.cache.heads * A.row_blocks <= kAttnFew)
+    hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 4, Args>), grid, dim3(1024), 0, st, A, K);
+  else
+    hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 1, Args>), grid, dim3(256), 0, st, A, K);
 }
 
 // Arguments of an attention call, checked, and its row tiles.

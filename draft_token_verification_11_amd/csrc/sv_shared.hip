@@ -7,6 +7,7 @@
 
 #include "specverify_step.h"
 #include "sv_cache4_host.hpp"
+#include "sv_cache4_short.hpp"
 
 namespace {
 
@@ -16,18 +17,40 @@ bool shared_sizes_ok(int32_t B, int32_t T, int32_t q_heads, int32_t fan) {
   return fan >= 1 && int64_t(std::min(fan, B)) * T <= kMaxSharedRows / q_heads;
 }
 
+// How the rows of a prefix are held.
+struct PrefixShape {
+  bool wide;           // many rows: the waves of a workgroup share the pages
+  int tiles;           // not wide: tiles of a block
+  int32_t block_rows;  // wide: rows of a block
+  int64_t blocks;
+};
+PrefixShape prefix_shape(int64_t rows, int32_t d, int64_t prefixes_heads, int64_t cols) {
+  PrefixShape x{};
+  x.wide = wide_pays(rows, d, prefixes_heads, cols);
+  if (x.wide) wide_blocks(rows, d, &x.block_rows, &x.blocks);
+  else row_blocks(rows, d, &x.tiles, &x.blocks);
+  return x;
+}
+// Pages of a branch's own up to which a wave goes through them by itself.
+constexpr int32_t kShortCols = 8;
+// Branches up to which their live rows are counted through.
+constexpr int32_t kCompactFan = 4096;
+
 // A call's workspace: the rows' records, and one attention's after the other.
+// Its size does not go by the tables, of which a size query knows nothing.
 struct SharedSpace {
   size_t rec, stat, scratch;
   size_t bytes() const { return rec + stat + scratch; }
 };
 SharedSpace shared_space(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d, int32_t fan) {
-  const size_t rows = size_t(B) * size_t(T) * size_t(q_heads);
+  const size_t count = size_t(B) * size_t(T) * size_t(q_heads);
+  const int64_t rows = int64_t(std::min(fan, B)) * T * (q_heads / kv_heads);
   int tiles;
   int64_t blocks;
-  row_blocks(int64_t(std::min(fan, B)) * T * (q_heads / kv_heads), d, &tiles, &blocks);
-  return {align256(rows * size_t(d) * 4), align256(rows * 16),
-          std::max(attention_workspace(T, q_heads, kv_heads, d), shape_workspace(d, tiles))};
+  row_blocks(rows, d, &tiles, &blocks);
+  const size_t prefix = std::max(shape_workspace(d, tiles), rows > 16 * max_tiles(d) ? wide_workspace(d) : 0);
+  return {align256(count * size_t(d) * 4), align256(count * 16),
+          std::max(attention_workspace(T, q_heads, kv_heads, d), prefix)};
 }
 
 }  // namespace
@@ -62,10 +85,8 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
   if ((rc = check_cache(prefix)) != SPEC_OK) return rc;
   if (!prefix_len || !aligned(prefix_len, 4)) return SPEC_ERR_INVALID_ARG;
   const int32_t d = cache.head_dim, each = std::min(fan, B), prefixes = (B + each - 1) / each;
-  int prefix_tiles;
-  int64_t blocks;
-  row_blocks(int64_t(each) * T * (q_heads / cache.heads), d, &prefix_tiles, &blocks);
-  if (prefixes * (int64_t(prefix_cols) + sv::kC4SegCost) * cache.heads >= (int64_t(1) << 40) / blocks)
+  const PrefixShape shape = prefix_shape(int64_t(each) * T * (q_heads / cache.heads), d, int64_t(prefixes) * cache.heads, prefix_cols);
+  if (prefixes * (int64_t(prefix_cols) + sv::kC4SegCost) * cache.heads >= (int64_t(1) << 40) / shape.blocks)
     return SPEC_ERR_UNSUPPORTED;
   const SharedSpace space = shared_space(B, T, q_heads, cache.heads, d, fan);
   if (workspace_bytes < space.bytes()) return SPEC_ERR_WORKSPACE;
@@ -78,7 +99,7 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
   P.cache = view(prefix);
   P.start = prefix_len;
   P.B = prefixes;
-  P.row_blocks = int32_t(blocks);
+  P.row_blocks = int32_t(shape.blocks);
   P.split = prefix_cols > kAttnWhole;
   P.fan = each;
   P.seqs = B;
@@ -92,8 +113,16 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
   O.stat = stat;
   auto st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  with_shape(d, prefix_tiles, [&](auto D, auto RT) { launch_attention<D, RT>(P, scratch, st); });
-  with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(O, scratch, st); });
+  const sv::C4Block K{shape.block_rows, count && each <= kCompactFan};
+  if (shape.wide) with_wide(d, [&](auto D) { launch_wide<D>(P, K, scratch, st); });
+  else with_shape(d, shape.tiles, [&](auto D, auto RT) { launch_attention<D, RT>(P, scratch, st); });
+  const int64_t waves = int64_t(B) * cache.heads * O.row_blocks;
+  if (cache.table_cols <= kShortCols && grid_fits((waves + 3) / 4, 256))
+    with_shape(d, tiles, [&](auto D, auto RT) {
+      hipLaunchKernelGGL((sv::k_attention_cache4_short<D, RT, sv::C4OwnArgs>), dim3(unsigned((waves + 3) / 4)), dim3(256), 0, st, O);
+    });
+  else
+    with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(O, scratch, st); });
   return finish_launch();
 }
 

@@ -50,6 +50,12 @@ int launch_rotate(sv::RotateArgs& A, hipStream_t st) {
   return finish_launch();
 }
 
+// Scratch of either kernel that a window may take.
+size_t window_workspace(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
+  const bool many = int64_t(T) * (q_heads / kv_heads) > 16 * max_tiles(d);
+  return std::max(attention_workspace(T, q_heads, kv_heads, d), many ? wide_workspace(d) : size_t(0));
+}
+
 }  // namespace
 
 extern "C" {
@@ -83,6 +89,12 @@ int spec_norm_rotate(spec_heads_t q, spec_heads_t q_out, int32_t q_heads, spec_h
   return to_bf ? launch_rotate<float, uint16_t>(A, st) : launch_rotate<float, float>(A, st);
 }
 
+size_t spec_attention_cache4_window_workspace(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
+                                              int32_t head_dim) {
+  if (check_attention_sizes(B, T, q_heads, heads, head_dim) != SPEC_OK) return 0;
+  return window_workspace(T, q_heads, heads, head_dim);
+}
+
 int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B, int32_t T,
                                  int32_t q_heads, const int32_t* start, const int32_t* count,
                                  const uint32_t* mask, int64_t mask_seq_stride,
@@ -97,6 +109,7 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
   const int rc = attention_args(cache, q, B, T, q_heads, start, count, mask, mask_seq_stride, mask_pos_stride, scale,
                                 out, lse, workspace, workspace_bytes, &A, &tiles);
   if (rc != SPEC_OK) return rc;
+  if (workspace_bytes < window_workspace(T, q_heads, cache.heads, cache.head_dim)) return SPEC_ERR_WORKSPACE;
   A.window = window;
   A.sinks = sinks;
   A.depth = depth;
@@ -105,8 +118,18 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
   const int64_t pages = (int64_t(window) + T + sv::kC4Page - 2) / sv::kC4Page + 1 + (int64_t(sinks) + sv::kC4Page - 1) / sv::kC4Page;
   A.split = std::min<int64_t>(pages, cache.table_cols) > kAttnWhole;
   auto st = static_cast<hipStream_t>(stream);
+  const int32_t d = cache.head_dim;
+  const int64_t rows = int64_t(T) * A.G;
   (void)hipGetLastError();
-  with_shape(cache.head_dim, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(A, workspace, st); });
+  if (wide_pays(rows, d, int64_t(B) * cache.heads, std::min<int64_t>(pages, cache.table_cols))) {
+    sv::C4Block K{0, 0};
+    int64_t blocks;
+    wide_blocks(rows, d, &K.rows, &blocks);
+    A.row_blocks = int32_t(blocks);
+    with_wide(d, [&](auto D) { launch_wide<D>(A, K, workspace, st); });
+  } else {
+    with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(A, workspace, st); });
+  }
   return finish_launch();
 }
 

@@ -71,8 +71,11 @@ int spec_norm_rotate(spec_heads_t q, spec_heads_t q_out, int32_t q_heads, spec_h
  *          depths, each in 0 .. T - 1 (others are taken as the nearer end); NULL:
  *          i.  Only with a mask.
  * Pages no position of which is below sinks or above start[b] - window are not
- * read, and their table entries may hold anything.  For all else, and the
- * workspace, spec_attention_cache4's words hold. */
+ * read, and their table entries may hold anything.  For all else
+ * spec_attention_cache4's words hold.
+ * workspace: spec_attention_cache4_window_workspace bytes, 256-byte aligned. */
+size_t spec_attention_cache4_window_workspace(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
+                                              int32_t head_dim);
 int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B, int32_t T,
                                  int32_t q_heads, const int32_t* start, const int32_t* count,
                                  const uint32_t* mask, int64_t mask_seq_stride,
@@ -93,7 +96,8 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
  *                 whose length lies outside, or that has a page outside the
  *                 pool, becomes NaN
  *   fan >= 1; min(fan, B) T q_heads at most 2^30
- * For all else spec_attention_cache4's words hold. */
+ * For all else spec_attention_cache4's words hold.
+ * workspace: spec_attention_cache4_shared_workspace bytes, 256-byte aligned. */
 size_t spec_attention_cache4_shared_workspace(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
                                               int32_t head_dim, int32_t fan);
 int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_table,

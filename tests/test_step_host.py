@@ -25,8 +25,8 @@ P, ODD = ctypes.c_void_p(4096), ctypes.c_void_p(4098)
 def test_header_and_symbols():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(spec_[a-z0-9_]+)\s*\(", text)))
-    assert names == sorted(["spec_norm_rotate", "spec_attention_cache4_window", "spec_attention_cache4_shared_workspace",
-                            "spec_attention_cache4_shared", "spec_cache4_reserve", "spec_cache4_slots"])
+    assert names == sorted(["spec_norm_rotate", "spec_attention_cache4_window", "spec_attention_cache4_window_workspace",
+                            "spec_attention_cache4_shared_workspace", "spec_attention_cache4_shared", "spec_cache4_reserve", "spec_cache4_slots"])
     out = subprocess.run(["nm", "-D", "--defined-only", sv.library_path()], capture_output=True, text=True,
                          check=True).stdout.split()
     assert all(n in out for n in names)
@@ -110,6 +110,12 @@ def test_attention_refusals(call):
 
 def test_window_refusals():
     assert _window(window=0) == BAD and _window(window=-5) == BAD and _window(sinks=-1) == BAD
+    L = sv.lib()
+    for T in (3, 100):
+        need = L.spec_attention_cache4_window_workspace(2, T, 4, 2, 128)
+        assert need > 0 and _window(T=T, wb=need - 1, q=_heads(seq=1 << 16, pos=512), out=_heads(seq=1 << 16, pos=512)) == WS
+    for bad in [(0, 1, 8, 8, 128), (1, 0, 8, 8, 128), (1, 257, 8, 8, 128), (1, 1, 9, 8, 128), (1, 1, 8, 8, 80)]:
+        assert L.spec_attention_cache4_window_workspace(*bad) == 0, bad
     assert _window(depth=ODD) == BAD and _window(depth=P, ds=-1) == BAD and _window(depth=P, mask=None) == BAD
 
 
