@@ -181,7 +181,9 @@ def lib():
                                                        i64, ctypes.c_float, spec_heads_t, vp, vp,
                                                        sz, vp]
             L.spec_attention_cache4_shared.restype = ctypes.c_int
-            L.spec_cache4_reserve.argtypes = [vp, i64, i32, vp, vp, i32, vp, i32, vp, vp]
+            L.spec_cache4_reserve_workspace.argtypes = [i32]
+            L.spec_cache4_reserve_workspace.restype = sz
+            L.spec_cache4_reserve.argtypes = [vp, i64, i32, vp, vp, i32, vp, i32, vp, vp, sz, vp]
             L.spec_cache4_reserve.restype = ctypes.c_int
             L.spec_cache4_slots.argtypes = [vp, i64, i32, i32, i32, i32, vp, vp, vp, vp]
             L.spec_cache4_slots.restype = ctypes.c_int
@@ -1187,7 +1189,8 @@ def attention_cache4_shared(q: torch.Tensor, pages: torch.Tensor, table: torch.T
 
 
 def cache4_reserve(table: torch.Tensor, held: torch.Tensor, need: torch.Tensor,
-                   free: torch.Tensor, free_count: torch.Tensor, *, stream=None) -> None:
+                   free: torch.Tensor, free_count: torch.Tensor, *,
+                   workspace: torch.Tensor | None = None, stream=None) -> None:
     """Brings every sequence to the pages that need[b] tokens take, in place:
     table [B][P] holds its held[b] pages first, ``free`` [capacity] the
     free_count[0] pages that are nobody's (all int32).  Pages too many go back on
@@ -1207,10 +1210,15 @@ def cache4_reserve(table: torch.Tensor, held: torch.Tensor, need: torch.Tensor,
     c = _per_sequence(free_count, "free_count", 1, index)
     if c is None:
         raise ValueError("free_count is required")
+    L = lib()
+    size = L.spec_cache4_reserve_workspace(B)
+    if size == 0:
+        _check(SPEC_ERR_UNSUPPORTED if B else SPEC_ERR_INVALID_ARG, "spec_cache4_reserve_workspace")
     st, ctx = _on(index, stream)
     with ctx:
-        rc = lib().spec_cache4_reserve(table.data_ptr(), stride, cols, h, w, B, free.data_ptr(),
-                                       free.shape[0], c, st)
+        ws = _scratch(workspace, table.device, size)
+        rc = L.spec_cache4_reserve(table.data_ptr(), stride, cols, h, w, B, free.data_ptr(),
+                                   free.shape[0], c, ws.data_ptr(), ws.numel() * ws.element_size(), st)
     _check(rc, "spec_cache4_reserve")
 
 

@@ -25,90 +25,126 @@ __device__ __forceinline__ void res_pages(const ReserveArgs& A, int32_t b, int32
   if (need < 0 || held < 0 || held > A.table_cols || want > A.table_cols) want = held;
 }
 
-// Moves `pages` pages between a row of the table and the stack, whose ends are
-// `row` (the first of them) and `top` (one past its place): page p stands at
-// top - 1 - p.
-template <bool GIVE>
-__device__ __forceinline__ void res_move(int32_t* row, int32_t* top, int32_t p) {
-  if constexpr (GIVE) {
-    top[-1 - p] = row[p];
-    row[p] = -1;
-  } else {
-    row[p] = top[-1 - p];
+// All pages that go back are counted through in the order of (sequence, page), and
+// so are those that are taken.  Page j that goes back stands at full - 1 - j of
+// the free pages, `full` being how many there are before the first is taken, and
+// page j that is taken comes from there: with fewer than j + 1 pages going back
+// from among those that were free before.  So index j alone says what is read
+// and what is written, for both together, and no two write or read what the
+// other writes.  Which sequence it is of follows from the sums over the
+// sequences before: a search in those.
+struct ReservePlan {
+  int64_t full, gives, takes;  // takes: of the sequences that are served
+};
+
+// The first of n ascending sums (each with its own element) that passes j.
+__device__ __forceinline__ int32_t res_find(const int32_t* upto, int32_t n, int32_t j) {
+  int32_t lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (upto[mid] > j) hi = mid;
+    else lo = mid + 1;
   }
+  return lo;
 }
-constexpr int32_t kResOwn = 8;  // pages that a thread moves by itself; more are a wave's
-template <bool GIVE>
-__device__ __forceinline__ void res_run(int32_t* row, int32_t* top, int32_t pages) {
-  const int lane = threadIdx.x & 63;
-  if (pages <= kResOwn)
-    for (int32_t p = 0; p < pages; ++p) res_move<GIVE>(row, top, p);
-  for (uint64_t many = __ballot(pages > kResOwn); many; many &= many - 1) {
-    const int l = __builtin_ctzll(many);
-    int32_t* const r = reinterpret_cast<int32_t*>(c4_lane(reinterpret_cast<int64_t>(row), l));
-    int32_t* const t = reinterpret_cast<int32_t*>(c4_lane(reinterpret_cast<int64_t>(top), l));
-    const int32_t n = __builtin_amdgcn_readlane(pages, l);
-    for (int32_t p = lane; p < n; p += 64) res_move<GIVE>(r, t, p);
+
+// Moves pages j, j + step, ..  held: as it is after the call.
+__device__ __forceinline__ void res_move(const ReserveArgs& A, const ReservePlan& P, const int32_t* give_upto,
+                                         const int32_t* take_upto, const int32_t* held, int64_t j, int64_t step) {
+  for (const int64_t end = P.gives > P.takes ? P.gives : P.takes; j < end; j += step) {
+    int32_t* const top = A.free_pages + (P.full - 1 - j);
+    int32_t page;
+    if (j < P.gives) {
+      const int32_t b = res_find(give_upto, A.B, (int32_t)j), before = b ? give_upto[b - 1] : 0;
+      int32_t* const at = A.table + b * A.table_stride + held[b] + ((int32_t)j - before);
+      page = *at;
+      *at = -1;
+      *top = page;
+    } else {
+      page = *top;
+    }
+    if (j < P.takes) {
+      const int32_t b = res_find(take_upto, A.B, (int32_t)j);
+      A.table[b * A.table_stride + held[b] - (take_upto[b] - (int32_t)j)] = page;
+    }
   }
 }
 
 constexpr int kResThreads = 1024;
 
-// One workgroup, a run of sequences a thread: both sums over the sequences, then
-// the pages that go back, then those that are taken, which may be among them.
-__global__ __launch_bounds__(kResThreads) void k_cache4_reserve(ReserveArgs A) {
+// The sums, by one workgroup, a run of `per` sequences a thread: into give_upto
+// and take_upto, with the lengths after the call in held (which may be A.held).
+// False where nothing may change.  Sums of what is taken past what there is
+// stand as one past the free pages: no page is searched for there.
+__device__ __forceinline__ bool res_plan(const ReserveArgs& A, ReservePlan& P, int32_t* give_upto, int32_t* take_upto,
+                                         int32_t* held_after) {
   __shared__ int64_t gives[kResThreads / 64], takes[kResThreads / 64];
   __shared__ unsigned long long used;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int32_t per = (A.B + kResThreads - 1) / kResThreads;
   const int32_t b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
   int64_t give = 0, take = 0;
+  int32_t held = 0, want = 0;
   for (int32_t b = b0; b < b1; ++b) {
-    int32_t held, want;
     res_pages(A, b, held, want);
     give += max(held - want, 0);
     take += max(want - held, 0);
   }
   const int64_t free0 = *A.free_count;
-  const int64_t give_upto = c4_prefix(give, lane), take_upto = c4_prefix(take, lane);
-  if (lane == 63) gives[w] = give_upto, takes[w] = take_upto;
+  int64_t give_at = c4_prefix(give, lane), take_at = c4_prefix(take, lane);
+  if (lane == 63) gives[w] = give_at, takes[w] = take_at;
   if (tid == 0) used = 0;
   __syncthreads();
-  int64_t give_at = give_upto - give, take_at = take_upto - take, full = free0;
+  give_at -= give;
+  take_at -= take;
+  P.gives = 0;
+#pragma unroll
   for (int x = 0; x < kResThreads / 64; ++x) {
     if (x < w) give_at += gives[x], take_at += takes[x];
-    full += gives[x];
+    P.gives += gives[x];
   }
-  if (free0 < 0 || full > A.capacity) return;  // free0 below its capacity too, then
-  // The threads of a wave go through their runs together; past its run a thread
-  // has no pages to move.
-  for (int32_t j = 0; j < per; ++j) {
-    const int32_t b = b0 + j;
-    int32_t held = 0, want = 0;
-    if (b < b1) res_pages(A, b, held, want);
-    const int32_t n = max(held - want, 0);
-    res_run<true>(A.table + b * A.table_stride + want, A.free_pages + (full - give_at), n);
-    give_at += n;
-    if (n) A.held[b] = want;
-  }
-  __syncthreads();
+  P.full = free0 + P.gives;
+  if (free0 < 0 || P.full > A.capacity) return false;
   int64_t most = 0;
-  for (int32_t j = 0; j < per; ++j) {
-    const int32_t b = b0 + j;
-    int32_t held = 0, want = 0;
-    if (b < b1) res_pages(A, b, held, want);
-    const int32_t miss = max(want - held, 0);
-    take_at += miss;
-    const bool served = miss > 0 && take_at <= full;
-    res_run<false>(A.table + b * A.table_stride + held, A.free_pages + (full - (take_at - miss)), served ? miss : 0);
-    if (served) {
-      A.held[b] = want;
-      most = take_at;
-    }
+  for (int32_t b = b0; b < b1; ++b) {
+    if (per > 1) res_pages(A, b, held, want);
+    give_at += max(held - want, 0);
+    take_at += max(want - held, 0);
+    const bool served = take_at <= P.full;
+    if (served) most = take_at;
+    give_upto[b] = (int32_t)give_at;
+    take_upto[b] = served ? (int32_t)take_at : 0x7FFFFFFF;
+    held_after[b] = want < held || served ? want : held;
   }
   if (most) atomicMax(&used, (unsigned long long)most);
   __syncthreads();
-  if (tid == 0) *A.free_count = (int32_t)(full - (int64_t)used);
+  P.takes = (int64_t)used;
+  return true;
+}
+
+// Few sequences: all of it by one workgroup.
+constexpr int32_t kResFew = 1024;
+__global__ __launch_bounds__(kResThreads) void k_cache4_reserve(ReserveArgs A) {
+  __shared__ int32_t give_upto[kResFew], take_upto[kResFew], held[kResFew];
+  ReservePlan P;
+  if (!res_plan(A, P, give_upto, take_upto, held)) return;
+  res_move(A, P, give_upto, take_upto, held, threadIdx.x, kResThreads);
+  if ((int32_t)threadIdx.x < A.B) A.held[threadIdx.x] = held[threadIdx.x];
+  if (threadIdx.x == 0) *A.free_count = (int32_t)(P.full - P.takes);
+}
+
+// Many: the sums by one workgroup, into `scratch` [plan, give_upto, take_upto], and
+// the pages by as many as it takes.
+__global__ __launch_bounds__(kResThreads) void k_cache4_reserve_plan(ReserveArgs A, ReservePlan* plan, int32_t* upto) {
+  ReservePlan P;
+  const bool ok = res_plan(A, P, upto, upto + A.B, A.held);
+  if (threadIdx.x) return;
+  if (ok) *A.free_count = (int32_t)(P.full - P.takes);
+  else P.full = P.gives = P.takes = 0;
+  *plan = P;
+}
+__global__ __launch_bounds__(256) void k_cache4_reserve_move(ReserveArgs A, const ReservePlan* plan, const int32_t* upto) {
+  res_move(A, *plan, upto, upto + A.B, A.held, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 struct SlotArgs {
@@ -124,7 +160,8 @@ struct SlotArgs {
 __global__ __launch_bounds__(256) void k_cache4_slots(SlotArgs A) {
   const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (x >= A.tokens) return;
-  const int64_t b = x / A.T;
+  // as a rule all of it has 32 bits
+  const int64_t b = A.tokens >> 31 ? x / A.T : (uint32_t)x / (uint32_t)A.T;
   const int32_t i = (int32_t)(x - b * A.T);
   const C4View cache{nullptr, A.table, A.table_stride, A.n_pages, A.table_cols, 0};
   const int32_t s = A.start[b], n = A.count ? A.count[b] : A.T;

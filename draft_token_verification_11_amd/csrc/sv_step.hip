@@ -16,6 +16,9 @@ namespace {
 // Waves that a small rotation is cut into: as many as the compute units hold at once.
 constexpr int64_t kRotateWaves = 8192;
 
+// Workgroups that move the pages of a call of many sequences.
+constexpr int64_t kReserveBlocks = 1024;
+
 // One side of a rotation; a side without heads is not looked at.
 int check_side(const spec_heads_t& in, const spec_heads_t& out, int32_t heads, const void* weight,
                const spec_rotate_t& how, int32_t B, int32_t T) {
@@ -133,18 +136,34 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
   return finish_launch();
 }
 
+size_t spec_cache4_reserve_workspace(int32_t B) {
+  return B < 1 || B > kMaxB ? 0 : 256 + align256(size_t(B) * 8);
+}
+
 int spec_cache4_reserve(int32_t* table, int64_t table_stride, int32_t table_cols, int32_t* held,
                         const int32_t* need, int32_t B, int32_t* free_pages,
-                        int32_t free_capacity, int32_t* free_count, void* stream) {
+                        int32_t free_capacity, int32_t* free_count, void* workspace,
+                        size_t workspace_bytes, void* stream) {
   for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(held), static_cast<const void*>(need),
                         static_cast<const void*>(free_pages), static_cast<const void*>(free_count)})
     if (!p || !aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
   if (B < 1 || table_cols < 1 || table_stride < table_cols || free_capacity < 1) return SPEC_ERR_INVALID_ARG;
   if (B > kMaxB || table_cols > kMaxTableCols) return SPEC_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < spec_cache4_reserve_workspace(B))
+    return SPEC_ERR_WORKSPACE;
   const sv::ReserveArgs A{table, table_stride, held, need, free_pages, free_count, table_cols, B, free_capacity};
   auto st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  hipLaunchKernelGGL(sv::k_cache4_reserve, dim3(1), dim3(sv::kResThreads), 0, st, A);
+  if (B <= sv::kResFew) {
+    hipLaunchKernelGGL(sv::k_cache4_reserve, dim3(1), dim3(sv::kResThreads), 0, st, A);
+    return finish_launch();
+  }
+  auto* const plan = static_cast<sv::ReservePlan*>(workspace);
+  auto* const upto = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + 256);
+  const int64_t most = std::min<int64_t>(int64_t(B) * table_cols, free_capacity);  // pages that a call can move
+  const unsigned blocks = unsigned(std::min<int64_t>((most + 255) / 256, kReserveBlocks));
+  hipLaunchKernelGGL(sv::k_cache4_reserve_plan, dim3(1), dim3(sv::kResThreads), 0, st, A, plan, upto);
+  hipLaunchKernelGGL(sv::k_cache4_reserve_move, dim3(blocks), dim3(256), 0, st, A, plan, upto);
   return finish_launch();
 }
 

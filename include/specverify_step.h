@@ -129,10 +129,13 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
  * Data faults: a sequence with held[b] or w outside 0 .. table_cols, or need[b]
  * < 0, stays as it is; where free_count[0], or what it would be before the first
  * page is taken, lies outside 0 .. free_capacity, nothing is changed.
- * B at most 65536. */
+ * B at most 65536.
+ * workspace: spec_cache4_reserve_workspace bytes, 256-byte aligned. */
+size_t spec_cache4_reserve_workspace(int32_t B);
 int spec_cache4_reserve(int32_t* table, int64_t table_stride, int32_t table_cols, int32_t* held,
                         const int32_t* need, int32_t B, int32_t* free_pages,
-                        int32_t free_capacity, int32_t* free_count, void* stream);
+                        int32_t free_capacity, int32_t* free_count, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /* slots[b][i] = 64 table[b][x / 64] + x % 64, x = start[b] + i: where new token i
  * stands in a pool of n_pages pages; -1 for i >= count[b] (NULL: T), for a page

@@ -44,17 +44,17 @@ int main() {
       h = how;
       h.rotary_dim = a;
       REFUSED(spec_norm_rotate(x, x, 2, x, x, 1, &h, 2, 3, c32, nullptr, nullptr));
-      REFUSED(spec_cache4_reserve(m32, 4, a > 1 << 24 ? a : -1, m32, c32, 2, m32, 8, m32, nullptr));
+      REFUSED(spec_cache4_reserve(m32, 4, a > 1 << 24 ? a : -1, m32, c32, 2, m32, 8, m32, p, 1 << 20, nullptr));
       REFUSED(spec_norm_rotate(x, x, 16384, x, x, a, &how, 2, 3, c32, nullptr, nullptr));
       REFUSED(spec_norm_rotate(x, x, a < 0 ? a : big, x, x, a, &how, 2, 3, c32, nullptr, nullptr));
     }
     if (a < 1 || a > 1 << 16) {
       REFUSED(spec_norm_rotate(x, x, 2, x, x, 1, &how, a, 3, c32, nullptr, nullptr));
-      REFUSED(spec_cache4_reserve(m32, 4, 4, m32, c32, a, m32, 8, m32, nullptr));
+      REFUSED(spec_cache4_reserve(m32, 4, 4, m32, c32, a, m32, 8, m32, p, 1 << 20, nullptr));
       REFUSED(spec_cache4_slots(c32, 4, 4, 8, a, 3, c32, nullptr, static_cast<int64_t*>(p), nullptr));
     }
     if (a < 1 || a > 1 << 24) REFUSED(spec_cache4_slots(c32, 4, 4, 8, 2, a, c32, nullptr, static_cast<int64_t*>(p), nullptr));
-    if (a < 1) REFUSED(spec_cache4_reserve(m32, 4, 4, m32, c32, 2, m32, a, m32, nullptr));
+    if (a < 1) REFUSED(spec_cache4_reserve(m32, 4, 4, m32, c32, 2, m32, a, m32, p, 1 << 20, nullptr));
   }
   const spec_rotate_t how{128, 128, 0, 1, 1e-6f, SPEC_DTYPE_BF16, p, p, static_cast<const float*>(p), nullptr, 0};
   REFUSED(spec_norm_rotate(x, x, 2, x, x, 1, &how, 1 << 16, 1 << 24, c32, nullptr, nullptr));
@@ -70,7 +70,7 @@ int main() {
   for (float c : {0.0f, -1.0f, -INFINITY, INFINITY, NAN, 3e38f, 1e-45f})
     REFUSED(spec_attention_cache4_shared(good, c32, 4, 4, c32, 2, x, 2, 3, 2, c32, nullptr, nullptr, 0, 0, c, x, nullptr, p, 0,
                                          nullptr));
-  REFUSED(spec_cache4_reserve(static_cast<int32_t*>(odd), 4, 4, m32, c32, 2, m32, 8, m32, nullptr));
+  REFUSED(spec_cache4_reserve(static_cast<int32_t*>(odd), 4, 4, m32, c32, 2, m32, 8, m32, p, 1 << 20, nullptr));
   std::printf(bad ? "bad %d\n" : "sanitized step validation ok\n", bad);
   return bad != 0;
 }

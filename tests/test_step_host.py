@@ -26,7 +26,8 @@ def test_header_and_symbols():
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(spec_[a-z0-9_]+)\s*\(", text)))
     assert names == sorted(["spec_norm_rotate", "spec_attention_cache4_window", "spec_attention_cache4_window_workspace",
-                            "spec_attention_cache4_shared_workspace", "spec_attention_cache4_shared", "spec_cache4_reserve", "spec_cache4_slots"])
+                            "spec_attention_cache4_shared_workspace", "spec_attention_cache4_shared", "spec_cache4_reserve", "spec_cache4_reserve_workspace",
+                            "spec_cache4_slots"])
     out = subprocess.run(["nm", "-D", "--defined-only", sv.library_path()], capture_output=True, text=True,
                          check=True).stdout.split()
     assert all(n in out for n in names)
@@ -141,12 +142,17 @@ def test_shared_refusals():
 def test_pages_refusals():
     L = sv.lib()
 
-    def reserve(table=P, stride=4, cols=4, held=P, need=P, B=2, free=P, cap=8, count=P):
-        return L.spec_cache4_reserve(table, stride, cols, held, need, B, free, cap, count, None)
+    def reserve(table=P, stride=4, cols=4, held=P, need=P, B=2, free=P, cap=8, count=P, w=P, wb=1 << 20):
+        return L.spec_cache4_reserve(table, stride, cols, held, need, B, free, cap, count, w, wb, None)
 
     for name in ("table", "held", "need", "free", "count"):
         assert reserve(**{name: None}) == BAD and reserve(**{name: ODD}) == BAD
     assert reserve(stride=3) == BAD and reserve(cols=0) == BAD and reserve(B=0) == BAD and reserve(cap=0) == BAD
+    assert reserve(w=None) == WS and reserve(w=ctypes.c_void_p(4096 + 16)) == WS
+    for B in (2, 1024, 5000):
+        need = L.spec_cache4_reserve_workspace(B)
+        assert need > 0 and reserve(B=B, wb=need - 1) == WS
+    assert [L.spec_cache4_reserve_workspace(B) for B in (0, -1, 65537)] == [0, 0, 0]
     assert reserve(B=65537) == UNSUP and reserve(cols=(1 << 24) + 1, stride=1 << 25) == UNSUP
 
     def slots(table=P, stride=4, cols=4, n=8, B=2, T=3, start=P, count=None, out=P):
