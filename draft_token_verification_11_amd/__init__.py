@@ -756,7 +756,9 @@ def _heads(t, what, shape=None) -> spec_heads_t:
 
 def _table(table, what, rows, index):
     """A page table [rows][cols], checked: (cols, the stride of its rows)."""
-    _device_tensor(table, what, (torch.int32,), 2, index)
+    if not (type(table) is torch.Tensor and table.dtype is torch.int32 and table.dim() == 2 and
+            table.get_device() == index):
+        _device_tensor(table, what, (torch.int32,), 2, index)
     n, cols = table.shape
     if n != rows or (table.stride(1) != 1 and cols > 1):
         raise ValueError("%s must be [%d][pages of a sequence] with a contiguous last axis" % (what, rows))
@@ -799,6 +801,9 @@ def _depths(depth, B, T, index):
 def _per_sequence(t, what, B, index):
     if t is None:
         return None
+    if type(t) is torch.Tensor and t.dtype is torch.int32 and t.shape == (B,) and \
+            t.get_device() == index and (B == 1 or t.stride(0) == 1):
+        return t.data_ptr()
     _device_tensor(t, what, (torch.int32,), 1, index)
     if t.shape[0] != B or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 [%d]" % (what, B))
@@ -1053,6 +1058,18 @@ def lmhead_fp8(hidden: torch.Tensor, weight: torch.Tensor, weight_scale: torch.T
 # They take and make tensors as the calls above do.
 
 
+_no_heads = spec_heads_t()
+
+
+def _weight(w, what, dtype, D, index):
+    if w is None:
+        return None
+    _device_tensor(w, what, (dtype,) if dtype in _FLOATS else _FLOATS, 1, index)
+    if w.shape[0] != D or not w.is_contiguous():
+        raise ValueError("%s must be a contiguous [%d]" % (what, D))
+    return w.data_ptr()
+
+
 def norm_rotate(q: torch.Tensor | None, k: torch.Tensor | None, start: torch.Tensor, *,
                 eps: float | None = None, q_weight: torch.Tensor | None = None,
                 k_weight: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None,
@@ -1069,45 +1086,42 @@ def norm_rotate(q: torch.Tensor | None, k: torch.Tensor | None, start: torch.Ten
     [B|1][T] (tree_depths).  Returns (q, k) in out_dtype (default: the input's);
     rows past count[b] are zero.  ``out`` = (q, k) takes the results instead and
     keeps those rows; it may be the inputs themselves."""
-    B = T = D = index = dtype = None
-    heads = []
-    for t, what in ((q, "q"), (k, "k")):
-        if t is None:
-            heads.append(0)
-            continue
-        index = _device_tensor(t, what, _FLOATS if dtype is None else (dtype,), 4, index)
-        if dtype is not None and (t.shape[0], t.shape[1], t.shape[3]) != (B, T, D):
-            raise ValueError("q and k disagree on B, T or D")
-        B, T, h, D = t.shape
-        dtype = t.dtype
-        heads.append(h)
-        if h == 0:
-            raise ValueError("%s has no heads" % what)
-    if index is None:
+    lead = q if q is not None else k
+    if lead is None:
         raise ValueError("norm_rotate needs q or k")
+    index = _device_tensor(lead, "q" if q is not None else "k", _FLOATS, 4)
+    B, T, Hq, D = lead.shape
+    H, dtype = 0, lead.dtype
+    if q is None:
+        Hq, H = 0, Hq
+    elif k is not None:
+        _device_tensor(k, "k", (dtype,), 4, index)
+        H = k.shape[2]
+        if k.shape != (B, T, H, D):
+            raise ValueError("q and k disagree on B, T or D")
+    if (q is not None and Hq == 0) or (k is not None and H == 0):
+        raise ValueError("q and k must have heads")
     if start is None:
         raise ValueError("start is required")
     s = _per_sequence(start, "start", B, index)
     n = _per_sequence(count, "count", B, index)
-    dp, ds = _depths(depth, B, T, index)
-    rot = 0
+    dp, ds = _depths(depth, B, T, index) if depth is not None else (None, 0)
+    rot, fp = 0, None
     if inv_freq is not None:
         _device_tensor(inv_freq, "inv_freq", (torch.float32,), 1, index)
-        rot = 2 * inv_freq.shape[0]
+        rot, fp = 2 * inv_freq.shape[0], inv_freq.data_ptr()
         if rot == 0 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous float32 [rotated values / 2]")
-    if eps is None and (q_weight is not None or k_weight is not None):
-        raise ValueError("weights need eps")
-    weights, w_dtype = [], None
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is None:
-            weights.append(None)
-            continue
-        _device_tensor(w, what, _FLOATS if w_dtype is None else (w_dtype,), 1, index)
-        if w.shape[0] != D or not w.is_contiguous():
-            raise ValueError("%s must be a contiguous [%d]" % (what, D))
-        w_dtype = w.dtype
-        weights.append(w.data_ptr())
+    wq = wk = w_dtype = None
+    if q_weight is not None or k_weight is not None:
+        if eps is None:
+            raise ValueError("weights need eps")
+        w_dtype = (q_weight if q_weight is not None else k_weight).dtype
+        wq = _weight(q_weight, "q_weight", w_dtype, D, index)
+        wk = _weight(k_weight, "k_weight", w_dtype, D, index)
+    how = spec_rotate_t(D, rot, 1 if interleaved else 0, 0 if eps is None else 1,
+                        0.0 if eps is None else eps,
+                        SPEC_DTYPE_BF16 if w_dtype is torch.bfloat16 else SPEC_DTYPE_F32, wq, wk, fp, dp, ds)
     st, ctx = _on(index, stream)
     with ctx:
         if out is None:
@@ -1115,26 +1129,20 @@ def norm_rotate(q: torch.Tensor | None, k: torch.Tensor | None, start: torch.Ten
             if to not in _FLOATS:
                 raise TypeError("out_dtype must be float32 or bfloat16, got %s" % to)
             make = torch.empty if count is None else torch.zeros
-            out = [make(t.shape, dtype=to, device=t.device) if t is not None else None for t in (q, k)]
+            qo = make(q.shape, dtype=to, device=q.device) if Hq else None
+            ko = make(k.shape, dtype=to, device=k.device) if H else None
         else:
-            to = None
-            for t, o, what in zip((q, k), out, ("out[0]", "out[1]")):
-                if t is not None:
-                    _device_tensor(o, what, _FLOATS if to is None else (to,), 4, index)
-                    to = o.dtype
-        none = spec_heads_t()
-        ins = [_heads(t, what) if t is not None else none for t, what in ((q, "q"), (k, "k"))]
-        outs = [_heads(o, what, t.shape) if t is not None else none
-                for t, o, what in ((q, out[0], "out[0]"), (k, out[1], "out[1]"))]
-        how = spec_rotate_t(D, rot, int(bool(interleaved)), int(eps is not None),
-                            float(eps) if eps is not None else 0.0,
-                            SPEC_DTYPE_BF16 if w_dtype is torch.bfloat16 else SPEC_DTYPE_F32,
-                            weights[0], weights[1],
-                            inv_freq.data_ptr() if inv_freq is not None else None, dp, ds)
-        rc = lib().spec_norm_rotate(ins[0], outs[0], heads[0], ins[1], outs[1], heads[1],
+            qo, ko = out
+            if Hq:
+                _device_tensor(qo, "out[0]", _FLOATS, 4, index)
+            if H:
+                _device_tensor(ko, "out[1]", (qo.dtype,) if Hq else _FLOATS, 4, index)
+        none = _no_heads
+        rc = lib().spec_norm_rotate(_heads(q, "q") if Hq else none, _heads(qo, "out[0]", q.shape) if Hq else none, Hq,
+                                    _heads(k, "k") if H else none, _heads(ko, "out[1]", k.shape) if H else none, H,
                                     ctypes.byref(how), B, T, s, n, st)
     _check(rc, "spec_norm_rotate")
-    return tuple(out)
+    return qo, ko
 
 
 def attention_cache4_shared(q: torch.Tensor, pages: torch.Tensor, table: torch.Tensor,
@@ -1198,8 +1206,8 @@ def cache4_reserve(table: torch.Tensor, held: torch.Tensor, need: torch.Tensor,
     end, for one sequence after the other until one finds too few: it and all
     after it that miss pages keep what they hold (held[b] tells)."""
     index = _device_tensor(table, "table", (torch.int32,), 2)
-    cols, stride = _table(table, "table", table.shape[0], index)
     B = table.shape[0]
+    cols, stride = _table(table, "table", B, index)
     if held is None or need is None:
         raise ValueError("held and need are required")
     h = _per_sequence(held, "held", B, index)
@@ -1212,13 +1220,12 @@ def cache4_reserve(table: torch.Tensor, held: torch.Tensor, need: torch.Tensor,
         raise ValueError("free_count is required")
     L = lib()
     size = L.spec_cache4_reserve_workspace(B)
-    if size == 0:
-        _check(SPEC_ERR_UNSUPPORTED if B else SPEC_ERR_INVALID_ARG, "spec_cache4_reserve_workspace")
     st, ctx = _on(index, stream)
     with ctx:
-        ws = _scratch(workspace, table.device, size)
+        ws = _scratch(workspace, table.device, size) if size else None
         rc = L.spec_cache4_reserve(table.data_ptr(), stride, cols, h, w, B, free.data_ptr(),
-                                   free.shape[0], c, ws.data_ptr(), ws.numel() * ws.element_size(), st)
+                                   free.shape[0], c, ws.data_ptr() if size else None,
+                                   ws.numel() * ws.element_size() if size else 0, st)
     _check(rc, "spec_cache4_reserve")
 
 

@@ -137,7 +137,7 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
 }
 
 size_t spec_cache4_reserve_workspace(int32_t B) {
-  return B < 1 || B > kMaxB ? 0 : 256 + align256(size_t(B) * 8);
+  return B <= sv::kResFew || B > kMaxB ? 0 : 256 + align256(size_t(B) * 8);
 }
 
 int spec_cache4_reserve(int32_t* table, int64_t table_stride, int32_t table_cols, int32_t* held,
@@ -149,8 +149,8 @@ int spec_cache4_reserve(int32_t* table, int64_t table_stride, int32_t table_cols
     if (!p || !aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
   if (B < 1 || table_cols < 1 || table_stride < table_cols || free_capacity < 1) return SPEC_ERR_INVALID_ARG;
   if (B > kMaxB || table_cols > kMaxTableCols) return SPEC_ERR_UNSUPPORTED;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < spec_cache4_reserve_workspace(B))
-    return SPEC_ERR_WORKSPACE;
+  const size_t need_bytes = spec_cache4_reserve_workspace(B);
+  if (need_bytes && (!workspace || !aligned(workspace, 256) || workspace_bytes < need_bytes)) return SPEC_ERR_WORKSPACE;
   const sv::ReserveArgs A{table, table_stride, held, need, free_pages, free_count, table_cols, B, free_capacity};
   auto st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
