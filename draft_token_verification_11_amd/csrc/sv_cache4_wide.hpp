@@ -68,27 +68,36 @@ __device__ __forceinline__ C4Share c4_map_rows(const Args& A, C4Block K, int64_t
   if (kC4Prefix<Args> && K.compact) {
     if constexpr (kC4Prefix<Args>) {
       // the rows of the branches before, 64 branches at a time
-      auto chunk = [&](int32_t m0, int64_t upto, int64_t& first) {
+      auto chunk = [&](int32_t m0, int32_t upto, int32_t& first) {
         const int64_t mb = b * A.fan + m0 + lane;
-        const int32_t n = m0 + lane < A.fan && mb < A.seqs ? c4_live(A, mb) : 0;
-        const int64_t incl = upto + c4_prefix((int64_t)n * A.G, lane);
-        first = incl - (int64_t)n * A.G;
+        const int32_t rows = (m0 + lane < A.fan && mb < A.seqs ? c4_live(A, mb) : 0) * A.G;
+        int32_t incl = rows;  // rows of a prefix stay below 2^30
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const int32_t o = __shfl_up(incl, off);
+          if (lane >= off) incl += o;
+        }
+        incl += upto;
+        first = incl - rows;
         return incl;
       };
-      int64_t upto = 0, first = 0, incl = 0;
+      int32_t upto = 0, first = 0, incl = 0;
       for (int32_t m0 = 0; m0 < A.fan && upto < r0 + K.rows; m0 += 64) {
         incl = chunk(m0, upto, first);
-        upto = c4_lane(incl, 63);
+        upto = __builtin_amdgcn_readlane(incl, 63);
       }
-      const C4Share x = c4_wave_share<D>((int32_t)min(max(upto - r0, (int64_t)0), (int64_t)K.rows), w);
-      const int64_t lo = r0 + x.row0, hi = lo + 16 * x.mine;
+      const C4Share x = c4_wave_share<D>(min(max(upto - r0, 0), K.rows), w);
+      const int32_t lo = r0 + x.row0, hi = lo + 16 * x.mine;
       if (lane < 16 && x.mine) map[16 * x.mine - 16 + lane] = {-1, 0};  // past the last row
       upto = 0;
       for (int32_t m0 = 0; m0 < A.fan && upto < hi; m0 += 64) {
         if (A.fan > 64) incl = chunk(m0, upto, first);
-        for (int64_t r = max(first, lo); r < min(incl, hi); ++r)
-          map[r - lo] = {(int32_t)(b * A.fan + m0 + lane), (int32_t)((r - first) / A.G)};
-        upto = c4_lane(incl, 63);
+        int32_t r = max(first, lo), tok = (r - first) / A.G, left = A.G - (r - first - tok * A.G);
+        for (const int32_t end = min(incl, hi); r < end; ++r) {
+          map[r - lo] = {(int32_t)(b * A.fan) + m0 + lane, tok};
+          if (--left == 0) left = A.G, ++tok;
+        }
+        upto = __builtin_amdgcn_readlane(incl, 63);
       }
       return x;
     }

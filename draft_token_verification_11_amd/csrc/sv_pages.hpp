@@ -84,11 +84,22 @@ __device__ __forceinline__ bool res_plan(const ReserveArgs& A, ReservePlan& P, i
   const int32_t per = (A.B + kResThreads - 1) / kResThreads;
   const int32_t b0 = min(tid * per, A.B), b1 = min(b0 + per, A.B);
   int64_t give = 0, take = 0;
-  int32_t held = 0, want = 0;
-  for (int32_t b = b0; b < b1; ++b) {
-    res_pages(A, b, held, want);
-    give += max(held - want, 0);
-    take += max(want - held, 0);
+  // the first few stay in registers
+  constexpr int kKeep = 4;
+  int32_t held[kKeep] = {}, want[kKeep] = {};
+#pragma unroll
+  for (int x = 0; x < kKeep; ++x)
+    if (b0 + x < b1) res_pages(A, b0 + x, held[x], want[x]);
+#pragma unroll
+  for (int x = 0; x < kKeep; ++x) {
+    give += max(held[x] - want[x], 0);
+    take += max(want[x] - held[x], 0);
+  }
+  for (int32_t b = b0 + kKeep; b < b1; ++b) {
+    int32_t h, n;
+    res_pages(A, b, h, n);
+    give += max(h - n, 0);
+    take += max(n - h, 0);
   }
   const int64_t free0 = *A.free_count;
   int64_t give_at = c4_prefix(give, lane), take_at = c4_prefix(take, lane);
@@ -106,15 +117,22 @@ __device__ __forceinline__ bool res_plan(const ReserveArgs& A, ReservePlan& P, i
   P.full = free0 + P.gives;
   if (free0 < 0 || P.full > A.capacity) return false;
   int64_t most = 0;
-  for (int32_t b = b0; b < b1; ++b) {
-    if (per > 1) res_pages(A, b, held, want);
-    give_at += max(held - want, 0);
-    take_at += max(want - held, 0);
+  auto put = [&](int32_t b, int32_t h, int32_t n) {
+    give_at += max(h - n, 0);
+    take_at += max(n - h, 0);
     const bool served = take_at <= P.full;
     if (served) most = take_at;
     give_upto[b] = (int32_t)give_at;
     take_upto[b] = served ? (int32_t)take_at : 0x7FFFFFFF;
-    held_after[b] = want < held || served ? want : held;
+    held_after[b] = n < h || served ? n : h;
+  };
+#pragma unroll
+  for (int x = 0; x < kKeep; ++x)
+    if (b0 + x < b1) put(b0 + x, held[x], want[x]);
+  for (int32_t b = b0 + kKeep; b < b1; ++b) {
+    int32_t h, n;
+    res_pages(A, b, h, n);
+    put(b, h, n);
   }
   if (most) atomicMax(&used, (unsigned long long)most);
   __syncthreads();
@@ -157,20 +175,25 @@ struct SlotArgs {
   int32_t table_cols, n_pages, T;
 };
 
+constexpr int kSlotsPer = 4;
 __global__ __launch_bounds__(256) void k_cache4_slots(SlotArgs A) {
-  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (x >= A.tokens) return;
-  // as a rule all of it has 32 bits
-  const int64_t b = A.tokens >> 31 ? x / A.T : (uint32_t)x / (uint32_t)A.T;
-  const int32_t i = (int32_t)(x - b * A.T);
-  const C4View cache{nullptr, A.table, A.table_stride, A.n_pages, A.table_cols, 0};
-  const int32_t s = A.start[b], n = A.count ? A.count[b] : A.T;
-  int64_t slot = -1;
-  if (cache.fits(s, n, A.T) && i < n) {
-    const int32_t pos = s + i, page = cache.page(b, pos / kC4Page);
-    if (page >= 0) slot = (int64_t)page * kC4Page + pos % kC4Page;
+  // four tokens a thread, whose loads do not wait for each other
+#pragma unroll
+  for (int k = 0; k < kSlotsPer; ++k) {
+    const int64_t x = ((int64_t)blockIdx.x * kSlotsPer + k) * 256 + threadIdx.x;
+    if (x >= A.tokens) return;
+    // as a rule all of it has 32 bits
+    const int64_t b = A.tokens >> 31 ? x / A.T : (uint32_t)x / (uint32_t)A.T;
+    const int32_t i = (int32_t)(x - b * A.T);
+    const C4View cache{nullptr, A.table, A.table_stride, A.n_pages, A.table_cols, 0};
+    const int32_t s = A.start[b], n = A.count ? A.count[b] : A.T;
+    int64_t slot = -1;
+    if (cache.fits(s, n, A.T) && i < n) {
+      const int32_t pos = s + i, page = cache.page(b, pos / kC4Page);
+      if (page >= 0) slot = (int64_t)page * kC4Page + pos % kC4Page;
+    }
+    A.slots[x] = slot;
   }
-  A.slots[x] = slot;
 }
 
 }  // namespace sv

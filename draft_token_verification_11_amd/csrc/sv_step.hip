@@ -176,7 +176,7 @@ int spec_cache4_slots(const int32_t* table, int64_t table_stride, int32_t table_
     return SPEC_ERR_INVALID_ARG;
   if (table_cols < 1 || table_stride < table_cols || n_pages < 1) return SPEC_ERR_INVALID_ARG;
   if (table_cols > kMaxTableCols) return SPEC_ERR_UNSUPPORTED;
-  const int64_t tokens = int64_t(B) * T, blocks = (tokens + 255) / 256;
+  const int64_t tokens = int64_t(B) * T, blocks = (tokens + 256 * sv::kSlotsPer - 1) / (256 * sv::kSlotsPer);
   if (!grid_fits(blocks, 256)) return SPEC_ERR_UNSUPPORTED;
   const sv::SlotArgs A{table, table_stride, start, count, slots, tokens, table_cols, n_pages, T};
   auto st = static_cast<hipStream_t>(stream);
