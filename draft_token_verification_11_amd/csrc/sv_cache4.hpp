@@ -346,11 +346,15 @@ struct C4WindowArgs : C4AttnArgs {
 
 // Branches that share a prefix: `fan` sequences in a row have one, whose pages
 // `cache.table` names and whose length stands in `start`; B counts prefixes,
-// and the rows of one are those of all its branches, (branch, token, head).  Each row
-// of the call has a record: O [D], and maximum, sum and rounded sum.
+// and the rows of one are those of all its branches, (branch, token, head): with
+// `compact` (of 64 branches at most) of their live tokens only, so that branches
+// with few new tokens make fewer blocks.  Each row of the call has a record: O [D],
+// and maximum, sum and rounded sum.
 struct C4PrefixArgs : C4AttnArgs {
-  int32_t fan, seqs;  // branches of a prefix, sequences of the call
-  int32_t dim;        // D
+  int32_t fan, seqs;   // branches of a prefix, sequences of the call
+  int32_t dim;         // D
+  int32_t block_rows;  // rows of a block; row_blocks: blocks at most
+  int32_t compact;
   float* rec;         // [seqs][T][q_heads][D]
   float* stat;        // [seqs][T][q_heads][4]
 };
@@ -383,6 +387,40 @@ __host__ __device__ __forceinline__ C4Gap c4_gap(int32_t window, int32_t sinks, 
   const int32_t head = (int32_t)(((int64_t)(sinks < s + n ? sinks : s + n) + kC4Page - 1) / kC4Page);
   const int32_t keep = head < low ? head : low;
   return {keep, low - keep};
+}
+
+// Live tokens of a branch.
+__device__ __forceinline__ int32_t c4_live(const C4PrefixArgs& A, int64_t b) {
+  if (b >= A.seqs) return 0;
+  const int32_t n = A.count ? A.count[b] : A.T;
+  return n < 0 || n > A.T ? 0 : n;
+}
+// Rows of prefix g in a kv head, `compact`.
+template <bool UNIFORM>
+__device__ __forceinline__ int32_t c4_live_rows(const C4PrefixArgs& A, int64_t g) {
+  int32_t n = 0;
+  if constexpr (UNIFORM) {  // a branch a lane
+    const int lane = threadIdx.x & 63;
+    if (lane < A.fan) n = c4_live(A, g * A.fan + lane);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) n += __shfl_xor(n, off);
+    n = __builtin_amdgcn_readfirstlane(n);
+  } else {
+    for (int32_t m = 0; m < A.fan; ++m) n += c4_live(A, g * A.fan + m);
+  }
+  return n * A.G;
+}
+// Blocks of rows that sequence b has in a kv head.
+template <bool UNIFORM, typename Args>
+__device__ __forceinline__ int32_t c4_blocks(const Args& A, int64_t b) {
+  if constexpr (kC4Prefix<Args>)
+    if (A.compact) return (c4_live_rows<UNIFORM>(A, b) + A.block_rows - 1) / A.block_rows;
+  return A.row_blocks;
+}
+// The segments of a sequence are so many times those that its weight counts.
+template <typename Args>
+__device__ __forceinline__ int32_t c4_times(const Args& A) {
+  return kC4Prefix<Args> ? A.cache.heads : A.cache.heads * A.row_blocks;
 }
 
 // Pages of sequence b that its new tokens attend to; 0 when it has no rows.
@@ -447,15 +485,22 @@ __device__ __forceinline__ int64_t c4_lane(int64_t x, int l) {
   return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-// Weight of all sequences' segments (of one head and row block): a lane sums a
-// run of `per` sequences; `before`: the weight before its run.
+// A sequence's part of the weight of all: its segments', over c4_times.
+template <int COST = kC4SegCost, typename Args>
+__device__ __forceinline__ int64_t c4_seq_weight(const Args& A, int64_t b) {
+  bool bad;
+  const int64_t one = c4_weight<COST>(c4_pages<false>(A, b, bad));
+  if constexpr (kC4Prefix<Args>) return one * c4_blocks<false>(A, b);
+  return one;
+}
+// Weight of all sequences' segments, over c4_times: a lane sums a run of `per`
+// sequences; `before`: the weight before its run.
 template <int COST = kC4SegCost, typename Args>
 __device__ __forceinline__ int64_t c4_plan(const Args& A, int lane, int32_t per, int64_t& before) {
   int64_t sum = 0;
   for (int32_t j = 0; j < per; ++j) {
     const int64_t b = (int64_t)lane * per + j;
-    bool bad;
-    if (b < A.B) sum += c4_weight<COST>(c4_pages<false>(A, b, bad));
+    if (b < A.B) sum += c4_seq_weight<COST>(A, b);
   }
   const int64_t incl = c4_prefix(sum, lane);
   before = incl - sum;
@@ -471,8 +516,7 @@ __device__ __forceinline__ int64_t c4_find(const Args& A, int lane, int32_t per,
   if (per == 1) return run;
   for (int64_t b0 = (int64_t)run * per;; b0 += 64) {
     const int64_t b = b0 + lane;
-    bool bad;
-    const int64_t wt = b < A.B ? c4_weight<COST>(c4_pages<false>(A, b, bad)) : 0;
+    const int64_t wt = b < A.B ? c4_seq_weight<COST>(A, b) : 0;
     const int64_t incl = c4_prefix(wt, lane);
     const uint64_t past = __ballot(at + incl > x);
     if (past) {
@@ -882,6 +926,41 @@ __device__ __forceinline__ bool c4_row(const Args& A, int32_t h, int32_t r, int3
     return r < A.T * A.G && i < nnew;
   }
 }
+// The rows of a compact prefix: lane m has the rows of the branches up to and with m.
+template <typename Args>
+__device__ __forceinline__ int32_t c4_rows_upto(const Args& A, int64_t g, int lane) {
+  int32_t incl = 0;
+  if constexpr (kC4Prefix<Args>) {
+    if (!A.compact) return 0;
+    if (lane < A.fan) incl = c4_live(A, g * A.fan + lane) * A.G;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int32_t o = __shfl_up(incl, off);
+      if (lane >= off) incl += o;
+    }
+  }
+  return incl;
+}
+// c4_row where the rows may be a compact prefix's; by all lanes of a wave.
+template <typename Args>
+__device__ __forceinline__ bool c4_any_row(const Args& A, int32_t upto, int32_t h, int32_t r, int32_t nnew, int64_t& b,
+                                           int32_t& i, int32_t& head) {
+  if constexpr (kC4Prefix<Args>) {
+    if (A.compact) {
+      int32_t m = 0;  // branches whose rows end at r or before
+#pragma unroll
+      for (int step = 32; step; step >>= 1)
+        if (__shfl(upto, m + step - 1) <= r) m += step;
+      const int32_t last = __shfl(upto, 63), before = __shfl(upto, m ? m - 1 : 0);
+      const int32_t at = r - (m ? before : 0);
+      b = b * A.fan + m;
+      i = at / A.G;
+      head = h * A.G + (at - i * A.G);
+      return r < last;
+    }
+  }
+  return c4_row(A, h, r, nnew, b, i, head);
+}
 // Rows of a kv head.
 template <typename Args>
 __device__ __forceinline__ int32_t c4_rows(const Args& A) {
@@ -1035,7 +1114,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   const int n16 = lane & 15, q = lane >> 4;
   // every wave for itself: no barrier before the first loads
   const int32_t per = (A.B + 63) / 64;
-  const int32_t HR = A.cache.heads * A.row_blocks;
+  const int32_t HR = c4_times(A);
   int64_t before;
   const int64_t all = c4_plan(A, lane, per, before) * HR;  // weight of all segments
   const int64_t share = c4_share<Sh::kGrid>(all);
@@ -1055,19 +1134,22 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   int64_t b = c4_find(A, lane, per, before, c4_div(lo, HR), seq_at);
   bool bad;
   int32_t pages = c4_pages<true>(A, b, bad);
+  int32_t nb = c4_blocks<true>(A, b);
   int32_t hr = (int32_t)c4_div(lo - seq_at * HR, c4_weight(pages));
   int64_t seg = seq_at * HR + hr * c4_weight(pages);  // where it begins
   const int32_t R = c4_rows(A);
   for (; seg < hi; seg += c4_weight(pages), ++hr) {
-    if (hr == HR) {  // the next sequence with pages (seg is its begin)
-      do pages = c4_pages<true>(A, ++b, bad);
-      while (pages == 0);
+    if (hr == A.cache.heads * nb) {  // the next sequence with pages (seg is its begin)
+      do {
+        pages = c4_pages<true>(A, ++b, bad);
+        nb = c4_blocks<true>(A, b);
+      } while (pages == 0 || nb == 0);
       hr = 0;
     }
     int32_t p0 = c4_cut(lo - seg, pages), p1 = c4_cut(hi - seg, pages);
     if (!A.split) p0 = 0, p1 = seg < lo ? 0 : pages;  // whole, where it begins
     if (p0 == p1) continue;  // its pages are another workgroup's
-    const int32_t h = hr / A.row_blocks, r0 = hr % A.row_blocks * kRows;
+    const int32_t h = hr / nb, r0 = hr % nb * kRows;
     const int32_t s0 = c4_scalar(A.start + b);
     // a prefix has no new tokens of its own
     const int32_t nnew = kC4Prefix<Args> ? 0 : bad || !A.count ? A.T : c4_scalar(A.count + b);
@@ -1076,7 +1158,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
       if (!bad) gap = c4_gap(A.window, A.sinks, s0, nnew);
     auto place = [&](int32_t p) { return kC4Window<Args> && p >= gap.keep ? p + gap.skip : p; };
     if (p0 == 0 && p1 < pages) {
-      cut_b = (int32_t)b, cut_hr = hr, cut_new = nnew, cut_slot = seg > lo ? 1 : 0;
+      cut_b = (int32_t)b, cut_hr = h * A.row_blocks + hr % nb, cut_new = nnew, cut_slot = seg > lo ? 1 : 0;
       cut_parts = (int32_t)c4_div(seg + kC4SegCost + pages - 1, share) - blockIdx.x + 1;
     }
 
@@ -1108,13 +1190,14 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     constexpr int kQ = Sh::kQRegs ? D / 32 : D / 128;  // chunks a wave loads of a tile
     uint4 qx[RT][kQ];
     int32_t tok[RT];  // this lane's rows' tokens; T past the last row
+    const int32_t upto = c4_rows_upto(A, b, lane);
     int64_t low[RT];  // the first position that their windows reach, relative to start
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int32_t r = r0 + 16 * rt + n16;
       int64_t bb = b;
       int32_t i, head;
-      const bool live = c4_row(A, h, r, nnew, bb, i, head);
+      const bool live = c4_any_row(A, upto, h, r, nnew, bb, i, head);
       tok[rt] = r < R ? i : A.T;
       if constexpr (kC4Window<Args>) low[rt] = (int64_t)c4_depth(A, b, tok[rt]) - A.window + 1;
       const uint16_t* qp = A.q + bb * A.q_seq + i * A.q_pos + (int64_t)head * A.q_head;
@@ -1233,7 +1316,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
       }
       int64_t bb = b;
       int32_t i, head;
-      const bool live = c4_row(A, h, r0 + row, nnew, bb, i, head);
+      const bool live = c4_any_row(A, upto, h, r0 + row, nnew, bb, i, head);
 #pragma unroll
       for (int x = 0; x < D / kCols; ++x) {
         // the buffers in turn: one barrier a time
@@ -1323,7 +1406,7 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join(Args A) {
   const int32_t row = blockIdx.y * 4 + w, h = hr / A.row_blocks;
   int64_t bb = b;
   int32_t i, head;
-  if (!c4_row(A, h, hr % A.row_blocks * kRows + row, nnew, bb, i, head)) return;
+  if (!c4_any_row(A, c4_rows_upto(A, b, lane), h, hr % A.row_blocks * kRows + row, nnew, bb, i, head)) return;
   const float* rest = A.parts + (int64_t)blockIdx.x * 2 * kFloats;
   float m, l, n, v[E];
   c4_gather<D>(rest + slot * kFloats, rest, 2 * kFloats, kRows, row, 0, parts, lane, m, l, n, v);
@@ -1339,20 +1422,24 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join_long(Args A) {
   constexpr int64_t kFloats = C4Rec<D, RT>::kFloats;
   __shared__ float vs[4][D], ms[4], ls[4], ns[4];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int32_t per = (A.B + 63) / 64, HR = A.cache.heads * A.row_blocks;
-  const int32_t b = blockIdx.x / HR, hr = blockIdx.x % HR, row = blockIdx.y;
-  const int32_t h = hr / A.row_blocks;
+  const int32_t per = (A.B + 63) / 64, most = A.cache.heads * A.row_blocks, HR = c4_times(A);
+  const int32_t b = blockIdx.x / most, row = blockIdx.y;
+  const int32_t h = blockIdx.x % most / A.row_blocks, block = blockIdx.x % A.row_blocks;
   int64_t before;
   const int64_t share = c4_share<GRID>(c4_plan(A, lane, per, before) * HR);
   bool bad;
   int64_t at = c4_lane(before, b / per);
-  for (int32_t x = b / per * per; x < b; ++x) at += c4_weight(c4_pages<true>(A, x, bad));
+  for (int32_t x = b / per * per; x < b; ++x) {
+    const int64_t one = c4_weight(c4_pages<true>(A, x, bad));
+    at += kC4Prefix<Args> ? one * c4_blocks<true>(A, x) : one;
+  }
   const int32_t pages = c4_pages<true>(A, b, bad);
   const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
   int64_t bb = b;
   int32_t i, head;
-  if (pages == 0 || !c4_row(A, h, hr % A.row_blocks * kRows + row, nnew, bb, i, head)) return;
-  const int64_t seg = at * HR + hr * c4_weight(pages);
+  const int32_t upto = c4_rows_upto(A, b, lane), nb = c4_blocks<true>(A, b);
+  if (pages == 0 || block >= nb || !c4_any_row(A, upto, h, block * kRows + row, nnew, bb, i, head)) return;
+  const int64_t seg = at * HR + (h * nb + block) * c4_weight(pages);
   // the workgroups that hold its first and last page
   const int32_t w0 = (int32_t)c4_div(seg + kC4SegCost, share);
   const int32_t parts = (int32_t)c4_div(seg + kC4SegCost + pages - 1, share) - w0 + 1;

@@ -173,11 +173,10 @@ void launch_attention(Args& A, void* workspace, hipStream_t st) {
 }
 
 // The same for many rows of a kv head, whose pages the waves of a workgroup
-// share: rows of a block, and blocks.
+// share: rows of a block, and blocks.  Heads of 128 and 256 only.
 template <typename F>
 void with_wide(int32_t d, F f) {
-  if (d == 64) f(std::integral_constant<int, 64>());
-  else if (d == 128) f(std::integral_constant<int, 128>());
+  if (d == 128) f(std::integral_constant<int, 128>());
   else f(std::integral_constant<int, 256>());
 }
 void wide_blocks(int64_t rows, int32_t d, int32_t* block_rows, int64_t* blocks) {
@@ -187,6 +186,27 @@ void wide_blocks(int64_t rows, int32_t d, int32_t* block_rows, int64_t* blocks) 
     *block_rows = int32_t((t + *blocks - 1) / *blocks * 16);
   });
 }
+// Whether sharing pays for `rows` rows of a kv head, so many (sequence, kv head)
+// and pages of each at most (whole calls, us, without it and with it):
+//   heads of 64   hardly: 192 rows, 16 heads over 16,384 tokens 51 and 64; 168 rows,
+//                 32 x 8 heads through a window of 4,000 121 and 110, the best
+//   heads of 128  where there is a sequence and head for each workgroup, so that few
+//                 are cut: 64 x 8 heads over 2,048, 64 rows 77 and 81, 160 rows 175
+//                 and 162, 256 rows 269 and 238; through a window of 1,000, 168
+//                 rows 93 and 73; not 8 x 8 heads over 16,384, 160 rows 155 and 195
+//   heads of 256  where its workgroups have some pages each, for they are half as
+//                 many: 16 x 4 heads through a window of 4,000, 168 rows 123 and 98;
+//                 4 x 4 heads, 378 rows, over 8,192 105 and 97, over 2,048 52 and 65;
+//                 40 rows, 8 x 4 heads, window of 8,000 45 and 48
+bool wide_rows(int64_t rows, int32_t d) { return d == 128 ? rows > 96 : d == 256 && rows > 64; }
+bool wide_pays(int64_t rows, int32_t d, int64_t seqs_heads, int64_t pages) {
+  if (!wide_rows(rows, d)) return false;
+  if (d == 128) return seqs_heads >= sv::C4Wide<128>::kGrid;
+  int32_t block_rows;
+  int64_t blocks;
+  wide_blocks(rows, d, &block_rows, &blocks);
+  return seqs_heads * blocks >= (16 * sv::C4Wide<256>::kGrid + pages - 1) / pages;
+}
 size_t wide_workspace(int32_t d) {
   size_t bytes = 0;
   with_wide(d, [&](auto D) {
@@ -194,30 +214,19 @@ size_t wide_workspace(int32_t d) {
   });
   return bytes;
 }
-// Rows of a kv head that take more than one block of the other kernel are worth
-// this one where its workgroups have so many pages each: its ends cost more.
-constexpr int64_t kWidePages = 16;
-bool wide_pays(int64_t rows, int32_t d, int64_t seqs_heads, int64_t pages) {
-  if (rows <= 16 * max_tiles(d)) return false;
-  int32_t block_rows;
-  int64_t blocks, grid = 0;
-  wide_blocks(rows, d, &block_rows, &blocks);
-  with_wide(d, [&](auto D) { grid = sv::C4Wide<D>::kGrid; });
-  return seqs_heads * blocks >= (kWidePages * grid + pages - 1) / pages;
-}
 template <int D, typename Args>
-void launch_wide(Args& A, sv::C4Block K, void* workspace, hipStream_t st) {
+void launch_wide(Args& A, int32_t block_rows, void* workspace, hipStream_t st) {
   using Sh = sv::C4Wide<D>;
   constexpr int kGrid = Sh::kGrid;
   A.cuts = static_cast<sv::C4Cut*>(workspace);
   A.parts = reinterpret_cast<float*>(A.cuts + kGrid);
-  hipLaunchKernelGGL((sv::k_attention_cache4_wide<D, Args>), dim3(kGrid), dim3(64 * Sh::kWaves), 0, st, A, K);
+  hipLaunchKernelGGL((sv::k_attention_cache4_wide<D, Args>), dim3(kGrid), dim3(64 * Sh::kWaves), 0, st, A, block_rows);
   if (!A.split) return;
-  const dim3 grid{unsigned(kGrid), unsigned(K.rows / 16)};
+  const dim3 grid{unsigned(kGrid), unsigned(block_rows / 16)};
   if (int64_t(A.B) * A.cache.heads * A.row_blocks <= kAttnFew)
-    hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 4, Args>), grid, dim3(1024), 0, st, A, K);
+    hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 4, Args>), grid, dim3(1024), 0, st, A, block_rows);
   else
-    hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 1, Args>), grid, dim3(256), 0, st, A, K);
+    hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 1, Args>), grid, dim3(256), 0, st, A, block_rows);
 }
 
 // Arguments of an attention call, checked, and its row tiles.

@@ -16,7 +16,8 @@ namespace sv {
 // wave then reads, while the page before is attended to.
 template <int D>
 struct C4Wide {
-  static constexpr int RT = D == 256 ? 1 : D == 128 ? 3 : 4;
+  static_assert(D == 128 || D == 256, "heads of 64 gain nothing by it");
+  static constexpr int RT = D == 256 ? 1 : 3;
   static constexpr int kWaves = D == 256 ? 8 : 4;
   static constexpr int kTiles = kWaves * RT, kRows = 16 * kTiles;  // of a block at most
   static constexpr int kPerCu = 8 / kWaves;                        // workgroups a compute unit: two waves a SIMD
@@ -26,18 +27,6 @@ struct C4Wide {
   // A cut segment: O [kRows][D], m, l, n [kRows], and what the rows are.
   static constexpr int64_t kFloats = kRows * (D + 5);
 };
-struct C4Block {
-  int32_t rows;     // of a block: 16 a tile
-  int32_t compact;  // prefixes: a block's rows are those of the branches' live tokens
-};
-
-// Live tokens of branch b of a prefix.
-template <typename Args>
-__device__ __forceinline__ int32_t c4_live(const Args& A, int64_t b) {
-  const int32_t n = A.count ? A.count[b] : A.T;
-  return n < 0 || n > A.T ? 0 : n;
-}
-
 // What a row is: its sequence (-1: none) and token.
 struct C4RowMap {
   int32_t seq, tok;
@@ -60,54 +49,22 @@ __device__ __forceinline__ C4Share c4_wave_share(int32_t rows, int w) {
   x.row0 = 16 * (x.tiles / W * v + min(v, x.tiles % W));
   return x;
 }
-// Finds a wave's rows in the block whose first row is r0, and puts down what
-// they are.
+// Finds a wave's rows in the block of `rows` rows whose first one is r0, and puts
+// down what they are.
 template <int D, typename Args>
-__device__ __forceinline__ C4Share c4_map_rows(const Args& A, C4Block K, int64_t b, int32_t r0, int32_t nnew, int w, int lane,
-                                               C4RowMap* map) {
-  if (kC4Prefix<Args> && K.compact) {
-    if constexpr (kC4Prefix<Args>) {
-      // the rows of the branches before, 64 branches at a time
-      auto chunk = [&](int32_t m0, int32_t upto, int32_t& first) {
-        const int64_t mb = b * A.fan + m0 + lane;
-        const int32_t rows = (m0 + lane < A.fan && mb < A.seqs ? c4_live(A, mb) : 0) * A.G;
-        int32_t incl = rows;  // rows of a prefix stay below 2^30
+__device__ __forceinline__ C4Share c4_map_rows(const Args& A, int32_t rows, int64_t b, int32_t r0, int32_t nnew, int w,
+                                               int lane, C4RowMap* map) {
+  const int32_t upto = c4_rows_upto(A, b, lane);
+  int32_t all = c4_rows(A);
+  if constexpr (kC4Prefix<Args>)
+    if (A.compact) all = __builtin_amdgcn_readlane(upto, 63);
+  const C4Share x = c4_wave_share<D>(min(max(all - r0, 0), rows), w);
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-          const int32_t o = __shfl_up(incl, off);
-          if (lane >= off) incl += o;
-        }
-        incl += upto;
-        first = incl - rows;
-        return incl;
-      };
-      int32_t upto = 0, first = 0, incl = 0;
-      for (int32_t m0 = 0; m0 < A.fan && upto < r0 + K.rows; m0 += 64) {
-        incl = chunk(m0, upto, first);
-        upto = __builtin_amdgcn_readlane(incl, 63);
-      }
-      const C4Share x = c4_wave_share<D>(min(max(upto - r0, 0), K.rows), w);
-      const int32_t lo = r0 + x.row0, hi = lo + 16 * x.mine;
-      if (lane < 16 && x.mine) map[16 * x.mine - 16 + lane] = {-1, 0};  // past the last row
-      upto = 0;
-      for (int32_t m0 = 0; m0 < A.fan && upto < hi; m0 += 64) {
-        if (A.fan > 64) incl = chunk(m0, upto, first);
-        int32_t r = max(first, lo), tok = (r - first) / A.G, left = A.G - (r - first - tok * A.G);
-        for (const int32_t end = min(incl, hi); r < end; ++r) {
-          map[r - lo] = {(int32_t)(b * A.fan) + m0 + lane, tok};
-          if (--left == 0) left = A.G, ++tok;
-        }
-        upto = __builtin_amdgcn_readlane(incl, 63);
-      }
-      return x;
-    }
-  }
-  const C4Share x = c4_wave_share<D>(min(max(c4_rows(A) - r0, 0), K.rows), w);
-  for (int32_t r = lane; r < 16 * x.mine; r += 64) {
+  for (int r = 0; r < 16 * C4Wide<D>::RT; r += 64) {
     int64_t bb = b;
     int32_t i = 0, head;
-    const bool live = c4_row(A, 0, r0 + x.row0 + r, nnew, bb, i, head);
-    map[r] = {live ? (int32_t)bb : -1, i};
+    const bool live = c4_any_row(A, upto, 0, r0 + x.row0 + r + lane, nnew, bb, i, head);
+    if (r + lane < 16 * x.mine) map[r + lane] = {live ? (int32_t)bb : -1, i};
   }
   return x;
 }
@@ -117,20 +74,12 @@ __device__ __forceinline__ C4Share c4_map_rows(const Args& A, C4Block K, int64_t
 // in a sixteenth of D.  With eight waves two have a tile, and half of each lane's.
 template <int D>
 struct C4Codes {
-  static constexpr int W = D == 256 ? 4 : D / 32;  // dwords of keys, and of values
-  uint32_t k[W], v[W];
-  uint32_t ke, ve;
+  uint32_t k[4], v[4], ke, ve;
 };
 
-template <int W>
-__device__ __forceinline__ void c4_load_dwords(const uint8_t* p, uint32_t (&x)[W]) {
-  if constexpr (W == 2) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    x[0] = a.x, x[1] = a.y;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  }
+__device__ __forceinline__ void c4_load_dwords(const uint8_t* p, uint32_t (&x)[4]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
 }
 
 // Where a thread's values stand: its tile of 16 tokens and, of it, the four, in
@@ -170,7 +119,7 @@ __device__ __forceinline__ void c4_load_values(const uint8_t* rec, int w, int la
 // values [2 pairs of tiles][D / 16][64 lanes], 16 bytes each.
 template <int D>
 __device__ __forceinline__ void c4_convert_keys(const C4Codes<D>& R, int w, int lane, uint8_t* keys) {
-  constexpr int NG = D / 32, N = C4Codes<D>::W;
+  constexpr int NG = D / 32, N = 4;
   const float sc = __uint_as_float(((R.ke >> (8 * (w & 3))) & 0xFFu) << 23);
   uint8_t* const to = keys + (((w & 3) * NG + N * (w >> 2)) * 64 + lane) * 16;
 #pragma unroll
@@ -187,7 +136,7 @@ __device__ __forceinline__ void c4_convert_keys(const C4Codes<D>& R, int w, int 
 // exponent of 1.
 template <int D>
 __device__ __forceinline__ void c4_convert_values(C4Codes<D>& R, int w, int lane, int have, uint8_t* values) {
-  constexpr int N = C4Codes<D>::W;  // bytes of a token's values here
+  constexpr int N = 4;  // bytes of a token's values here
   const C4ValuePlace V = c4_value_place(w, lane);
   if (have < 64) {
     const int left = have - 16 * V.tile - 4 * V.quad;  // of the four
@@ -195,8 +144,7 @@ __device__ __forceinline__ void c4_convert_values(C4Codes<D>& R, int w, int lane
     for (int j = 0; j < 4; ++j)
       if (j >= left) {
         R.ve = (R.ve & ~(0xFFu << (8 * j))) | (127u << (8 * j));
-        if constexpr (D == 64) R.v[j / 2] &= j % 2 ? 0xFFFFu : 0xFFFF0000u;
-        else R.v[j] = 0u;
+        R.v[j] = 0u;
       }
   }
   float sc[4];
@@ -477,7 +425,7 @@ __device__ __forceinline__ void c4_wide_run(const Args& A, C4Segment G, uint8_t 
 }
 
 template <int D, typename Args>
-__global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_attention_cache4_wide(Args A, C4Block K) {
+__global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_attention_cache4_wide(Args A, int32_t block_rows) {
   using Sh = C4Wide<D>;
   __shared__ __attribute__((aligned(16))) uint8_t pagebuf[2][2][Sh::kKeys];
   __shared__ C4RowMap maps[Sh::kWaves][16 * Sh::RT];
@@ -485,7 +433,7 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
 
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int32_t per = (A.B + 63) / 64;
-  const int32_t HR = A.cache.heads * A.row_blocks;
+  const int32_t HR = c4_times(A);
   int64_t before;
   const int64_t all = c4_plan<Sh::kCost>(A, lane, per, before) * HR;  // weight of all segments
   const int64_t share = c4_share<Sh::kGrid, Sh::kCost>(all);
@@ -504,19 +452,22 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
   G.b = c4_find<Sh::kCost>(A, lane, per, before, c4_div(lo, HR), seq_at);
   bool bad;
   G.pages = c4_pages<true>(A, G.b, bad);
+  int32_t nb = c4_blocks<true>(A, G.b);
   int32_t hr = (int32_t)c4_div(lo - seq_at * HR, c4_weight<Sh::kCost>(G.pages));
   int64_t seg = seq_at * HR + hr * c4_weight<Sh::kCost>(G.pages);  // where it begins
   for (; seg < hi; seg += c4_weight<Sh::kCost>(G.pages), ++hr) {
-    if (hr == HR) {  // the next sequence with pages (seg is its begin)
-      do G.pages = c4_pages<true>(A, ++G.b, bad);
-      while (G.pages == 0);
+    if (hr == A.cache.heads * nb) {  // the next sequence with pages (seg is its begin)
+      do {
+        G.pages = c4_pages<true>(A, ++G.b, bad);
+        nb = c4_blocks<true>(A, G.b);
+      } while (G.pages == 0 || nb == 0);
       hr = 0;
     }
     G.p0 = c4_cut<Sh::kCost>(lo - seg, G.pages), G.p1 = c4_cut<Sh::kCost>(hi - seg, G.pages);
     if (!A.split) G.p0 = 0, G.p1 = seg < lo ? 0 : G.pages;  // whole, where it begins
     if (G.p0 == G.p1) continue;  // its pages are another workgroup's
-    G.h = hr / A.row_blocks;
-    G.r0 = hr % A.row_blocks * K.rows;
+    G.h = hr / nb;
+    G.r0 = hr % nb * block_rows;
     G.s0 = c4_scalar(A.start + G.b);
     G.nnew = kC4Prefix<Args> ? 0 : bad || !A.count ? A.T : c4_scalar(A.count + G.b);
     G.gap = C4Gap{0, 0};
@@ -538,11 +489,11 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
       c4_load_keys<D>(rec, w, lane, codes);
       c4_load_values<D>(rec, w, lane, codes);
     }
-    const C4Share W = c4_map_rows<D>(A, K, G.b, G.r0, G.nnew, w, lane, maps[w]);
+    const C4Share W = c4_map_rows<D>(A, block_rows, G.b, G.r0, G.nnew, w, lane, maps[w]);
     const int32_t tiles = __builtin_amdgcn_readfirstlane(W.tiles);
     if (tiles == 0) continue;
     if (G.p0 == 0 && G.p1 < G.pages) {
-      cut_b = (int32_t)G.b, cut_hr = hr, cut_new = tiles, cut_slot = seg > lo ? 1 : 0;
+      cut_b = (int32_t)G.b, cut_hr = G.h * A.row_blocks + hr % nb, cut_new = tiles, cut_slot = seg > lo ? 1 : 0;
       cut_parts = (int32_t)c4_div(seg + Sh::kCost + G.pages - 1, share) - blockIdx.x + 1;
     }
     const int32_t mine = __builtin_amdgcn_readfirstlane(W.mine), row0 = __builtin_amdgcn_readfirstlane(W.row0);
@@ -555,9 +506,8 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
     };
     if (mine == 0) run(std::integral_constant<int, 0>());
     else if (mine == 1) run(std::integral_constant<int, 1>());
-    if constexpr (Sh::RT >= 2) if (mine == 2) run(std::integral_constant<int, 2>());
-    if constexpr (Sh::RT >= 3) if (mine == 3) run(std::integral_constant<int, 3>());
-    if constexpr (Sh::RT >= 4) if (mine == 4) run(std::integral_constant<int, 4>());
+    else if (mine == 2) run(std::integral_constant<int, Sh::RT >= 2 ? 2 : 0>());
+    else run(std::integral_constant<int, Sh::RT >= 3 ? 3 : 0>());
   }
   note();
 }
@@ -566,7 +516,7 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
 // workgroup blockIdx.x of the attention began.  Sixteen threads hold a row's
 // columns, four in each 64; SHARE times as many share its records.
 template <int D, int SHARE, typename Args>
-__global__ __launch_bounds__(256 * SHARE) void k_attention_cache4_wide_join(Args A, C4Block K) {
+__global__ __launch_bounds__(256 * SHARE) void k_attention_cache4_wide_join(Args A, int32_t block_rows) {
   using Sh = C4Wide<D>;
   constexpr int E = D / 16, N = 4;  // columns of a thread; records under way at a time
   __shared__ float vs[SHARE > 1 ? SHARE : 1][SHARE > 1 ? 16 : 1][SHARE > 1 ? D + 1 : 1], st[SHARE][3][16];
@@ -629,7 +579,7 @@ __global__ __launch_bounds__(256 * SHARE) void k_attention_cache4_wide_join(Args
     }
   }
   if (seq < 0) return;
-  const int32_t head = c4_head(A, hr / A.row_blocks, hr % A.row_blocks * K.rows + row);
+  const int32_t head = c4_head(A, hr / A.row_blocks, hr % A.row_blocks * block_rows + row);
 #pragma unroll
   for (int e = 0; e < E; e += 4) c4_finish<4>(A, seq, tok, head, 16 * e + 4 * grp, v + e, m, l, n);
 }

@@ -24,17 +24,20 @@ struct PrefixShape {
   int32_t block_rows;  // wide: rows of a block
   int64_t blocks;
 };
-PrefixShape prefix_shape(int64_t rows, int32_t d, int64_t prefixes_heads, int64_t cols) {
+PrefixShape prefix_shape(int64_t rows, int32_t d, int64_t prefixes_heads, int64_t cols, bool compact) {
   PrefixShape x{};
-  x.wide = wide_pays(rows, d, prefixes_heads, cols);
+  // `rows` are far more than the live ones where those are counted through; heads of
+  // 128 then gain nothing by wide blocks (64 x 8 heads, 96 of 160 rows live: 185 us
+  // and 190)
+  x.wide = wide_pays(rows, d, prefixes_heads, cols) && !(compact && d == 128);
   if (x.wide) wide_blocks(rows, d, &x.block_rows, &x.blocks);
   else row_blocks(rows, d, &x.tiles, &x.blocks);
   return x;
 }
 // Pages of a branch's own up to which a wave goes through them by itself.
 constexpr int32_t kShortCols = 8;
-// Branches up to which their live rows are counted through.
-constexpr int32_t kCompactFan = 4096;
+// Branches up to which their live rows are counted through: one a lane.
+constexpr int32_t kCompactFan = 64;
 
 // A call's workspace: the rows' records, and one attention's after the other.
 // Its size does not go by the tables, of which a size query knows nothing.
@@ -48,7 +51,7 @@ SharedSpace shared_space(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads
   int tiles;
   int64_t blocks;
   row_blocks(rows, d, &tiles, &blocks);
-  const size_t prefix = std::max(shape_workspace(d, tiles), rows > 16 * max_tiles(d) ? wide_workspace(d) : 0);
+  const size_t prefix = std::max(shape_workspace(d, tiles), wide_rows(rows, d) ? wide_workspace(d) : 0);
   return {align256(count * size_t(d) * 4), align256(count * 16),
           std::max(attention_workspace(T, q_heads, kv_heads, d), prefix)};
 }
@@ -85,7 +88,9 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
   if ((rc = check_cache(prefix)) != SPEC_OK) return rc;
   if (!prefix_len || !aligned(prefix_len, 4)) return SPEC_ERR_INVALID_ARG;
   const int32_t d = cache.head_dim, each = std::min(fan, B), prefixes = (B + each - 1) / each;
-  const PrefixShape shape = prefix_shape(int64_t(each) * T * (q_heads / cache.heads), d, int64_t(prefixes) * cache.heads, prefix_cols);
+  const bool compact = count && each <= kCompactFan;
+  const PrefixShape shape = prefix_shape(int64_t(each) * T * (q_heads / cache.heads), d, int64_t(prefixes) * cache.heads, prefix_cols,
+                                         compact);
   if (prefixes * (int64_t(prefix_cols) + sv::kC4SegCost) * cache.heads >= (int64_t(1) << 40) / shape.blocks)
     return SPEC_ERR_UNSUPPORTED;
   const SharedSpace space = shared_space(B, T, q_heads, cache.heads, d, fan);
@@ -100,6 +105,8 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
   P.start = prefix_len;
   P.B = prefixes;
   P.row_blocks = int32_t(shape.blocks);
+  P.block_rows = shape.wide ? shape.block_rows : 16 * shape.tiles;
+  P.compact = compact;
   P.split = prefix_cols > kAttnWhole;
   P.fan = each;
   P.seqs = B;
@@ -113,8 +120,7 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
   O.stat = stat;
   auto st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  const sv::C4Block K{shape.block_rows, count && each <= kCompactFan};
-  if (shape.wide) with_wide(d, [&](auto D) { launch_wide<D>(P, K, scratch, st); });
+  if (shape.wide) with_wide(d, [&](auto D) { launch_wide<D>(P, P.block_rows, scratch, st); });
   else with_shape(d, shape.tiles, [&](auto D, auto RT) { launch_attention<D, RT>(P, scratch, st); });
   const int64_t waves = int64_t(B) * cache.heads * O.row_blocks;
   if (cache.table_cols <= kShortCols && grid_fits((waves + 3) / 4, 256))

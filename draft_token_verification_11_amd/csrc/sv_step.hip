@@ -55,7 +55,7 @@ int launch_rotate(sv::RotateArgs& A, hipStream_t st) {
 
 // Scratch of either kernel that a window may take.
 size_t window_workspace(int32_t T, int32_t q_heads, int32_t kv_heads, int32_t d) {
-  const bool many = int64_t(T) * (q_heads / kv_heads) > 16 * max_tiles(d);
+  const bool many = wide_rows(int64_t(T) * (q_heads / kv_heads), d);
   return std::max(attention_workspace(T, q_heads, kv_heads, d), many ? wide_workspace(d) : size_t(0));
 }
 
@@ -125,11 +125,11 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
   const int64_t rows = int64_t(T) * A.G;
   (void)hipGetLastError();
   if (wide_pays(rows, d, int64_t(B) * cache.heads, std::min<int64_t>(pages, cache.table_cols))) {
-    sv::C4Block K{0, 0};
+    int32_t block_rows;
     int64_t blocks;
-    wide_blocks(rows, d, &K.rows, &blocks);
+    wide_blocks(rows, d, &block_rows, &blocks);
     A.row_blocks = int32_t(blocks);
-    with_wide(d, [&](auto D) { launch_wide<D>(A, K, workspace, st); });
+    with_wide(d, [&](auto D) { launch_wide<D>(A, block_rows, workspace, st); });
   } else {
     with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(A, workspace, st); });
   }
