@@ -13,18 +13,21 @@ DEV = "cuda:0"
 
 
 def _case(seed, B, fan, T, Hq, H, D, start, prefix, slack=0):
-    """q, a pool of random values, the branches' tables and their prefixes'."""
+    """q, a pool of random values, the branches' tables and their prefixes', `slack` columns wider
+    than they need be."""
     rs = np.random.default_rng([seed, B, T, Hq, D])
-    P = max(1, -(-(max(start) + T) // 64)) + slack
-    PP = max(1, -(-max(prefix) // 64)) + slack
+    P = max(1, -(-(max(start) + T) // 64))
+    PP = max(1, -(-max(prefix) // 64))
     n = B * P + len(prefix) * PP + 2
     order = rs.permutation(n).astype(np.int32)
     table, ptable = order[: B * P].reshape(B, P), order[B * P: B * P + len(prefix) * PP].reshape(-1, PP)
     pages = sv.cache4_alloc(n, H, D, DEV)
-    k, v = (torch.tensor(rs.normal(0, 1, (1, n * 64, H, D)), dtype=torch.float32, device=DEV) for _ in range(2))
+    g = torch.Generator(DEV).manual_seed(seed + B)
+    k, v = (torch.randn(1, n * 64, H, D, generator=g, device=DEV) for _ in range(2))
     sv.cache4_write(pages, _i32([list(range(n))]), _i32([0]), k, v)
-    q = torch.tensor(rs.normal(0, 1, (B, T, Hq, D)), dtype=torch.float32).bfloat16().to(DEV)
-    return q, pages, table.copy(), ptable.copy()
+    q = torch.randn(B, T, Hq, D, generator=g, device=DEV).bfloat16()
+    table, ptable = (np.concatenate([x, np.full((len(x), slack), -1, np.int32)], 1) for x in (table, ptable))
+    return q, pages, table, ptable
 
 
 def _run(q, pages, table, start, ptable, prefix, fan, count=None, **kw):
@@ -169,6 +172,108 @@ def test_many_rows_and_long_prefixes(D, B, fan, T, Hq, H, prefix):
     got = _run(q, pages, table, start, ptable, prefix, fan)
     _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: (b * 7 + i * 3 + h) % 11 == 0)
     assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+
+
+# Shapes whose pages the waves of a workgroup share: heads of 128 with more than 96 rows and 512
+# (prefix, kv head) pairs, heads of 256 with more than 64 rows and wide tables.  (B, fan, T, Hq, H, D,
+# slack of the tables: wide ones are cut, and whole ones not)
+SHARED = [(104, 13, 2, 256, 64, 128, 0), (103, 13, 2, 256, 64, 128, 21), (40, 5, 9, 256, 64, 128, 21),
+          (70, 7, 5, 192, 64, 128, 0), (12, 6, 9, 14, 2, 256, 400), (7, 7, 3, 8, 2, 256, 2200), (9, 3, 22, 8, 8, 256, 200),
+          (24, 2, 17, 128, 64, 256, 5)]
+
+
+@pytest.mark.parametrize("B,fan,T,Hq,H,D,slack", SHARED)
+def test_shared_pages(B, fan, T, Hq, H, D, slack):
+    n = -(-B // fan)
+    start = [(b * 23) % 90 for b in range(B)]
+    prefix = [(0, 1, 64, 65, 97, 127, 128, 190)[(g * 5 + 3) % 8] for g in range(n)]
+    q, pages, table, ptable = _case(11, B, fan, T, Hq, H, D, start, prefix, slack)
+    got = _run(q, pages, table, start, ptable, prefix, fan)
+    _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: (b * 7 + i * 5 + h) % 61 == 0)
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+    again = _run(q, pages, table, start, ptable, prefix, fan)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("B,fan,T,Hq,H,D,slack", [(12, 6, 9, 14, 2, 256, 400), (18, 6, 9, 14, 2, 128, 21)])
+def test_shared_pages_of_live_rows(B, fan, T, Hq, H, D, slack):
+    """Fewer new tokens than columns: rows of one tile up to all, none at all, and counts that fit no
+    call, whose sequences are NaN and whose neighbours are not."""
+    n = -(-B // fan)
+    start, prefix = [(b * 23) % 90 for b in range(B)], [130 - g for g in range(n)]
+    q, pages, table, ptable = _case(12, B, fan, T, Hq, H, D, start, prefix, slack)
+    for counts in ([(b * 5) % (T + 1) for b in range(B)], [1] + [0] * (B - 1), [0] * B, [T] * B,
+                   [T + 1, -1, 3, 0, T, 1] * (B // 6)):
+        got = _run(q, pages, table, start, ptable, prefix, fan, counts)
+        _check(q, pages, table, start, ptable, prefix, fan, got, counts, rows=lambda b, i, h: (b + i + h) % 7 == 0)
+
+
+@pytest.mark.parametrize("fan,D", [(64, 64), (65, 64), (64, 256), (65, 128)])
+def test_counts_around_64_branches(fan, D):
+    """Live rows are counted through up to 64 branches; above that all rows have their place."""
+    B, T, start, prefix = 2 * fan - 3, 3, [7] * (2 * fan - 3), [200, 66]
+    counts = [(b * 7) % 4 for b in range(B)]
+    q, pages, table, ptable = _case(13, B, fan, T, 4, 1, D, start, prefix, slack=21)
+    got = _run(q, pages, table, start, ptable, prefix, fan, counts)
+    _check(q, pages, table, start, ptable, prefix, fan, got, counts, rows=lambda b, i, h: (b + i + h) % 5 == 0)
+
+
+@pytest.mark.parametrize("case", [(104, 13, 2, 256, 64, 128), (24, 6, 9, 14, 2, 256)])
+def test_shared_pages_bad_ones_and_noise(case):
+    """An ill-formed prefix, a page outside the pool, noise behind a prefix's end and a NaN in one."""
+    B, fan, T, Hq, H, D = case
+    n = -(-B // fan)
+    prefix, start = ([70, 1 << 20, 130, 70] + [70] * n)[:n], [5] * B
+    q, pages, table, ptable = _case(14, B, fan, T, Hq, H, D, start, [130] * n, 400 if D == 256 else 0)
+    ptable[2, 1] = -3
+    raw = pages.cpu().numpy()
+    for x in range(70, 128):
+        for at in low.offsets(x % 64, D):
+            raw[ptable[0, 1], :, at] = 255
+    pages = torch.from_numpy(raw).to(DEV)
+    if n > 3:
+        k = torch.zeros(1, 1, H, D, device=DEV)
+        k[0, 0, 1, 0] = float("nan")
+        sv.cache4_write(pages, _i32(ptable[3:4]), _i32([69]), k, torch.ones_like(k))
+    got = _run(q, pages, table, start, ptable, prefix, fan)
+    nan = torch.isnan(got[0]).any(-1).cpu()
+    want = torch.zeros(B, T, Hq, dtype=torch.bool)
+    want[fan: 3 * fan] = True
+    want[3 * fan: 4 * fan, :, Hq // H: 2 * (Hq // H)] = True
+    assert torch.equal(nan, want) and torch.equal(torch.isnan(got[1]).cpu(), want)
+    _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: (b + i + h) % 53 == 0)
+
+
+def test_captured_with_shared_pages():
+    B, fan, T, Hq, H, D = 104, 13, 2, 256, 64, 128
+    start, prefix = [3] * B, [100 + g for g in range(8)]
+    q, pages, table, ptable = _case(15, B, fan, T, Hq, H, D, start, prefix, 21)
+    args = [q, pages, _i32(table), _i32(start), _i32(ptable), _i32(prefix)]
+    want = sv.attention_cache4_shared(*args, fan=fan, return_lse=True)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = sv.attention_cache4_shared(*args, fan=fan, return_lse=True)
+    for _ in range(4):
+        got[0].zero_()
+        got[1].zero_()
+        g.replay()
+        other = sv.attention_cache4_shared(*args, fan=fan, return_lse=True)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) and torch.equal(z, y) for x, y, z in zip(got, want, other))
+
+
+def test_another_stream():
+    B, fan, T, Hq, H, D = 6, 3, 2, 8, 2, 64
+    start, prefix = [9] * B, [100, 64]
+    q, pages, table, ptable = _case(16, B, fan, T, Hq, H, D, start, prefix)
+    args = [q, pages, _i32(table), _i32(start), _i32(ptable), _i32(prefix)]
+    want = sv.attention_cache4_shared(*args, fan=fan)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = sv.attention_cache4_shared(*args, fan=fan, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
 
 
 def test_far_scores():

@@ -98,6 +98,43 @@ def test_trees(T, window, sinks):
         _check(q, pages, table, start, None, window, sinks, got, lambda i, j: see[i, j], rows)
 
 
+@pytest.mark.parametrize("B,T,Hq,H,D,window,sinks", [(8, 21, 512, 64, 128, 100, 5), (8, 30, 256, 64, 128, 1500, 0),
+                                                     (8, 27, 256, 64, 128, 40, 70), (3, 21, 32, 4, 256, 40000, 0),
+                                                     (2, 33, 8, 2, 256, 1 << 20, 9), (4, 70, 2, 2, 256, 30000, 1)])
+def test_shared_pages(B, T, Hq, H, D, window, sinks):
+    """Shapes whose pages the waves of a workgroup share (heads of 128: more than 96 rows and 512
+    sequences times kv heads; of 256: more than 64 rows and wide tables), as chains and as trees."""
+    start = [(b * 131) % 700 for b in range(B)]
+    slack = 5200 // (B * H) * 4 if D == 256 else 0
+    q, pages, table = _case(8, B, T, Hq, H, D, start)
+    table = np.concatenate([_forget(table, start, T, window, sinks), np.full((B, slack), -1, np.int32)], 1)
+    keep = [(b, i, h) for b in range(B) for i in range(T) for h in range(Hq) if (b * 7 + i * 5 + h) % 97 == 0]
+    rs = np.random.default_rng(T)
+    par = [-1] + [int(rs.integers(0, i)) for i in range(1, T)]
+    see = np.zeros((T, T), bool)
+    for i in range(T):
+        see[i] = see[par[i]] if i else see[i]
+        see[i, i] = True
+    count = [T - b % 3 for b in range(B)]
+    for kw, rule, depth in ((dict(), None, None),
+                            (dict(mask=sv.tree_mask(par).to(DEV), depth=sv.tree_depths(par).to(DEV)),
+                             lambda i, j: see[i, j], sv.tree_depths(par)[0].tolist())):
+        got = _run(q, pages, table, start, count, window=window, sinks=sinks, **kw)
+        assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+        a, pool, held = q.double().cpu().numpy(), pages.cpu().numpy(), {}
+        out, lse = (x.double().cpu().numpy() for x in got)
+        for b in range(B):
+            assert (out[b, count[b]:] == 7).all() and (lse[b, count[b]:] == 7).all()
+            held[b] = plain.held(pool, table[b], start[b] + count[b], D)[:2] + (
+                plain.window_sees(start[b], count[b], T, rule or (lambda i, j: j <= i), depth, rule is not None, window, sinks),)
+        for b, i, h in keep:
+            if i < count[b]:
+                k, v, sees = held[b]
+                want = plain.attend(a[b, i, h], k[:, h // (Hq // H)], v[:, h // (Hq // H)], sees[i], D ** -0.5)
+                assert (np.abs(out[b, i, h] - want[0]) <= want[2]).all(), (b, i, h)
+                assert abs(lse[b, i, h] - want[1]) <= want[3], (b, i, h)
+
+
 def test_rows_that_see_nothing():
     T, start = 3, [200, 0]
     q, pages, table = _case(4, 2, T, 2, 1, 128, start)

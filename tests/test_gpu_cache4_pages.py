@@ -129,6 +129,61 @@ def test_most_sequences():
         s.check()
 
 
+def test_rows_past_4_gib_apart_and_another_stream():
+    wide = torch.full((3, (1 << 30) + 8), 55, dtype=torch.int32, device=DEV)
+    table = wide[:, :8]
+    table.fill_(-1)
+    held, free, count = _i32([0, 0, 0]), _i32(range(20)), _i32([20])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    sv.cache4_reserve(table, held, _i32([64, 65, 500]), free, count, stream=s)
+    slots = sv.cache4_slots(table, _i32([0, 64, 499]), 1, 20, stream=s)
+    s.synchronize()
+    assert table.tolist() == [[19] + [-1] * 7, [18, 17] + [-1] * 6, list(range(16, 8, -1))]
+    assert held.tolist() == [1, 2, 8] and int(count) == 9
+    assert slots.tolist() == [[19 * 64], [17 * 64], [9 * 64 + 51]]
+    assert (wide[:, 8:16] == 55).all()
+
+
+def test_one_sequence_of_many_pages():
+    n = 200_000
+    held, need, free, count = _i32([0]), _i32([64 * n]), torch.arange(n, dtype=torch.int32, device=DEV), _i32([n])
+    table = torch.full((1, n), -1, dtype=torch.int32, device=DEV)
+    sv.cache4_reserve(table, held, need, free, count)
+    assert torch.equal(table[0], torch.arange(n - 1, -1, -1, dtype=torch.int32, device=DEV)) and int(count) == 0
+    sv.cache4_reserve(table, held, _i32([1]), free, count)
+    assert table[0, 0] == n - 1 and (table[0, 1:] == -1).all() and int(count) == n - 1 and int(held) == 1
+    assert torch.equal(free, torch.arange(n, dtype=torch.int32, device=DEV))
+
+
+def test_captured_reserve_of_many_sequences():
+    """Both kernels in a graph, replayed with other lengths in place."""
+    r = random.Random(3)
+    s = State(2000, 6, 9000)
+    need = _i32([0] * 2000)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        sv.cache4_reserve(s.table, s.held, need, s.free, s.count)
+    for _ in range(6):
+        lengths = [r.randint(0, 384) for _ in range(2000)]
+        need.copy_(_i32(lengths))
+        g.replay()
+        torch.cuda.synchronize()
+        s.n = plain.reserve(s.rows, s.held_, lengths, s.stack, s.n)
+        s.check()
+
+
+def test_slots_of_more_than_32_bits_of_tokens():
+    B, T = 1 << 16, (1 << 15) + 1
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None].expand(B, 1).contiguous()
+    start = torch.arange(B, dtype=torch.int32, device=DEV) % 64
+    got = sv.cache4_slots(table, start, T, B, count=torch.ones(B, dtype=torch.int32, device=DEV))
+    b = torch.arange(B, device=DEV)
+    assert torch.equal(got[:, 0], b * 64 + b % 64)
+    assert bool((got[:, 1] == -1).all()) and bool((got[:, T - 1] == -1).all()) and bool((got[-1, 1:] == -1).all())
+
+
 @pytest.mark.parametrize("T", [1, 7, 300])
 def test_slots(T):
     start, count = [0, 63, 60, -1, 10, 200, 250, 5, 2147483647], [T, T, T - 1, T, 0, T, T, T + 1, T]
