@@ -366,6 +366,15 @@ struct C4OwnArgs : C4AttnArgs {
   const float* stat;
 };
 
+// Branches whose pages are their prefix's and then their own, each for itself:
+// where sharing would save less than the records cost.
+struct C4BehindArgs : C4AttnArgs {
+  C4View prefix;
+  const int32_t* prefix_len;
+  int32_t fan;
+};
+
+template <typename Args> constexpr bool kC4Behind = std::is_same<Args, C4BehindArgs>::value;
 template <typename Args> constexpr bool kC4Window = std::is_same<Args, C4WindowArgs>::value;
 template <typename Args> constexpr bool kC4Prefix = std::is_same<Args, C4PrefixArgs>::value;
 template <typename Args> constexpr bool kC4Own = std::is_same<Args, C4OwnArgs>::value;
@@ -388,6 +397,18 @@ __host__ __device__ __forceinline__ C4Gap c4_gap(int32_t window, int32_t sinks, 
   const int32_t keep = head < low ? head : low;
   return {keep, low - keep};
 }
+
+// The tokens of branch b's prefix, whose pages come before its own; -1: ill-formed.
+template <bool UNIFORM, typename Args>
+__device__ __forceinline__ int32_t c4_behind(const Args& A, int64_t b) {
+  if constexpr (kC4Behind<Args>) {
+    const int32_t g = (int32_t)b / A.fan;
+    const int32_t n = UNIFORM ? c4_scalar(A.prefix_len + g) : A.prefix_len[g];
+    return A.prefix.fits(n, 0, 0) ? n : -1;
+  }
+  return 0;
+}
+__device__ __forceinline__ int32_t c4_pages_of(int32_t tokens) { return tokens > 0 ? (tokens - 1) / kC4Page + 1 : 0; }
 
 // Live tokens of a branch.
 __device__ __forceinline__ int32_t c4_live(const C4PrefixArgs& A, int64_t b) {
@@ -438,6 +459,12 @@ __device__ __forceinline__ int32_t c4_pages(const Args& A, int64_t b, bool& bad)
   if (bad) return 1;
   const int32_t all = n == 0 ? 0 : (s + n + kC4Page - 1) / kC4Page;
   if constexpr (kC4Window<Args>) return n == 0 ? 0 : all - c4_gap(A.window, A.sinks, s, n).skip;
+  if constexpr (kC4Behind<Args>) {
+    const int32_t before = c4_behind<UNIFORM>(A, b);
+    if (n == 0) return 0;
+    bad = before < 0;
+    return bad ? 1 : c4_pages_of(before) + all;
+  }
   return all;
 }
 
@@ -1157,6 +1184,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     if constexpr (kC4Window<Args>)
       if (!bad) gap = c4_gap(A.window, A.sinks, s0, nnew);
     auto place = [&](int32_t p) { return kC4Window<Args> && p >= gap.keep ? p + gap.skip : p; };
+    const int32_t ps = kC4Behind<Args> && !bad ? c4_behind<true>(A, b) : 0, np = c4_pages_of(ps);
     if (p0 == 0 && p1 < pages) {
       cut_b = (int32_t)b, cut_hr = h * A.row_blocks + hr % nb, cut_new = nnew, cut_slot = seg > lo ? 1 : 0;
       cut_parts = (int32_t)c4_div(seg + kC4SegCost + pages - 1, share) - blockIdx.x + 1;
@@ -1171,8 +1199,14 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     const int32_t pw = p0 + (w >> 1);  // this wave's pages: pw, pw + 2, ..
     int32_t nu = end > pw ? (end - pw + 1) / 2 : 0;
     // the last page may hold no token in its second half
-    if (nu && place(pw + 2 * (nu - 1)) * (int64_t)kC4Page + 32 * half >= (int64_t)s0 + nnew) --nu;
+    if (nu && (place(pw + 2 * (nu - 1)) - np) * (int64_t)kC4Page + 32 * half >= (int64_t)s0 + nnew) --nu;
     auto page_of = [&](int32_t u) {
+      if constexpr (kC4Behind<Args>) {
+        const int32_t p = pw + 2 * u;
+        if (u >= nu) return 0;
+        return p < np ? c4_scalar(A.prefix.table + (b / A.fan) * A.prefix.table_stride + p)
+                      : c4_scalar(A.cache.table + b * A.cache.table_stride + (p - np));
+      }
       return u < nu ? c4_scalar(A.cache.table + b * A.cache.table_stride + place(pw + 2 * u)) : 0;
     };
     auto fetch = [&](int32_t page, uint8_t* buf, int k) {
@@ -1255,7 +1289,9 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
         else if (N == 2 && later == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Sh::kLoads) : "memory");
         else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         // the first of its positions relative to the new tokens'
-        const int64_t base = (int64_t)place(pw + 2 * u) * kC4Page + 32 * half - s0;
+        const int64_t base = kC4Behind<Args> && pw + 2 * u < np  // a prefix has no new tokens
+                                 ? (int64_t)(pw + 2 * u) * kC4Page + 32 * half - ps
+                                 : (int64_t)(place(pw + 2 * u) - np) * kC4Page + 32 * half - s0;
         bool masked = base + 32 > 0;
         if constexpr (kC4Window<Args>)  // or the last token's window ends behind, and these are not all sinks
           masked |= base <= (int64_t)A.T - 1 - A.window && base + s0 + 32 > A.sinks;
@@ -1263,12 +1299,13 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
         if (masked) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            if constexpr (kC4Prefix<Args>) sees[rt] = c4_below(-base);
+            if (kC4Prefix<Args> || (kC4Behind<Args> && pw + 2 * u < np)) sees[rt] = c4_below(-base);
             else sees[rt] = c4_sees(A, b, tok[rt], nnew, base);
             if constexpr (kC4Window<Args>) sees[rt] &= c4_in_window(A, s0, low[rt], base);
           }
-          const int64_t have = nnew - base;
-          valid = have >= 32 ? ~0u : (1u << have) - 1u;
+          const int64_t have = (kC4Behind<Args> && pw + 2 * u < np ? 0 : nnew) - base;
+          if constexpr (kC4Behind<Args>) valid = c4_below(have);
+          else valid = have >= 32 ? ~0u : (1u << have) - 1u;
         }
         c4_unit<D, RT>(buf + w * Sh::kBuf + k * Sh::kUnit, half, rows_of, S, A.c, lane, masked, sees, valid);
         if (u + 2 * N < nu) {

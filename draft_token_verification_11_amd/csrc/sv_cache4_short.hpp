@@ -35,14 +35,19 @@ __global__ __launch_bounds__(256, 2) void k_attention_cache4_short(Args A) {
   const int32_t s0 = c4_scalar(A.start + b);
   const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
   bool faulty = bad;
+  const int32_t ps = kC4Behind<Args> && !bad ? c4_behind<true>(A, b) : 0, np = c4_pages_of(ps);
   // pairs of tiles; the last page may hold no token in its second half
-  const int32_t pairs = bad ? 0 : (int32_t)(((int64_t)s0 + nnew + 31) / 32);
+  const int32_t pairs = bad ? 0 : 2 * np + (int32_t)(((int64_t)s0 + nnew + 31) / 32);
   uint8_t* const buf = buffers[w];
   int32_t page = 0;
   auto fetch = [&](int32_t u) {
     if (u >= pairs) return;
     if (!(u & 1)) {
-      page = c4_scalar(A.cache.table + b * A.cache.table_stride + u / 2);
+      const int32_t p = u / 2;
+      if constexpr (kC4Behind<Args>)
+        page = p < np ? c4_scalar(A.prefix.table + (b / A.fan) * A.prefix.table_stride + p)
+                      : c4_scalar(A.cache.table + b * A.cache.table_stride + (p - np));
+      else page = c4_scalar(A.cache.table + b * A.cache.table_stride + p);
       if ((uint32_t)page >= (uint32_t)A.cache.n_pages) {
         faulty = true;
         page = 0;
@@ -86,13 +91,15 @@ __global__ __launch_bounds__(256, 2) void k_attention_cache4_short(Args A) {
   for (int32_t u = 0; u < pairs; ++u) {
     if (u + 1 < pairs) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Sh::kLoads) : "memory");
     else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    const int64_t base = (int64_t)32 * u - s0;
+    const bool before = kC4Behind<Args> && u < 2 * np;  // a prefix has no new tokens
+    const int64_t base = before ? (int64_t)32 * u - ps : (int64_t)32 * (u - 2 * np) - s0;
     const bool masked = base + 32 > 0;
     uint32_t sees[RT] = {}, valid = 0;
     if (masked) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) sees[rt] = live >> rt & 1 ? c4_sees(A, b, tok[rt], nnew, base) : 0u;
-      valid = c4_below(nnew - base);
+      for (int rt = 0; rt < RT; ++rt)
+        sees[rt] = !(live >> rt & 1) ? 0u : before ? c4_below(-base) : c4_sees(A, b, tok[rt], nnew, base);
+      valid = c4_below((before ? 0 : nnew) - base);
     }
     c4_unit<D, RT>(buf + (u & 1) * Sh::kUnit, u & 1, rows_of, S, A.c, lane, masked, sees, valid);
     fetch(u + 2);

@@ -39,6 +39,29 @@ constexpr int32_t kShortCols = 8;
 // Branches up to which their live rows are counted through: one a lane.
 constexpr int32_t kCompactFan = 64;
 
+// Whether a prefix's pages are read for all its branches at once, or by each branch
+// before its own.  Sharing them saves a block of rows of each branch the pages, at
+// about 2.7 ns a page for the whole GPU (three blocks of 16 rows in one that shares
+// the conversion cost a block of heads of 256 2.6 times as much), and costs further
+// passes, 10 us, and the rows' records, written and read.  Whole calls, us, by each
+// branch and shared:
+//   heads of 128  4 branches of 4 rows, 8 kv heads, 777 tokens: 15 and 18; 16 such
+//                 prefixes 21 and 18; 64 x 8 branches of 20 rows, 200 tokens 45 and 75,
+//                 512 tokens 117 and 85
+//   heads of 64   96 branches of 2 rows, 16 kv heads, 200 tokens 37 and 42 (the rule
+//                 shares), 1,000 tokens 52 and 49; 32 x 16 branches of 8 rows, 256
+//                 tokens 22 and 31 (the rule shares), 1,024 tokens 94 and 39
+//   heads of 256  8 x 45 branches of 14 rows, 16 kv heads, 256 tokens 74 and 162, 1,024
+//                 tokens 277 and 217; 4 x 6 of 63 rows, 4 kv heads, 2,048 tokens 46
+//                 and 56, 8,155 tokens 127 and 80
+// The rule sees the table's width and not the prefixes' lengths.
+bool shared_pays(const PrefixShape& shape, int64_t each, int64_t prefixes, int64_t kv_heads, int64_t cols, int64_t rows,
+                 int32_t d, int64_t branch_blocks) {
+  const double blocks = shape.wide ? shape.blocks * 2.6 : double(shape.blocks);
+  const double saved = (double(each) * double(branch_blocks) - blocks) * double(prefixes * kv_heads) * double(cols) * 0.0027;
+  return saved > 10.0 + double(rows) * d * 8 / 4e6;
+}
+
 // A call's workspace: the rows' records, and one attention's after the other.
 // Its size does not go by the tables, of which a size query knows nothing.
 struct SharedSpace {
@@ -54,6 +77,18 @@ SharedSpace shared_space(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads
   const size_t prefix = std::max(shape_workspace(d, tiles), wide_rows(rows, d) ? wide_workspace(d) : 0);
   return {align256(count * size_t(d) * 4), align256(count * 16),
           std::max(attention_workspace(T, q_heads, kv_heads, d), prefix)};
+}
+
+// The branches' pass, over at most `cols` pages each.
+template <typename Args>
+void launch_own(Args& A, int32_t d, int tiles, int64_t cols, void* scratch, hipStream_t st) {
+  const int64_t waves = int64_t(A.B) * A.cache.heads * A.row_blocks;
+  if (cols <= kShortCols && grid_fits((waves + 3) / 4, 256))
+    with_shape(d, tiles, [&](auto D, auto RT) {
+      hipLaunchKernelGGL((sv::k_attention_cache4_short<D, RT, Args>), dim3(unsigned((waves + 3) / 4)), dim3(256), 0, st, A);
+    });
+  else
+    with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(A, scratch, st); });
 }
 
 }  // namespace
@@ -93,6 +128,23 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
                                          compact);
   if (prefixes * (int64_t(prefix_cols) + sv::kC4SegCost) * cache.heads >= (int64_t(1) << 40) / shape.blocks)
     return SPEC_ERR_UNSUPPORTED;
+  const int64_t rows = int64_t(B) * T * q_heads;
+  if (!shared_pays(shape, each, prefixes, cache.heads, prefix_cols, rows, d, base.row_blocks)) {
+    const int64_t cols = int64_t(prefix_cols) + cache.table_cols;
+    if (int64_t(B) * (cols + sv::kC4SegCost) * cache.heads < (int64_t(1) << 40) / base.row_blocks) {
+      sv::C4BehindArgs A;
+      static_cast<sv::C4AttnArgs&>(A) = base;
+      A.prefix = view(prefix);
+      A.prefix_len = prefix_len;
+      A.fan = each;
+      A.split = cols > kAttnWhole;
+      if (workspace_bytes < shared_space(B, T, q_heads, cache.heads, d, fan).bytes()) return SPEC_ERR_WORKSPACE;
+      auto st = static_cast<hipStream_t>(stream);
+      (void)hipGetLastError();
+      launch_own(A, d, tiles, cols, workspace, st);
+      return finish_launch();
+    }
+  }
   const SharedSpace space = shared_space(B, T, q_heads, cache.heads, d, fan);
   if (workspace_bytes < space.bytes()) return SPEC_ERR_WORKSPACE;
   auto* const rec = static_cast<float*>(workspace);
@@ -122,13 +174,7 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
   (void)hipGetLastError();
   if (shape.wide) with_wide(d, [&](auto D) { launch_wide<D>(P, P.block_rows, scratch, st); });
   else with_shape(d, shape.tiles, [&](auto D, auto RT) { launch_attention<D, RT>(P, scratch, st); });
-  const int64_t waves = int64_t(B) * cache.heads * O.row_blocks;
-  if (cache.table_cols <= kShortCols && grid_fits((waves + 3) / 4, 256))
-    with_shape(d, tiles, [&](auto D, auto RT) {
-      hipLaunchKernelGGL((sv::k_attention_cache4_short<D, RT, sv::C4OwnArgs>), dim3(unsigned((waves + 3) / 4)), dim3(256), 0, st, O);
-    });
-  else
-    with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(O, scratch, st); });
+  launch_own(O, d, tiles, cache.table_cols, scratch, st);
   return finish_launch();
 }
 

@@ -12,9 +12,14 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
-def _case(seed, B, fan, T, Hq, H, D, start, prefix, slack=0):
+# Columns of a prefix's table with which its pages are shared: calls go by the tables' width, and
+# with narrow ones each branch of a small call reads its prefix itself.
+WIDE = 6000
+
+
+def _case(seed, B, fan, T, Hq, H, D, start, prefix, slack=0, wide=0):
     """q, a pool of random values, the branches' tables and their prefixes', `slack` columns wider
-    than they need be."""
+    than they need be, the prefixes' `wide` columns more."""
     rs = np.random.default_rng([seed, B, T, Hq, D])
     P = max(1, -(-(max(start) + T) // 64))
     PP = max(1, -(-max(prefix) // 64))
@@ -26,7 +31,7 @@ def _case(seed, B, fan, T, Hq, H, D, start, prefix, slack=0):
     k, v = (torch.randn(1, n * 64, H, D, generator=g, device=DEV) for _ in range(2))
     sv.cache4_write(pages, _i32([list(range(n))]), _i32([0]), k, v)
     q = torch.randn(B, T, Hq, D, generator=g, device=DEV).bfloat16()
-    table, ptable = (np.concatenate([x, np.full((len(x), slack), -1, np.int32)], 1) for x in (table, ptable))
+    table, ptable = (np.concatenate([x, np.full((len(x), n), -1, np.int32)], 1) for x, n in ((table, slack), (ptable, slack + wide)))
     return q, pages, table, ptable
 
 
@@ -75,6 +80,7 @@ def _check(q, pages, table, start, ptable, prefix, fan, got, count=None, sees=No
                     assert lse[b, i, h] == want[1] or abs(lse[b, i, h] - want[1]) <= want[3], (b, i, h)
 
 
+@pytest.mark.parametrize("wide", [0, WIDE])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("B,fan,T,Hq,H,start,prefix", [
     (1, 1, 1, 1, 1, [0], [1]),
@@ -85,22 +91,24 @@ def _check(q, pages, table, start, ptable, prefix, fan, got, count=None, sees=No
     (9, 9, 9, 8, 2, [7, 0, 1, 2, 3, 64, 65, 66, 300], [350]),  # 324 rows
     (33, 16, 2, 4, 4, list(range(33)), [31, 95, 33]),
 ])
-def test_branches(D, B, fan, T, Hq, H, start, prefix):
-    q, pages, table, ptable = _case(1, B, fan, T, Hq, H, D, start, prefix)
+def test_branches(D, B, fan, T, Hq, H, start, prefix, wide):
+    q, pages, table, ptable = _case(1, B, fan, T, Hq, H, D, start, prefix, wide=wide)
     _check(q, pages, table, start, ptable, prefix, fan, _run(q, pages, table, start, ptable, prefix, fan))
 
 
+@pytest.mark.parametrize("wide", [0, WIDE])
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_counts_and_wide_tables(D):
+def test_counts_and_wide_tables(D, wide):
     """Fewer new tokens than columns, none at all, tables wide enough for pages to be cut."""
     B, fan, T = 7, 3, 6
     start, count, prefix = [0, 70, 3, 1, 0, 200, 5], [6, 0, 1, 3, 0, 2, 6], [1000, 65, 300]
-    q, pages, table, ptable = _case(2, B, fan, T, 8, 2, D, start, prefix, slack=21)
+    q, pages, table, ptable = _case(2, B, fan, T, 8, 2, D, start, prefix, 21, wide)
     _check(q, pages, table, start, ptable, prefix, fan, _run(q, pages, table, start, ptable, prefix, fan, count), count)
 
 
+@pytest.mark.parametrize("wide", [0, WIDE])
 @pytest.mark.parametrize("T", [5, 21, 40])
-def test_trees(T):
+def test_trees(T, wide):
     rs = np.random.default_rng(T)
     par = [-1] + [int(rs.integers(0, i)) for i in range(1, T)]
     see = np.zeros((T, T), bool)
@@ -108,24 +116,26 @@ def test_trees(T):
         see[i] = see[par[i]] if i else see[i]
         see[i, i] = True
     start, prefix = [0, 30, 64, 2, 0], [100, 0, 190]
-    q, pages, table, ptable = _case(3, 5, 2, T, 4, 1, 64, start, prefix)
+    q, pages, table, ptable = _case(3, 5, 2, T, 4, 1, 64, start, prefix, wide=wide)
     got = _run(q, pages, table, start, ptable, prefix, 2, mask=sv.tree_mask(par).to(DEV))
     _check(q, pages, table, start, ptable, prefix, 2, got, sees=lambda i, j: see[i, j])
 
 
-def test_rows_that_see_nothing_of_their_own():
+@pytest.mark.parametrize("wide", [0, WIDE])
+def test_rows_that_see_nothing_of_their_own(wide):
     T, start, prefix = 3, [0, 0, 0, 0], [70, 0]
-    q, pages, table, ptable = _case(4, 4, 2, T, 2, 1, 128, start, prefix)
+    q, pages, table, ptable = _case(4, 4, 2, T, 2, 1, 128, start, prefix, wide=wide)
     none = torch.zeros(1, T, 1, dtype=torch.int32, device=DEV)
     got = _run(q, pages, table, start, ptable, prefix, 2, mask=none)
     _check(q, pages, table, start, ptable, prefix, 2, got, sees=lambda i, j: False)
     assert (got[0][2:] == 0).all() and (got[1][2:] == -float("inf")).all()
 
 
-def test_bad_prefixes_sequences_and_pages():
+@pytest.mark.parametrize("wide", [0, 3 * WIDE])
+def test_bad_prefixes_sequences_and_pages(wide):
     B, fan, T = 10, 2, 2
-    start, count, prefix = [0, 3, 0, 0, 5, -1, 9, 1, 0, 0], [2, 2, 2, 2, 2, 2, 3, 2, 2, 2], [100, -1, 60, 9, 1 << 20]
-    q, pages, table, ptable = _case(5, B, fan, T, 2, 1, 64, [70] * B, [130] * 5)
+    start, count, prefix = [0, 3, 0, 0, 5, -1, 9, 1, 0, 0], [2, 2, 2, 2, 2, 2, 3, 2, 2, 2], [100, -1, 60, 9, 1 << 24]
+    q, pages, table, ptable = _case(5, B, fan, T, 2, 1, 64, [70] * B, [130] * 5, wide=wide)
     ptable[0, 2] = -7   # behind the prefix's end: not looked at
     ptable[2, 0] = 1 << 28
     table[7, 0] = -1
@@ -135,10 +145,11 @@ def test_bad_prefixes_sequences_and_pages():
     assert nan == [False, False, True, True, True, True, True, True, True, True]
 
 
-def test_noise_behind_a_prefix_and_nan_in_it():
+@pytest.mark.parametrize("wide", [0, WIDE])
+def test_noise_behind_a_prefix_and_nan_in_it(wide):
     D, T, fan = 128, 2, 3
     start, prefix = [0] * 6, [70, 70]
-    q, pages, table, ptable = _case(6, 6, fan, T, 4, 2, D, start, prefix)
+    q, pages, table, ptable = _case(6, 6, fan, T, 4, 2, D, start, prefix, wide=wide)
     raw = pages.cpu().numpy()
     rs = np.random.default_rng(1)
     for g in range(2):
@@ -244,6 +255,21 @@ def test_shared_pages_bad_ones_and_noise(case):
     _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: (b + i + h) % 53 == 0)
 
 
+@pytest.mark.parametrize("case", [(104, 13, 2, 256, 64, 128, 0), (24, 6, 9, 14, 2, 256, 400)])
+def test_shared_pages_and_rows_of_any_magnitude(case):
+    """Rows whose scores pass 2^24 or F32's range beside ordinary ones in one tile."""
+    B, fan, T, Hq, H, D, slack = case
+    start, prefix = [3] * B, [150] * (-(-B // fan))
+    q, pages, table, ptable = _case(17, B, fan, T, Hq, H, D, start, prefix, slack)
+    size = torch.ones(B, 1, Hq, 1, device=DEV)
+    size[1::5, :, ::3], size[2::5, :, 1::3], size[3::5, :, ::2] = 1e8, 3e37, 1e-30
+    got = _run((q.float() * size).bfloat16(), pages, table, start, ptable, prefix, fan)
+    usual = (size[:, 0, :, 0] == 1).cpu().numpy()
+    _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: usual[b, h] and (b * 7 + i * 5 + h) % 61 == 0)
+    far = (size[:, 0, :, 0] == 1e8)[:, None].expand(B, T, Hq)
+    assert torch.isfinite(got[0][far]).all() and (got[0][far].abs() <= 8).all()
+
+
 def test_captured_with_shared_pages():
     B, fan, T, Hq, H, D = 104, 13, 2, 256, 64, 128
     start, prefix = [3] * B, [100 + g for g in range(8)]
@@ -276,11 +302,12 @@ def test_another_stream():
     assert torch.equal(got, want)
 
 
-def test_far_scores():
+@pytest.mark.parametrize("wide", [0, 3 * WIDE])
+def test_far_scores(wide):
     """Scores of ordinary and of large magnitude side by side, in the prefix and behind it."""
     D, T, fan = 64, 1, 4
     start, prefix = [3] * 4, [200]
-    q, pages, table, ptable = _case(8, 4, fan, T, 2, 1, D, start, prefix)
+    q, pages, table, ptable = _case(8, 4, fan, T, 2, 1, D, start, prefix, wide=wide)
     q = q * torch.tensor([1.0, 1e4, 1e9, 1e-9], device=DEV).view(4, 1, 1, 1).bfloat16()
     got = _run(q, pages, table, start, ptable, prefix, fan)
     _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: b in (0, 3))
@@ -288,22 +315,24 @@ def test_far_scores():
     assert torch.isfinite(got[0]).all() and (got[0].abs() <= 64).all()
 
 
-def test_agrees_with_one_cache():
+@pytest.mark.parametrize("wide", [0, WIDE])
+def test_agrees_with_one_cache(wide):
     """A prefix of whole pages with each branch's own pages behind it, as one table."""
     B, fan, T, Hq, H, D, n = 12, 4, 4, 8, 2, 128, 512
     start, prefix = [(b * 29) % 90 for b in range(B)], [n] * 3
-    q, pages, table, ptable = _case(9, B, fan, T, Hq, H, D, start, prefix)
+    q, pages, table, ptable = _case(9, B, fan, T, Hq, H, D, start, prefix, wide=wide)
     got = _run(q, pages, table, start, ptable, prefix, fan)
-    one = np.concatenate([np.repeat(ptable, fan, 0), table], 1)
+    one = np.concatenate([np.repeat(ptable[:, : n // 64], fan, 0), table], 1)
     out, lse = sv.attention_cache4(q, pages, _i32(one), _i32([n + s for s in start]), return_lse=True)
     assert (got[1] - lse).abs().max() <= 2.0 ** -17
     assert (got[0].float() - out.float()).abs().max() <= 2.0 ** -6
 
 
-def test_same_outputs_every_time_and_strided():
+@pytest.mark.parametrize("wide", [0, WIDE])
+def test_same_outputs_every_time_and_strided(wide):
     B, fan, T, Hq, H, D = 16, 8, 3, 8, 2, 128
     start, prefix = [11] * B, [1999, 2345]
-    q, pages, table, ptable = _case(10, B, fan, T, Hq, H, D, start, prefix)
+    q, pages, table, ptable = _case(10, B, fan, T, Hq, H, D, start, prefix, wide=wide)
     want = _run(q, pages, table, start, ptable, prefix, fan)
     wide = torch.zeros(T, B, Hq + 3, D + 8, dtype=torch.bfloat16, device=DEV)
     wide[:, :, :Hq, :D] = q.transpose(0, 1)
