@@ -214,6 +214,10 @@ size_t wide_workspace(int32_t d) {
   });
   return bytes;
 }
+// Segments up to which four times as many threads share a row's records, which are
+// 32 or more (378 rows of heads of 256 over 131,072 tokens, 3 segments: 104 us and
+// 139; 12 segments over 65,536: 158 and 159; 24 over 16,384: 98 and 95).
+constexpr int64_t kWideFew = 8;
 template <int D, typename Args>
 void launch_wide(Args& A, int32_t block_rows, void* workspace, hipStream_t st) {
   using Sh = sv::C4Wide<D>;
@@ -223,10 +227,12 @@ void launch_wide(Args& A, int32_t block_rows, void* workspace, hipStream_t st) {
   hipLaunchKernelGGL((sv::k_attention_cache4_wide<D, Args>), dim3(kGrid), dim3(64 * Sh::kWaves), 0, st, A, block_rows);
   if (!A.split) return;
   const dim3 grid{unsigned(kGrid), unsigned(block_rows / 16)};
-  if (int64_t(A.B) * A.cache.heads * A.row_blocks <= kAttnFew)
-    hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 4, Args>), grid, dim3(1024), 0, st, A, block_rows);
-  else
-    hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 1, Args>), grid, dim3(256), 0, st, A, block_rows);
+  if constexpr (D == 256)  // of heads of 128 there are always more
+    if (int64_t(A.B) * A.cache.heads * A.row_blocks <= kWideFew) {
+      hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 4, Args>), grid, dim3(1024), 0, st, A, block_rows);
+      return;
+    }
+  hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 1, Args>), grid, dim3(256), 0, st, A, block_rows);
 }
 
 // Arguments of an attention call, checked, and its row tiles.

@@ -134,7 +134,9 @@ __device__ __forceinline__ bool res_plan(const ReserveArgs& A, ReservePlan& P, i
     res_pages(A, b, h, n);
     put(b, h, n);
   }
-  if (most) atomicMax(&used, (unsigned long long)most);
+  // sums ascend with the threads: the wave's last served one has its largest
+  const uint64_t any = __ballot(most > 0);
+  if (any && lane == 63 - __builtin_clzll(any)) atomicMax(&used, (unsigned long long)most);
   __syncthreads();
   P.takes = (int64_t)used;
   return true;
@@ -175,24 +177,30 @@ struct SlotArgs {
   int32_t table_cols, n_pages, T;
 };
 
-constexpr int kSlotsPer = 4;
+__device__ __forceinline__ int64_t slot_of(const SlotArgs& A, int64_t b, int32_t s, int32_t n, int32_t i) {
+  const C4View cache{nullptr, A.table, A.table_stride, A.n_pages, A.table_cols, 0};
+  if (!cache.fits(s, n, A.T) || i >= n) return -1;
+  const int32_t pos = s + i, page = cache.page(b, pos / kC4Page);
+  return page < 0 ? -1 : (int64_t)page * kC4Page + pos % kC4Page;
+}
+
+// Few tokens a sequence: a token a thread, whatever its sequence.
 __global__ __launch_bounds__(256) void k_cache4_slots(SlotArgs A) {
-  // four tokens a thread, whose loads do not wait for each other
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (x >= A.tokens) return;
+  // as a rule all of it has 32 bits
+  const int64_t b = A.tokens >> 31 ? x / A.T : (uint32_t)x / (uint32_t)A.T;
+  A.slots[x] = slot_of(A, b, A.start[b], A.count ? A.count[b] : A.T, (int32_t)(x - b * A.T));
+}
+// Many: four tokens of one sequence a thread.
+constexpr int kSlotsRun = 4 * 256;
+__global__ __launch_bounds__(256) void k_cache4_slots_run(SlotArgs A) {
+  const int64_t b = blockIdx.x;
+  const int32_t s = c4_scalar(A.start + b), n = A.count ? c4_scalar(A.count + b) : A.T;
 #pragma unroll
-  for (int k = 0; k < kSlotsPer; ++k) {
-    const int64_t x = ((int64_t)blockIdx.x * kSlotsPer + k) * 256 + threadIdx.x;
-    if (x >= A.tokens) return;
-    // as a rule all of it has 32 bits
-    const int64_t b = A.tokens >> 31 ? x / A.T : (uint32_t)x / (uint32_t)A.T;
-    const int32_t i = (int32_t)(x - b * A.T);
-    const C4View cache{nullptr, A.table, A.table_stride, A.n_pages, A.table_cols, 0};
-    const int32_t s = A.start[b], n = A.count ? A.count[b] : A.T;
-    int64_t slot = -1;
-    if (cache.fits(s, n, A.T) && i < n) {
-      const int32_t pos = s + i, page = cache.page(b, pos / kC4Page);
-      if (page >= 0) slot = (int64_t)page * kC4Page + pos % kC4Page;
-    }
-    A.slots[x] = slot;
+  for (int k = 0; k < 4; ++k) {
+    const int32_t i = (int32_t)blockIdx.y * kSlotsRun + k * 256 + threadIdx.x;
+    if (i < A.T) A.slots[b * A.T + i] = slot_of(A, b, s, n, i);
   }
 }
 

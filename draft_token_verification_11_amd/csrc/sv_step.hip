@@ -19,6 +19,9 @@ constexpr int64_t kRotateWaves = 8192;
 // Workgroups that move the pages of a call of many sequences.
 constexpr int64_t kReserveBlocks = 1024;
 
+// New tokens from which on a workgroup has those of one sequence only.
+constexpr int32_t kSlotsLong = 256;
+
 // One side of a rotation; a side without heads is not looked at.
 int check_side(const spec_heads_t& in, const spec_heads_t& out, int32_t heads, const void* weight,
                const spec_rotate_t& how, int32_t B, int32_t T) {
@@ -176,12 +179,15 @@ int spec_cache4_slots(const int32_t* table, int64_t table_stride, int32_t table_
     return SPEC_ERR_INVALID_ARG;
   if (table_cols < 1 || table_stride < table_cols || n_pages < 1) return SPEC_ERR_INVALID_ARG;
   if (table_cols > kMaxTableCols) return SPEC_ERR_UNSUPPORTED;
-  const int64_t tokens = int64_t(B) * T, blocks = (tokens + 256 * sv::kSlotsPer - 1) / (256 * sv::kSlotsPer);
+  const int64_t tokens = int64_t(B) * T, blocks = (tokens + 255) / 256;
   if (!grid_fits(blocks, 256)) return SPEC_ERR_UNSUPPORTED;
   const sv::SlotArgs A{table, table_stride, start, count, slots, tokens, table_cols, n_pages, T};
   auto st = static_cast<hipStream_t>(stream);
   (void)hipGetLastError();
-  hipLaunchKernelGGL(sv::k_cache4_slots, dim3(unsigned(blocks)), dim3(256), 0, st, A);
+  if (T >= kSlotsLong)
+    hipLaunchKernelGGL(sv::k_cache4_slots_run, dim3(unsigned(B), unsigned((T + sv::kSlotsRun - 1) / sv::kSlotsRun)), dim3(256), 0, st, A);
+  else
+    hipLaunchKernelGGL(sv::k_cache4_slots, dim3(unsigned(blocks)), dim3(256), 0, st, A);
   return finish_launch();
 }
 
