@@ -332,6 +332,7 @@ struct C4AttnArgs {
   int32_t split;          // 0: no segment is cut, and there is nothing to join
   struct C4Cut* cuts;     // [workgroups] the segment that a workgroup begins and others end
   float* parts;           // [2 x workgroups] records of a workgroup's first and last cut segment
+  int32_t each = 0;       // a workgroup a segment (none is cut), by its place among B x heads x row_blocks
 };
 
 // A call whose cached tokens are seen through a window, but for a few first ones
@@ -378,6 +379,7 @@ template <typename Args> constexpr bool kC4Behind = std::is_same<Args, C4BehindA
 template <typename Args> constexpr bool kC4Window = std::is_same<Args, C4WindowArgs>::value;
 template <typename Args> constexpr bool kC4Prefix = std::is_same<Args, C4PrefixArgs>::value;
 template <typename Args> constexpr bool kC4Own = std::is_same<Args, C4OwnArgs>::value;
+template <typename Args> constexpr bool kC4Each = !std::is_same<Args, C4AttnArgs>::value && !kC4Prefix<Args>;
 
 struct C4Cut {
   int32_t b, hr, nnew;  // its sequence, head and block of rows, and the sequence's new tokens
@@ -1142,11 +1144,14 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   // every wave for itself: no barrier before the first loads
   const int32_t per = (A.B + 63) / 64;
   const int32_t HR = c4_times(A);
-  int64_t before;
-  const int64_t all = c4_plan(A, lane, per, before) * HR;  // weight of all segments
-  const int64_t share = c4_share<Sh::kGrid>(all);
-  const int64_t lo = (int64_t)blockIdx.x * share;
-  const int64_t hi = min(lo + share, all);
+  const bool each = kC4Each<Args> && A.each;
+  int64_t before = 0, share = 1, lo = 0, hi = 1;
+  if (!each) {
+    const int64_t all = c4_plan(A, lane, per, before) * HR;  // weight of all segments
+    share = c4_share<Sh::kGrid>(all);
+    lo = (int64_t)blockIdx.x * share;
+    hi = min(lo + share, all);
+  }
   int32_t cut_b = 0, cut_hr = 0, cut_new = 0, cut_parts = 0, cut_slot = 0;
   auto note = [&] {
     if (A.split && tid == 0) A.cuts[blockIdx.x] = {cut_b, cut_hr, cut_new, cut_parts, cut_slot, {0, 0, 0}};
@@ -1157,13 +1162,16 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
   }
 
   // the segment of weight `lo`: its sequence, then its head and block of rows
-  int64_t seq_at;
-  int64_t b = c4_find(A, lane, per, before, c4_div(lo, HR), seq_at);
+  int64_t seq_at = 0, b;
+  if (each) b = blockIdx.x / (uint32_t)(A.cache.heads * A.row_blocks);
+  else b = c4_find(A, lane, per, before, c4_div(lo, HR), seq_at);
   bool bad;
   int32_t pages = c4_pages<true>(A, b, bad);
   int32_t nb = c4_blocks<true>(A, b);
-  int32_t hr = (int32_t)c4_div(lo - seq_at * HR, c4_weight(pages));
-  int64_t seg = seq_at * HR + hr * c4_weight(pages);  // where it begins
+  int32_t hr = each ? (int32_t)(blockIdx.x % (uint32_t)(A.cache.heads * A.row_blocks))
+                    : (int32_t)c4_div(lo - seq_at * HR, c4_weight(pages));
+  if (each && pages == 0) return;
+  int64_t seg = each ? 0 : seq_at * HR + hr * c4_weight(pages);  // where it begins
   const int32_t R = c4_rows(A);
   for (; seg < hi; seg += c4_weight(pages), ++hr) {
     if (hr == A.cache.heads * nb) {  // the next sequence with pages (seg is its begin)

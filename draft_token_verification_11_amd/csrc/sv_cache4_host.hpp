@@ -113,6 +113,21 @@ void row_blocks(int64_t rows, int32_t d, int* tiles, int64_t* blocks) {
 // rule sees the table's width, not the lengths, which stand in device memory: 777
 // tokens of one sequence take 11.9 us with a table of 13 columns, 14.0 with one of 512.
 constexpr int32_t kAttnWhole = 20;
+// Whether so many segments of so many pages at most are better not cut, where a
+// segment can have a workgroup of its own (not in spec_attention_cache4, whose
+// workgroups take what begins in their shares).  The GPU hands out the next one when
+// one ends, there is nothing to find or to join, and a segment's pages take their
+// time: four times as many segments as pages are enough to fill the rest of the GPU.
+// Whole calls, us, cut and each (24 rows a kv head, 8 of them of 128, lengths up to
+// 9,000):
+//   window of 2,000   8 sequences 24.8 and 25.3, 16 28.2 and 25.7, 64 53 and 38
+//   window of 4,000   16 sequences 33.9 and 41.1, 32 48.8 and 42.3, 64 81 and 65
+//   window of 8,000   64 sequences 136 and 116, with lengths from 10 on 89 and 90
+// Past 72 pages one long sequence among short ones would be waited for too long.
+constexpr int64_t kEachCols = 72;
+bool each_pays(int64_t segments, int64_t pages) {
+  return pages <= kAttnWhole || (pages <= kEachCols && segments >= 4 * pages);
+}
 // Up to this many segments (sequences x heads x blocks of rows) each is in four
 // records or more on average, and their rows are joined by a workgroup each (4 x 8
 // heads over 4,000 to 16,000 tokens: 25.5 us, by a wave each 28.8; 8 x 8: 35.6 and
@@ -163,9 +178,11 @@ void launch_attention(Args& A, void* workspace, hipStream_t st) {
   constexpr int kGrid = sv::C4Shape<D, RT>::kGrid;
   A.cuts = static_cast<sv::C4Cut*>(workspace);
   A.parts = reinterpret_cast<float*>(A.cuts + kGrid);
-  hipLaunchKernelGGL((sv::k_attention_cache4<D, RT, Args>), dim3(kGrid), dim3(256), 0, st, A);
-  if (!A.split) return;
   const int64_t segments = int64_t(A.B) * A.cache.heads * A.row_blocks;
+  A.each = sv::kC4Each<Args> && !A.split && grid_fits(segments, 256);
+  const unsigned grid = A.each ? unsigned(segments) : kGrid;
+  hipLaunchKernelGGL((sv::k_attention_cache4<D, RT, Args>), dim3(grid), dim3(256), 0, st, A);
+  if (!A.split) return;
   if (segments <= kAttnFew)
     hipLaunchKernelGGL((sv::k_attention_cache4_join_long<D, RT, Args>), dim3(unsigned(segments), RT * 16), dim3(256), 0, st, A);
   else
@@ -224,11 +241,17 @@ void launch_wide(Args& A, int32_t block_rows, void* workspace, hipStream_t st) {
   constexpr int kGrid = Sh::kGrid;
   A.cuts = static_cast<sv::C4Cut*>(workspace);
   A.parts = reinterpret_cast<float*>(A.cuts + kGrid);
-  hipLaunchKernelGGL((sv::k_attention_cache4_wide<D, Args>), dim3(kGrid), dim3(64 * Sh::kWaves), 0, st, A, block_rows);
+  const int64_t segments = int64_t(A.B) * A.cache.heads * A.row_blocks;
+  if constexpr (sv::kC4Each<Args>)
+    if (!A.split && grid_fits(segments, 64 * Sh::kWaves)) {
+      hipLaunchKernelGGL((sv::k_attention_cache4_wide<D, Args, true>), dim3(unsigned(segments)), dim3(64 * Sh::kWaves), 0, st, A, block_rows);
+      return;
+    }
+  hipLaunchKernelGGL((sv::k_attention_cache4_wide<D, Args, false>), dim3(kGrid), dim3(64 * Sh::kWaves), 0, st, A, block_rows);
   if (!A.split) return;
   const dim3 grid{unsigned(kGrid), unsigned(block_rows / 16)};
   if constexpr (D == 256)  // of heads of 128 there are always more
-    if (int64_t(A.B) * A.cache.heads * A.row_blocks <= kWideFew) {
+    if (segments <= kWideFew) {
       hipLaunchKernelGGL((sv::k_attention_cache4_wide_join<D, 4, Args>), grid, dim3(1024), 0, st, A, block_rows);
       return;
     }

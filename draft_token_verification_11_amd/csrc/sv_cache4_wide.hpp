@@ -424,7 +424,8 @@ __device__ __forceinline__ void c4_wide_run(const Args& A, C4Segment G, uint8_t 
   }
 }
 
-template <int D, typename Args>
+// EACH: a workgroup a segment, none of which is cut.
+template <int D, typename Args, bool EACH>
 __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_attention_cache4_wide(Args A, int32_t block_rows) {
   using Sh = C4Wide<D>;
   __shared__ __attribute__((aligned(16))) uint8_t pagebuf[2][2][Sh::kKeys];
@@ -434,11 +435,13 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int32_t per = (A.B + 63) / 64;
   const int32_t HR = c4_times(A);
-  int64_t before;
-  const int64_t all = c4_plan<Sh::kCost>(A, lane, per, before) * HR;  // weight of all segments
-  const int64_t share = c4_share<Sh::kGrid, Sh::kCost>(all);
-  const int64_t lo = (int64_t)blockIdx.x * share;
-  const int64_t hi = min(lo + share, all);
+  int64_t before = 0, share = 1, lo = 0, hi = 1;
+  if (!EACH) {
+    const int64_t all = c4_plan<Sh::kCost>(A, lane, per, before) * HR;  // weight of all segments
+    share = c4_share<Sh::kGrid, Sh::kCost>(all);
+    lo = (int64_t)blockIdx.x * share;
+    hi = min(lo + share, all);
+  }
   int32_t cut_b = 0, cut_hr = 0, cut_new = 0, cut_parts = 0, cut_slot = 0;
   auto note = [&] {
     if (A.split && tid == 0) A.cuts[blockIdx.x] = {cut_b, cut_hr, cut_new, cut_parts, cut_slot, {0, 0, 0}};
@@ -447,14 +450,17 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
     note();
     return;
   }
-  int64_t seq_at;
+  int64_t seq_at = 0;
   C4Segment G;
-  G.b = c4_find<Sh::kCost>(A, lane, per, before, c4_div(lo, HR), seq_at);
+  if (EACH) G.b = blockIdx.x / (uint32_t)(A.cache.heads * A.row_blocks);
+  else G.b = c4_find<Sh::kCost>(A, lane, per, before, c4_div(lo, HR), seq_at);
   bool bad;
   G.pages = c4_pages<true>(A, G.b, bad);
   int32_t nb = c4_blocks<true>(A, G.b);
-  int32_t hr = (int32_t)c4_div(lo - seq_at * HR, c4_weight<Sh::kCost>(G.pages));
-  int64_t seg = seq_at * HR + hr * c4_weight<Sh::kCost>(G.pages);  // where it begins
+  int32_t hr = EACH ? (int32_t)(blockIdx.x % (uint32_t)(A.cache.heads * A.row_blocks))
+                      : (int32_t)c4_div(lo - seq_at * HR, c4_weight<Sh::kCost>(G.pages));
+  if (EACH && G.pages == 0) return;
+  int64_t seg = EACH ? 0 : seq_at * HR + hr * c4_weight<Sh::kCost>(G.pages);  // where it begins
   for (; seg < hi; seg += c4_weight<Sh::kCost>(G.pages), ++hr) {
     if (hr == A.cache.heads * nb) {  // the next sequence with pages (seg is its begin)
       do {

@@ -34,32 +34,52 @@ PrefixShape prefix_shape(int64_t rows, int32_t d, int64_t prefixes_heads, int64_
   else row_blocks(rows, d, &x.tiles, &x.blocks);
   return x;
 }
-// Pages of a branch's own up to which a wave goes through them by itself.
-constexpr int32_t kShortCols = 8;
+// Whether a wave goes through the pages of a (branch, kv head, block of rows) by itself:
+// where there are as many of those as waves in flight, or half as many and few
+// pages.  Whole calls, us, four waves to each and one (16 rows a kv head):
+//   256   of heads of 128, 2 pages 8.7 and 13.7, 4 9.6 and 16.6
+//   512   2 pages 10.8 and 14.5, 8 14.0 and 23.1
+//   1,024 2 pages 18.7 and 15.7, 8 23.9 and 23.8, 32 55 and 58
+//   2,048 2 pages 27.7 and 19.7, 8 37.2 and 30.7, 32 95 and 95
+//   2,048 of heads of 256, 8 pages 66 and 49, 32 147 and 130; 4,096 of heads of 64, 32
+//         pages 143 and 123
+bool short_pays(int64_t segments, int64_t cols) {
+  return (segments >= 2048 && cols <= 32) || (segments >= 1024 && cols <= 8);
+}
 // Branches up to which their live rows are counted through: one a lane.
 constexpr int32_t kCompactFan = 64;
 
+// What a page costs a block of rows, in those of a block of one tile: more tiles share
+// the conversion of its codes, wide blocks (of up to 192 and 128 rows) yet more.
+double block_cost(bool wide, int tiles, int32_t d) {
+  if (wide) return d == 128 ? 4.2 : 3.8;
+  return tiles == 1 ? 1.0 : tiles == 2 ? 1.2 : tiles == 3 ? 1.3 : 2.6;
+}
 // Whether a prefix's pages are read for all its branches at once, or by each branch
-// before its own.  Sharing them saves a block of rows of each branch the pages, at
-// about 2.7 ns a page for the whole GPU (three blocks of 16 rows in one that shares
-// the conversion cost a block of heads of 256 2.6 times as much), and costs further
-// passes, 10 us, and the rows' records, written and read.  Whole calls, us, by each
-// branch and shared:
-//   heads of 128  4 branches of 4 rows, 8 kv heads, 777 tokens: 15 and 18; 16 such
-//                 prefixes 21 and 18; 64 x 8 branches of 20 rows, 200 tokens 45 and 75,
-//                 512 tokens 117 and 85
-//   heads of 64   96 branches of 2 rows, 16 kv heads, 200 tokens 37 and 42 (the rule
-//                 shares), 1,000 tokens 52 and 49; 32 x 16 branches of 8 rows, 256
-//                 tokens 22 and 31 (the rule shares), 1,024 tokens 94 and 39
-//   heads of 256  8 x 45 branches of 14 rows, 16 kv heads, 256 tokens 74 and 162, 1,024
-//                 tokens 277 and 217; 4 x 6 of 63 rows, 4 kv heads, 2,048 tokens 46
-//                 and 56, 8,155 tokens 127 and 80
+// before its own.  Sharing them saves the branches' blocks the pages, at 0.8, 1.3 or
+// 1.6 ns each for the whole GPU, and costs a pass more, 9 us, another one where only
+// the prefixes' segments are cut, and the rows' records: written and read at 4 TB/s, what
+// is past 32 MB at a quarter of that.  Of counted branches some rows are taken not to
+// be live.  Whole calls, us, by each branch and shared:
+//   heads of 128  4 samples of one prompt of 777 tokens, 8 kv heads: 11.7 and 16.6; 16
+//                 such prompts of 777 15.6 and 19.1, of 2,000 27.0 and 27.9, of 4,000 44
+//                 and 33; 64 x 8 branches of 20 rows behind 512 tokens 61 and 88, 1,000
+//                 105 and 114, 2,000 249 and 169
+//   heads of 64   96 branches of 2 rows, 16 kv heads, 200 tokens 13.4 and 17.5, 500 23.1
+//                 and 20.0, 2,000 50 and 35; 32 x 16 of 8 rows, 4 kv heads, 512 tokens
+//                 20.8 and 26.1 (the rule reads them by each), 1,024 34.3 and 32.3
+//   heads of 256  8 x 45 branches of 14 rows, 16 kv heads, 1,024 tokens 178 and 213; 4 x
+//                 6 of 63 rows, 4 kv heads, 4,096 tokens 67 and 72, 8,155 116 and 95
 // The rule sees the table's width and not the prefixes' lengths.
-bool shared_pays(const PrefixShape& shape, int64_t each, int64_t prefixes, int64_t kv_heads, int64_t cols, int64_t rows,
-                 int32_t d, int64_t branch_blocks) {
-  const double blocks = shape.wide ? shape.blocks * 2.6 : double(shape.blocks);
-  const double saved = (double(each) * double(branch_blocks) - blocks) * double(prefixes * kv_heads) * double(cols) * 0.0027;
-  return saved > 10.0 + double(rows) * d * 8 / 4e6;
+bool shared_pays(const PrefixShape& shape, const sv::C4AttnArgs& A, int tiles, int64_t each, int64_t prefixes,
+                 int64_t cols, int64_t rows, int32_t d, bool compact) {
+  const double blocks = double(shape.blocks) * block_cost(shape.wide, shape.tiles, d) * (compact ? 0.6 : 1.0);
+  const double branches = double(each) * double(A.row_blocks) * block_cost(false, tiles, d);
+  const double page = d == 64 ? 0.83e-3 : d == 128 ? 1.3e-3 : 1.6e-3;
+  const double saved = (branches - blocks) * double(prefixes * A.cache.heads) * double(cols) * page;
+  const bool cut = cols > kAttnWhole && each_pays(int64_t(A.B) * A.cache.heads * A.row_blocks, cols + A.cache.table_cols);
+  const double mb = double(rows) * d * 8 / 1e6;
+  return saved > 9.0 + (cut ? 10.0 : 0.0) + mb / 4 + std::max(mb - 32, 0.0) * 0.75;
 }
 
 // A call's workspace: the rows' records, and one attention's after the other.
@@ -82,10 +102,11 @@ SharedSpace shared_space(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads
 // The branches' pass, over at most `cols` pages each.
 template <typename Args>
 void launch_own(Args& A, int32_t d, int tiles, int64_t cols, void* scratch, hipStream_t st) {
-  const int64_t waves = int64_t(A.B) * A.cache.heads * A.row_blocks;
-  if (cols <= kShortCols && grid_fits((waves + 3) / 4, 256))
+  const int64_t segments = int64_t(A.B) * A.cache.heads * A.row_blocks, grid = (segments + 3) / 4;
+  A.split = !each_pays(segments, cols);
+  if (short_pays(segments, cols) && grid_fits(grid, 256))
     with_shape(d, tiles, [&](auto D, auto RT) {
-      hipLaunchKernelGGL((sv::k_attention_cache4_short<D, RT, Args>), dim3(unsigned((waves + 3) / 4)), dim3(256), 0, st, A);
+      hipLaunchKernelGGL((sv::k_attention_cache4_short<D, RT, Args>), dim3(unsigned(grid)), dim3(256), 0, st, A);
     });
   else
     with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(A, scratch, st); });
@@ -129,7 +150,7 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
   if (prefixes * (int64_t(prefix_cols) + sv::kC4SegCost) * cache.heads >= (int64_t(1) << 40) / shape.blocks)
     return SPEC_ERR_UNSUPPORTED;
   const int64_t rows = int64_t(B) * T * q_heads;
-  if (!shared_pays(shape, each, prefixes, cache.heads, prefix_cols, rows, d, base.row_blocks)) {
+  if (!shared_pays(shape, base, tiles, each, prefixes, prefix_cols, rows, d, compact)) {
     const int64_t cols = int64_t(prefix_cols) + cache.table_cols;
     if (int64_t(B) * (cols + sv::kC4SegCost) * cache.heads < (int64_t(1) << 40) / base.row_blocks) {
       sv::C4BehindArgs A;
@@ -137,7 +158,6 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
       A.prefix = view(prefix);
       A.prefix_len = prefix_len;
       A.fan = each;
-      A.split = cols > kAttnWhole;
       if (workspace_bytes < shared_space(B, T, q_heads, cache.heads, d, fan).bytes()) return SPEC_ERR_WORKSPACE;
       auto st = static_cast<hipStream_t>(stream);
       (void)hipGetLastError();

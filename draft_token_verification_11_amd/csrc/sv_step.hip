@@ -122,18 +122,20 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
   A.depth_seq = depth_stride;
   // pages that a sequence can have read at most
   const int64_t pages = (int64_t(window) + T + sv::kC4Page - 2) / sv::kC4Page + 1 + (int64_t(sinks) + sv::kC4Page - 1) / sv::kC4Page;
-  A.split = std::min<int64_t>(pages, cache.table_cols) > kAttnWhole;
+  const int64_t cols = std::min<int64_t>(pages, cache.table_cols);
   auto st = static_cast<hipStream_t>(stream);
   const int32_t d = cache.head_dim;
   const int64_t rows = int64_t(T) * A.G;
   (void)hipGetLastError();
-  if (wide_pays(rows, d, int64_t(B) * cache.heads, std::min<int64_t>(pages, cache.table_cols))) {
+  if (wide_pays(rows, d, int64_t(B) * cache.heads, cols)) {
     int32_t block_rows;
     int64_t blocks;
     wide_blocks(rows, d, &block_rows, &blocks);
     A.row_blocks = int32_t(blocks);
+    A.split = !each_pays(int64_t(B) * cache.heads * blocks, cols);
     with_wide(d, [&](auto D) { launch_wide<D>(A, block_rows, workspace, st); });
   } else {
+    A.split = !each_pays(int64_t(B) * cache.heads * A.row_blocks, cols);
     with_shape(d, tiles, [&](auto D, auto RT) { launch_attention<D, RT>(A, workspace, st); });
   }
   return finish_launch();

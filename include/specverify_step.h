@@ -131,7 +131,7 @@ int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_tabl
  * page is taken, lies outside 0 .. free_capacity, nothing is changed.
  * B at most 65536.
  * workspace: spec_cache4_reserve_workspace bytes, 256-byte aligned; where that
- * is 0 (B at most 1024) there need be none. */
+ * is 0 (B at most 128) there need be none. */
 size_t spec_cache4_reserve_workspace(int32_t B);
 int spec_cache4_reserve(int32_t* table, int64_t table_stride, int32_t table_cols, int32_t* held,
                         const int32_t* need, int32_t B, int32_t* free_pages,

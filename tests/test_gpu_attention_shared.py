@@ -185,12 +185,14 @@ def test_many_rows_and_long_prefixes(D, B, fan, T, Hq, H, prefix):
     assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
 
 
-# Shapes whose pages the waves of a workgroup share: heads of 128 with more than 96 rows and 512
-# (prefix, kv head) pairs, heads of 256 with more than 64 rows and wide tables.  (B, fan, T, Hq, H, D,
-# slack of the tables: wide ones are cut, and whole ones not)
-SHARED = [(104, 13, 2, 256, 64, 128, 0), (103, 13, 2, 256, 64, 128, 21), (40, 5, 9, 256, 64, 128, 21),
-          (70, 7, 5, 192, 64, 128, 0), (12, 6, 9, 14, 2, 256, 400), (7, 7, 3, 8, 2, 256, 2200), (9, 3, 22, 8, 8, 256, 200),
-          (24, 2, 17, 128, 64, 256, 5)]
+# Shapes whose prefixes are shared, in blocks of rows or, heads of 128 with more than 96 rows and
+# 512 (prefix, kv head) pairs and heads of 256 with more than 64 rows and wide tables, by the waves of
+# a workgroup; the first one by each branch, 6,656 segments of few pages.  (B, fan, T, Hq, H, D, slack
+# of the tables: wide ones are cut, and those of up to 20 columns not)
+SHARED = [(104, 13, 2, 256, 64, 128, 0), (104, 13, 2, 256, 64, 128, 17), (103, 13, 2, 256, 64, 128, 21),
+          (40, 5, 9, 256, 64, 128, 70), (70, 7, 5, 192, 64, 128, 40), (12, 6, 9, 14, 2, 256, 400), (7, 7, 3, 8, 2, 256, 2200),
+          (9, 3, 22, 8, 8, 256, 200), (24, 2, 17, 128, 64, 256, 40), (48, 12, 3, 128, 64, 256, 17),
+          (32, 16, 4, 128, 64, 64, 17), (40, 10, 2, 256, 64, 128, 17), (32, 8, 1, 128, 64, 256, 17)]
 
 
 @pytest.mark.parametrize("B,fan,T,Hq,H,D,slack", SHARED)
@@ -206,7 +208,8 @@ def test_shared_pages(B, fan, T, Hq, H, D, slack):
     assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
 
 
-@pytest.mark.parametrize("B,fan,T,Hq,H,D,slack", [(12, 6, 9, 14, 2, 256, 400), (18, 6, 9, 14, 2, 128, 21)])
+@pytest.mark.parametrize("B,fan,T,Hq,H,D,slack", [(12, 6, 9, 14, 2, 256, 400), (18, 6, 9, 14, 2, 128, 400),
+                                                    (12, 6, 9, 14, 2, 128, 2)])
 def test_shared_pages_of_live_rows(B, fan, T, Hq, H, D, slack):
     """Fewer new tokens than columns: rows of one tile up to all, none at all, and counts that fit no
     call, whose sequences are NaN and whose neighbours are not."""
@@ -224,7 +227,7 @@ def test_counts_around_64_branches(fan, D):
     """Live rows are counted through up to 64 branches; above that all rows have their place."""
     B, T, start, prefix = 2 * fan - 3, 3, [7] * (2 * fan - 3), [200, 66]
     counts = [(b * 7) % 4 for b in range(B)]
-    q, pages, table, ptable = _case(13, B, fan, T, 4, 1, D, start, prefix, slack=21)
+    q, pages, table, ptable = _case(13, B, fan, T, 4, 1, D, start, prefix, slack=600)
     got = _run(q, pages, table, start, ptable, prefix, fan, counts)
     _check(q, pages, table, start, ptable, prefix, fan, got, counts, rows=lambda b, i, h: (b + i + h) % 5 == 0)
 
@@ -235,7 +238,7 @@ def test_shared_pages_bad_ones_and_noise(case):
     B, fan, T, Hq, H, D = case
     n = -(-B // fan)
     prefix, start = ([70, 1 << 20, 130, 70] + [70] * n)[:n], [5] * B
-    q, pages, table, ptable = _case(14, B, fan, T, Hq, H, D, start, [130] * n, 400 if D == 256 else 0)
+    q, pages, table, ptable = _case(14, B, fan, T, Hq, H, D, start, [130] * n, 400 if D == 256 else 17)
     ptable[2, 1] = -3
     raw = pages.cpu().numpy()
     for x in range(70, 128):
@@ -255,7 +258,7 @@ def test_shared_pages_bad_ones_and_noise(case):
     _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: (b + i + h) % 53 == 0)
 
 
-@pytest.mark.parametrize("case", [(104, 13, 2, 256, 64, 128, 0), (24, 6, 9, 14, 2, 256, 400)])
+@pytest.mark.parametrize("case", [(104, 13, 2, 256, 64, 128, 0), (104, 13, 2, 256, 64, 128, 17), (24, 6, 9, 14, 2, 256, 400)])
 def test_shared_pages_and_rows_of_any_magnitude(case):
     """Rows whose scores pass 2^24 or F32's range beside ordinary ones in one tile."""
     B, fan, T, Hq, H, D, slack = case
@@ -268,6 +271,25 @@ def test_shared_pages_and_rows_of_any_magnitude(case):
     _check(q, pages, table, start, ptable, prefix, fan, got, rows=lambda b, i, h: usual[b, h] and (b * 7 + i * 5 + h) % 61 == 0)
     far = (size[:, 0, :, 0] == 1e8)[:, None].expand(B, T, Hq)
     assert torch.isfinite(got[0][far]).all() and (got[0][far].abs() <= 8).all()
+
+
+# Branches with so many (branch, kv head, block of rows) that a wave has one by itself, for few pages
+# and for more, or a workgroup, behind short prefixes (wide: 0) and behind shared ones; 1 to 4 tiles.
+@pytest.mark.parametrize("wide", [0, 100])
+@pytest.mark.parametrize("B,fan,T,Hq,H,D,slack", [
+    (33, 4, 1, 32, 32, 64, 0), (40, 3, 5, 160, 32, 64, 0), (66, 5, 10, 128, 32, 64, 25), (33, 2, 15, 128, 32, 64, 3),
+    (33, 4, 1, 64, 32, 128, 0), (33, 4, 7, 96, 32, 128, 5), (66, 4, 10, 128, 32, 128, 20), (20, 2, 2, 16, 16, 128, 30),
+    (33, 3, 2, 32, 32, 256, 0), (24, 4, 5, 128, 32, 256, 25), (12, 3, 3, 32, 16, 256, 45)])
+def test_many_segments(B, fan, T, Hq, H, D, slack, wide):
+    n = -(-B // fan)
+    start = [(b * 29) % 120 for b in range(B)]
+    prefix = [(0, 1, 64, 65, 97, 127, 128)[(g * 5 + 3) % 7] for g in range(n)]
+    count = [(b * 3 + 1) % (T + 1) for b in range(B)]
+    q, pages, table, ptable = _case(18, B, fan, T, Hq, H, D, start, prefix, slack, wide)
+    table[3, 0] = -1
+    for counts in (None, count):
+        got = _run(q, pages, table, start, ptable, prefix, fan, counts)
+        _check(q, pages, table, start, ptable, prefix, fan, got, counts, rows=lambda b, i, h: (b * 7 + i * 5 + h) % 83 == 0)
 
 
 def test_captured_with_shared_pages():

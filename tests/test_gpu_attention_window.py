@@ -135,6 +135,19 @@ def test_shared_pages(B, T, Hq, H, D, window, sinks):
                 assert abs(lse[b, i, h] - want[1]) <= want[3], (b, i, h)
 
 
+@pytest.mark.parametrize("B,T,Hq,H,D", [(4, 3, 48, 48, 64), (4, 12, 96, 48, 128), (4, 2, 48, 48, 256)])
+def test_windows_of_many_pages_not_cut(B, T, Hq, H, D):
+    """Four times as many segments as pages, more than 20 of those."""
+    start, window, sinks = [1700, 0, 900, 2300], 1500, 70
+    count = [T, T, 0, max(1, T - 1)]
+    q, pages, table = _case(19, B, T, Hq, H, D, start)
+    table = _forget(table, start, T, window, sinks)
+    got = _run(q, pages, table, start, count, window=window, sinks=sinks)
+    some = [0, 1, 2, Hq - 1]  # query heads that are looked at, each with its kv head
+    _check(q[:, :, some].contiguous(), pages[:, [h // (Hq // H) for h in some]].contiguous(), table, start, count, window,
+           sinks, tuple(x[:, :, some] for x in got))
+
+
 def test_rows_that_see_nothing():
     T, start = 3, [200, 0]
     q, pages, table = _case(4, 2, T, 2, 1, 128, start)

@@ -41,7 +41,8 @@ class State:
         assert (self.wide[:, self.table.shape[1]:] == 55).all()
 
 
-@pytest.mark.parametrize("B,cols,n", [(1, 1, 1), (1, 40, 64), (3, 5, 9), (64, 30, 700), (65, 9, 300), (1024, 4, 2500),
+@pytest.mark.parametrize("B,cols,n", [(1, 1, 1), (1, 40, 64), (3, 5, 9), (64, 30, 700), (65, 9, 300), (128, 12, 900),
+                                      (129, 12, 900), (1024, 4, 2500),
                                       (1025, 3, 3500), (3000, 3, 5000), (17, 400, 3000)])
 def test_random_steps(B, cols, n):
     """Growing, shrinking and ending, with enough pages and with too few."""

@@ -148,11 +148,11 @@ def test_pages_refusals():
     for name in ("table", "held", "need", "free", "count"):
         assert reserve(**{name: None}) == BAD and reserve(**{name: ODD}) == BAD
     assert reserve(stride=3) == BAD and reserve(cols=0) == BAD and reserve(B=0) == BAD and reserve(cap=0) == BAD
-    for B in (1025, 5000, 65536):
+    for B in (129, 5000, 65536):
         need = L.spec_cache4_reserve_workspace(B)
         assert need > 8 * B and reserve(B=B, wb=need - 1) == WS
         assert reserve(B=B, w=None) == WS and reserve(B=B, w=ctypes.c_void_p(4096 + 16)) == WS
-    assert [L.spec_cache4_reserve_workspace(B) for B in (1, 1024, 0, -1, 65537)] == [0] * 5
+    assert [L.spec_cache4_reserve_workspace(B) for B in (1, 128, 0, -1, 65537)] == [0] * 5
     assert reserve(B=65537) == UNSUP and reserve(cols=(1 << 24) + 1, stride=1 << 25) == UNSUP
 
     def slots(table=P, stride=4, cols=4, n=8, B=2, T=3, start=P, count=None, out=P):
