@@ -339,6 +339,11 @@ struct C4AttnArgs {
 // (sinks).  Of a sequence's pages those that no new token sees are left out: the
 // pages that are read are counted through, and from `keep` on they stand `skip`
 // further back in the table.
+// 64 x 6 tokens through 1,024, 8 heads of 128: 28.5 us, 83 MB fetched, a workgroup a
+// segment of 17 or 18 pages (41.6 where workgroups take what begins in their shares, of
+// which some then have two and some none).  Trees of 21 nodes through 4,001, 16 x 8
+// heads: 77 us, 221 MB by four blocks of rows, vector instructions in 54 % of the busy
+// cycles; cut 77 and a join of 13.
 struct C4WindowArgs : C4AttnArgs {
   int32_t window, sinks;
   const int32_t* depth;  // or null: a new token's index
@@ -351,6 +356,9 @@ struct C4WindowArgs : C4AttnArgs {
 // `compact` (of 64 branches at most) of their live tokens only, so that branches
 // with few new tokens make fewer blocks.  Each row of the call has a record: O [D],
 // and maximum, sum and rounded sum.
+// 64 prefixes of 1,500 to 4,091 tokens, up to 40 live tokens of eight branches each, 8
+// heads of 128: 150 us and the join 16, 480 MB fetched, vector instructions in 57 % of the
+// busy cycles, matrix units in 27 %.
 struct C4PrefixArgs : C4AttnArgs {
   int32_t fan, seqs;   // branches of a prefix, sequences of the call
   int32_t dim;         // D

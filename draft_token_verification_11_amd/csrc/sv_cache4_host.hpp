@@ -208,13 +208,14 @@ void wide_blocks(int64_t rows, int32_t d, int32_t* block_rows, int64_t* blocks) 
 //   heads of 64   hardly: 192 rows, 16 heads over 16,384 tokens 51 and 64; 168 rows,
 //                 32 x 8 heads through a window of 4,000 121 and 110, the best
 //   heads of 128  where there is a sequence and head for each workgroup, so that few
-//                 are cut: 64 x 8 heads over 2,048, 64 rows 77 and 81, 160 rows 175
-//                 and 162, 256 rows 269 and 238; through a window of 1,000, 168
-//                 rows 93 and 73; not 8 x 8 heads over 16,384, 160 rows 155 and 195
+//                 are cut: behind shared prefixes 64 x 8 heads over 2,048, 64 rows 77
+//                 and 81, 160 rows 175 and 162, 256 rows 269 and 238; 168 rows through
+//                 windows 64 x 8 of 1,000 104 and 82, of 4,000 276 and 231, 32 x 8 of
+//                 2,000 84 and 98, 16 x 8 of 1,000 31 and 59
 //   heads of 256  where its workgroups have some pages each, for they are half as
-//                 many: 16 x 4 heads through a window of 4,000, 168 rows 123 and 98;
-//                 4 x 4 heads, 378 rows, over 8,192 105 and 97, over 2,048 52 and 65;
-//                 40 rows, 8 x 4 heads, window of 8,000 45 and 48
+//                 many: 168 rows through windows 16 x 4 heads of 4,000 101 and 92, 64 x
+//                 4 of 1,000 117 and 95, 8 x 4 of 1,000 25 and 45; 4 x 4 heads, 378
+//                 rows, over 8,192 105 and 97, over 2,048 52 and 65
 bool wide_rows(int64_t rows, int32_t d) { return d == 128 ? rows > 96 : d == 256 && rows > 64; }
 bool wide_pays(int64_t rows, int32_t d, int64_t seqs_heads, int64_t pages) {
   if (!wide_rows(rows, d)) return false;

@@ -14,6 +14,12 @@ namespace sv {
 // of 16 rows each and go through the same pages together: each converts its part
 // of a page's codes to bf16 and puts them into LDS, as the operands that every
 // wave then reads, while the page before is attended to.
+// 4 prefixes of up to 8,155 tokens, 378 rows on each of 4 heads of 256: 55 us, matrix
+// units 25 % and vector instructions 34 % of the busy cycles, 78 MB fetched; a page
+// takes its workgroup about 3 us, the ends of a segment 17.  What bounds it is the
+// barrier after each page, behind which converting, scores, exponentials and the
+// second product follow each other; scores of the next page begun before it gained
+// nothing.
 template <int D>
 struct C4Wide {
   static_assert(D == 128 || D == 256, "heads of 64 gain nothing by it");

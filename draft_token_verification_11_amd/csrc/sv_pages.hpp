@@ -72,6 +72,9 @@ __device__ __forceinline__ void res_move(const ReserveArgs& A, const ReservePlan
 
 constexpr int kResThreads = 1024;
 
+// Integers only.  Bound by loads that wait for each other and by launches: lengths,
+// sums, a search, a page (64 sequences 5.7 us; 4,093 7.6 for the sums and 7.9 for
+// 24,000 pages, their 1,000 slots each 8.2, 33 MB at 4 TB/s).
 // The sums, by one workgroup, a run of `per` sequences a thread: into give_upto
 // and take_upto, with the lengths after the call in held (which may be A.held).
 // False where nothing may change.  Sums of what is taken past what there is

@@ -73,6 +73,14 @@ __device__ __forceinline__ float rot_max(float x) {
   return x;
 }
 
+// y = x / sqrt(mean x^2 + eps) w for each head, then pairs (a, b) of its first `rot`
+// values become (a cos t - b sin t, b cos t + a sin t), t = (start + depth) inv_freq.
+// All of it is F32, but for the angle: a product of 2^30 and a frequency needs more
+// bits than F32 has, so that it is taken in 64 bits and brought into one turn there.
+// The one rounding to fewer bits is that of a BF16 output.
+// Bound by memory for prompts (4 x 8,191 tokens of 32 + 8 heads of 128, BF16: 671 MB
+// in 141 us, 4.7 TB/s, where a copy reaches 5.1), by its launch and one chain of
+// loads for a step (64 x 6 tokens 6.8 us, one token 4.0).
 // A thread holds 8 neighbouring values of a head, LANES of them a head (those past
 // D / 8 none), a wave 64 / LANES heads of one token, whose angles it makes
 // once for all the heads that it goes through, queries first.

@@ -46,7 +46,9 @@ PrefixShape prefix_shape(int64_t rows, int32_t d, int64_t prefixes_heads, int64_
 bool short_pays(int64_t segments, int64_t cols) {
   return (segments >= 2048 && cols <= 32) || (segments >= 1024 && cols <= 8);
 }
-// Branches up to which their live rows are counted through: one a lane.
+// Branches up to which their live rows are counted through: one a lane.  (64 x 8 branches
+// of up to 5 tokens, on average 3: 180 us, 242 with all rows; all of them live: 256 and
+// 257; 8 x 48 of up to 3: 98 and 111.)
 constexpr int32_t kCompactFan = 64;
 
 // What a page costs a block of rows, in those of a block of one tile: more tiles share

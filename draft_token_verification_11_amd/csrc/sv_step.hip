@@ -14,12 +14,18 @@
 namespace {
 
 // Waves that a small rotation is cut into: as many as the compute units hold at once.
+// 128 x 16 tokens of 32 + 8 heads of 128 take 15.1 us with it, 18.3 with 2,048 and
+// 20.5 with 32,768, for each of which the angles are made again; 16 x 256 tokens 20.1,
+// 22.1, 24.4; 64 x 6 6.8, 6.2, 6.7; one token 4.4 with any.
 constexpr int64_t kRotateWaves = 8192;
 
-// Workgroups that move the pages of a call of many sequences.
+// Workgroups that move the pages of a call of many sequences (4,093 sequences there and
+// back with slots 40.1 us, with 256 43.9, with 4,096 40.1).
 constexpr int64_t kReserveBlocks = 1024;
 
-// New tokens from which on a workgroup has those of one sequence only.
+// New tokens from which on a workgroup has those of one sequence only (4,093 x 1,000 in
+// such a call 40.1 us, by tokens 43.2; 512 x 400 32.2 both; 4,093 x 16 32.4 by
+// sequences, 31.4 by tokens).
 constexpr int32_t kSlotsLong = 256;
 
 // One side of a rotation; a side without heads is not looked at.
