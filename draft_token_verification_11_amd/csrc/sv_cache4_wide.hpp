@@ -30,6 +30,10 @@ struct C4Wide {
   static constexpr int kGrid = 256 * kPerCu;
   static constexpr int kKeys = 64 * D * 2;                         // bytes of a page's keys, or values, in bf16
   static constexpr int kCost = 8;   // pages that a segment's ends cost
+  // What a pair of waves with the same rows hands over: float4s of O, floats of m, l, n.
+  static constexpr int kHandO = RT * (D / 16) * 64, kHandStats = 3 * RT * 64;
+  static constexpr int kStats = kWaves / 2 * kHandStats;
+  static_assert(kWaves / 2 * kHandO * 16 <= 4 * kKeys, "in two pages' buffers");
   // A cut segment: O [kRows][D], m, l, n [kRows], and what the rows are.
   static constexpr int64_t kFloats = kRows * (D + 5);
 };
@@ -45,15 +49,28 @@ struct C4Share {
 // Neighbouring tiles to a wave; where half the waves hold them all, two waves
 // have the same.
 template <int D>
-__device__ __forceinline__ C4Share c4_wave_share(int32_t rows, int w) {
+__host__ __device__ __forceinline__ C4Share c4_wave_share(int32_t rows, int w) {
   using Sh = C4Wide<D>;
   C4Share x;
   x.tiles = (rows + 15) / 16;
   x.half = x.tiles <= Sh::kTiles / 2;
   const int W = x.half ? Sh::kWaves / 2 : Sh::kWaves, v = x.half ? w >> 1 : w;
-  x.mine = x.tiles / W + (v < x.tiles % W);
-  x.row0 = 16 * (x.tiles / W * v + min(v, x.tiles % W));
+  const int more = x.tiles % W;  // waves that have a tile more
+  x.mine = x.tiles / W + (v < more);
+  x.row0 = 16 * (x.tiles / W * v + (v < more ? v : more));
   return x;
+}
+// Where wave w's pair of waves with the same rows hands them over: its float4s of O
+// in the pages' buffers, and its floats of m, l and n.  Each pair has room for as many
+// tiles as one can have, however many it has: of a block of 3 or 5 tiles one pair has
+// one more than the other.
+struct C4HandOver {
+  int32_t o, stats;
+};
+template <int D>
+__host__ __device__ constexpr C4HandOver c4_hand_over(int w) {
+  using Sh = C4Wide<D>;
+  return {(w >> 1) * Sh::kHandO, (w >> 1) * Sh::kHandStats};
 }
 // Finds a wave's rows in the block of `rows` rows whose first one is r0, and puts
 // down what they are.
@@ -368,8 +385,9 @@ __device__ __forceinline__ void c4_wide_run(const Args& A, C4Segment G, uint8_t 
     c4_barrier();
   }
   if constexpr (HALF) {  // the two waves of the same rows: the second's go to the first
-    float4* const o = reinterpret_cast<float4*>(pagebuf) + (w >> 1) * (NT * (D / 16) * 64) + lane;
-    float* const st = stats + (w >> 1) * (3 * RT * 64) + lane;
+    const C4HandOver to = c4_hand_over<D>(w);
+    float4* const o = reinterpret_cast<float4*>(pagebuf) + to.o + lane;
+    float* const st = stats + to.stats + lane;
     if (w & 1) {
 #pragma unroll
       for (int rt = 0; rt < NT; ++rt) {
@@ -436,7 +454,7 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
   using Sh = C4Wide<D>;
   __shared__ __attribute__((aligned(16))) uint8_t pagebuf[2][2][Sh::kKeys];
   __shared__ C4RowMap maps[Sh::kWaves][16 * Sh::RT];
-  __shared__ float stats[Sh::kWaves / 2 * 3 * Sh::RT * 64];
+  __shared__ float stats[Sh::kStats];
 
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int32_t per = (A.B + 63) / 64;
