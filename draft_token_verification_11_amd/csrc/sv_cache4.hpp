@@ -478,6 +478,17 @@ __device__ __forceinline__ int32_t c4_pages(const Args& A, int64_t b, bool& bad)
   return all;
 }
 
+// New tokens of sequence b, whose pages c4_pages has counted: T where it is
+// ill-formed, for then all of its rows are NaN; behind an ill-formed prefix its own.
+template <typename Args>
+__device__ __forceinline__ int32_t c4_new(const Args& A, int64_t b, bool bad) {
+  if constexpr (kC4Prefix<Args>) return 0;  // a prefix has none of its own
+  if (!A.count) return A.T;
+  const int32_t n = c4_scalar(A.count + b);
+  if constexpr (kC4Behind<Args>) return bad && !A.cache.fits(c4_scalar(A.start + b), n, A.T) ? A.T : n;
+  return bad ? A.T : n;
+}
+
 // Beginning and ending a segment (its rows, the first loads, joining the four
 // waves) costs a workgroup as much time as about this many pages; without it
 // in the shares a batch with short sequences waits for the workgroups that
@@ -1194,8 +1205,7 @@ __global__ __launch_bounds__(256, (C4Shape<D, RT>::kWaves)) void k_attention_cac
     if (p0 == p1) continue;  // its pages are another workgroup's
     const int32_t h = hr / nb, r0 = hr % nb * kRows;
     const int32_t s0 = c4_scalar(A.start + b);
-    // a prefix has no new tokens of its own
-    const int32_t nnew = kC4Prefix<Args> ? 0 : bad || !A.count ? A.T : c4_scalar(A.count + b);
+    const int32_t nnew = c4_new(A, b, bad);
     C4Gap gap{0, 0};
     if constexpr (kC4Window<Args>)
       if (!bad) gap = c4_gap(A.window, A.sinks, s0, nnew);
@@ -1487,7 +1497,7 @@ __global__ __launch_bounds__(256) void k_attention_cache4_join_long(Args A) {
     at += kC4Prefix<Args> ? one * c4_blocks<true>(A, x) : one;
   }
   const int32_t pages = c4_pages<true>(A, b, bad);
-  const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
+  const int32_t nnew = c4_new(A, b, bad);
   int64_t bb = b;
   int32_t i, head;
   const int32_t upto = c4_rows_upto(A, b, lane), nb = c4_blocks<true>(A, b);

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(256, 2) void k_attention_cache4_short(Args A) {
   const int32_t pages = c4_pages<true>(A, b, bad);
   if (pages == 0) return;
   const int32_t s0 = c4_scalar(A.start + b);
-  const int32_t nnew = bad || !A.count ? A.T : c4_scalar(A.count + b);
+  const int32_t nnew = c4_new(A, b, bad);
   bool faulty = bad;
   const int32_t ps = kC4Behind<Args> && !bad ? c4_behind<true>(A, b) : 0, np = c4_pages_of(ps);
   // pairs of tiles; the last page may hold no token in its second half

@@ -499,7 +499,7 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
     G.h = hr / nb;
     G.r0 = hr % nb * block_rows;
     G.s0 = c4_scalar(A.start + G.b);
-    G.nnew = kC4Prefix<Args> ? 0 : bad || !A.count ? A.T : c4_scalar(A.count + G.b);
+    G.nnew = c4_new(A, G.b, bad);
     G.gap = C4Gap{0, 0};
     if constexpr (kC4Window<Args>)
       if (!bad) G.gap = c4_gap(A.window, A.sinks, G.s0, G.nnew);

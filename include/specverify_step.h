@@ -92,9 +92,9 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
  * spec_attention_cache4 says.  The prefix's pages are read and converted once for
  * the rows of all its branches, up to a block's rows.
  *   prefix_table  [ceil(B / fan)][prefix_cols], row g at + g * prefix_stride
- *   prefix_len    [ceil(B / fan)], 0 .. 64 prefix_cols; every row of a prefix
- *                 whose length lies outside, or that has a page outside the
- *                 pool, becomes NaN
+ *   prefix_len    [ceil(B / fan)], 0 .. 64 prefix_cols; the rows i < count[b] of
+ *                 branches whose prefix has a length outside, or a page outside
+ *                 the pool, become NaN
  *   fan >= 1; min(fan, B) T q_heads at most 2^30
  * For all else spec_attention_cache4's words hold.
  * workspace: spec_attention_cache4_shared_workspace bytes, 256-byte aligned. */
