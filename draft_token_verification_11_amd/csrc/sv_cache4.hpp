@@ -386,7 +386,6 @@ struct C4BehindArgs : C4AttnArgs {
 template <typename Args> constexpr bool kC4Behind = std::is_same<Args, C4BehindArgs>::value;
 template <typename Args> constexpr bool kC4Window = std::is_same<Args, C4WindowArgs>::value;
 template <typename Args> constexpr bool kC4Prefix = std::is_same<Args, C4PrefixArgs>::value;
-template <typename Args> constexpr bool kC4Own = std::is_same<Args, C4OwnArgs>::value;
 template <typename Args> constexpr bool kC4Each = !std::is_same<Args, C4AttnArgs>::value && !kC4Prefix<Args>;
 
 struct C4Cut {

@@ -30,6 +30,9 @@ struct C4Wide {
   static constexpr int kGrid = 256 * kPerCu;
   static constexpr int kKeys = 64 * D * 2;                         // bytes of a page's keys, or values, in bf16
   static constexpr int kCost = 8;   // pages that a segment's ends cost
+  // Whether calls whose live rows are counted through come here: of heads of 128 they
+  // gain nothing (64 x 8 heads, 96 of 160 rows live: 185 us by k_attention_cache4, 190).
+  static constexpr bool kCounted = D == 256;
   // What a pair of waves with the same rows hands over: float4s of O, floats of m, l, n.
   static constexpr int kHandO = RT * (D / 16) * 64, kHandStats = 3 * RT * 64;
   static constexpr int kStats = kWaves / 2 * kHandStats;
@@ -456,6 +459,7 @@ __global__ __launch_bounds__(64 * C4Wide<D>::kWaves, C4Wide<D>::kPerCu) void k_a
   __shared__ C4RowMap maps[Sh::kWaves][16 * Sh::RT];
   __shared__ float stats[Sh::kStats];
 
+  if constexpr (kC4Prefix<Args> && !Sh::kCounted) A.compact = 0;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int32_t per = (A.B + 63) / 64;
   const int32_t HR = c4_times(A);

@@ -26,10 +26,9 @@ struct PrefixShape {
 };
 PrefixShape prefix_shape(int64_t rows, int32_t d, int64_t prefixes_heads, int64_t cols, bool compact) {
   PrefixShape x{};
-  // `rows` are far more than the live ones where those are counted through; heads of
-  // 128 then gain nothing by wide blocks (64 x 8 heads, 96 of 160 rows live: 185 us
-  // and 190)
-  x.wide = wide_pays(rows, d, prefixes_heads, cols) && !(compact && d == 128);
+  // `rows` are far more than the live ones where those are counted through
+  x.wide = wide_pays(rows, d, prefixes_heads, cols);
+  if (x.wide && compact) with_wide(d, [&](auto D) { x.wide = sv::C4Wide<D>::kCounted; });
   if (x.wide) wide_blocks(rows, d, &x.block_rows, &x.blocks);
   else row_blocks(rows, d, &x.tiles, &x.blocks);
   return x;
