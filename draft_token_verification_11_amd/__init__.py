@@ -1155,8 +1155,10 @@ def attention_cache4_shared(q: torch.Tensor, pages: torch.Tensor, table: torch.T
     """attention_cache4 of branches behind shared prefixes: sequences fan g ..
     fan g + fan - 1 see, before their own tokens (table, start, count, mask as
     there), the prefix_len[g] tokens whose pages prefix_table [ceil(B / fan)][.]
-    names in the same pool.  A prefix is read once for all its branches.  A new
-    token's position in the text, for norm_rotate, is prefix_len + start + i."""
+    names in the same pool.  By the sizes and the tables' widths a prefix is read
+    for many rows of its branches at once or, where that costs less, by each branch
+    (a prefix_table no wider than need be serves best).  A new token's position in
+    the text, for norm_rotate, is prefix_len + start + i."""
     index = _device_tensor(q, "q", (torch.bfloat16,), 4)
     B, T, Hq, D = q.shape
     cache, _ = _cache4(pages, table, D, B, index)

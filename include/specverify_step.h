@@ -89,15 +89,21 @@ int spec_attention_cache4_window(spec_cache4_t cache, spec_heads_t q, int32_t B,
  * fan - 1 (those below B) are branches of prefix g, whose prefix_len[g] tokens
  * stand in pages prefix_table[g][0 ..] of the same pool.  A new token sees its
  * whole prefix, and of its own sequence (start, count, mask, cache.table) what
- * spec_attention_cache4 says.  The prefix's pages are read and converted once for
- * the rows of all its branches, up to a block's rows.
+ * spec_attention_cache4 says.  Either a prefix's pages are read and converted once
+ * for each block of the rows of all its branches, or each branch reads them before
+ * its own, where that costs less (short prefixes, few branches): the sizes and the
+ * tables' widths decide, not prefix_len, so that tables serve best that are no
+ * wider than need be.  The results of both differ by roundings within the bounds
+ * of spec_attention_cache4.
  *   prefix_table  [ceil(B / fan)][prefix_cols], row g at + g * prefix_stride
  *   prefix_len    [ceil(B / fan)], 0 .. 64 prefix_cols; the rows i < count[b] of
  *                 branches whose prefix has a length outside, or a page outside
  *                 the pool, become NaN
  *   fan >= 1; min(fan, B) T q_heads at most 2^30
  * For all else spec_attention_cache4's words hold.
- * workspace: spec_attention_cache4_shared_workspace bytes, 256-byte aligned. */
+ * workspace: spec_attention_cache4_shared_workspace bytes, 256-byte aligned: by
+ * these sizes alone, with room for a record of each row (4 head_dim + 16 bytes)
+ * also where branches read their prefix themselves. */
 size_t spec_attention_cache4_shared_workspace(int32_t B, int32_t T, int32_t q_heads, int32_t heads,
                                               int32_t head_dim, int32_t fan);
 int spec_attention_cache4_shared(spec_cache4_t cache, const int32_t* prefix_table,
